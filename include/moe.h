@@ -376,6 +376,149 @@ moe_status moe_layer_backward_timed(const moe_config* cfg, const void* x,
 moe_status moe_update_select_bias(int32_t N, const int32_t* counts, float rate,
                                   float* select_bias, void* stream);
 
+/* ------------------------------------------------ experts of one's own
+ *
+ * The parts of the layer as calls of their own, for experts other than the
+ * layer's (another activation, biases, a residual, activations kept between
+ * forward and backward):
+ *
+ *   moe_route            x -> topk_idx, topk_gate
+ *   moe_group_rows       topk_idx -> offsets, row_token, slot_row
+ *   moe_grouped_linear   rows by expert, any number of times
+ *   moe_combine          rows -> tokens
+ *
+ * and backwards moe_combine_backward, moe_grouped_linear_backward, and
+ * moe_combine without gates for the rows read through row_token.  The
+ * conventions at the top of this file hold; the calls are deterministic.
+ *
+ * Grouping.  topk_idx [T, k] (moe_route's, or any int32 indices) to
+ *   offsets   [N + 1]  expert e owns rows offsets[e] .. offsets[e + 1] - 1
+ *   row_token [T k]    token of every row (entries at or past offsets[N]
+ *                      are left as they were)
+ *   slot_row  [T, k]   row of every (token, slot), -1 for one without a row
+ * The rows of an expert are in the flat order of their (token, slot) pairs.
+ * capacity: 0, or the most pairs an expert keeps, its first ones (as in
+ * moe_config).  A pair whose index lies outside [0, N) gets no row: -1 marks
+ * the slots of padding.  1 <= N <= 512, k <= 16, T k < 2^30; T = 0 writes
+ * offsets only.  workspace: moe_group_workspace_size(T, N, k) bytes, 256-byte
+ * aligned (the size is 0 for sizes outside these). */
+size_t moe_group_workspace_size(int32_t T, int32_t N, int32_t k);
+moe_status moe_group_rows(int32_t T, int32_t N, int32_t k, int32_t capacity,
+                          const int32_t* topk_idx, int32_t* offsets, int32_t* row_token,
+                          int32_t* slot_row, void* workspace, size_t ws_bytes, void* stream);
+
+/* Activations of moe_grouped_linear.  GELU is z Phi(z) with the normal
+ * distribution's CDF; SWIGLU is SiLU(z[:out]) * z[out:], the weights of a
+ * group being the gate's rows and then the up projection's. */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,
+  MOE_ACT_SILU = 3,
+  MOE_ACT_SWIGLU = 4
+} moe_activation;
+
+/* A linear map for each of `groups` groups of rows.  z_dim = out_dim, or
+ * 2 out_dim with MOE_ACT_SWIGLU, is the number of rows of a group's weights.
+ * One group is an ordinary dense product.  groups <= 512, in_dim and out_dim
+ * multiples of 64 up to 2^20, rows < 2^30; MOE_WEIGHTS_FP8_E4M3 needs
+ * MOE_BF16. */
+typedef struct {
+  int32_t rows;          /* rows of y (and of residual, dy, dx, the checkpoint)       */
+  int32_t x_rows;        /* rows of x when row_index is given; 0: x has `rows` rows   */
+  int32_t groups;
+  int32_t in_dim;
+  int32_t out_dim;
+  int32_t dtype;         /* a moe_dtype                                               */
+  int32_t weight_format; /* a moe_weight_format                                       */
+  int32_t activation;    /* a moe_activation                                          */
+} moe_linear_config;
+
+/* z[r] = x[src(r)] W_e^T + bias[e],  y[r] = act(z[r]) + residual[r]
+ * for the rows r of every group e, src(r) = row_index[r] (clamped to x's
+ * rows) or r.  Rows at or past offsets[groups] are left as they were.
+ *
+ * offsets is read on the device; values outside [0, rows], or decreasing,
+ * are clamped.  y may be residual.  With z_codes and z_scale the call also
+ * writes the 8-bit checkpoint of z (below), which the backward of an
+ * activation reads.  z is held in fp32 until it is rounded to y or coded. */
+typedef struct {
+  const void* x;            /* [x_rows or rows, in_dim]                               */
+  const int32_t* row_index; /* [rows], or NULL when x_rows = 0                        */
+  const int32_t* offsets;   /* [groups + 1]                                           */
+  const void* w;            /* [groups, z_dim, in_dim]                                */
+  const float* w_scale;     /* [groups, z_dim], FP8 weights only                      */
+  const float* bias;        /* [groups, z_dim] or NULL                                */
+  const void* residual;     /* [rows, out_dim] or NULL                                */
+  void* y;                  /* [rows, out_dim]                                        */
+  uint8_t* z_codes;         /* [rows, z_dim] or NULL                                  */
+  float* z_scale;           /* [rows, z_dim / 64], with z_codes                       */
+} moe_linear_args;
+
+/* Bytes of device workspace moe_grouped_linear needs (a multiple of 256);
+ * 0 for an invalid or unsupported cfg. */
+size_t moe_linear_workspace_size(const moe_linear_config* cfg);
+moe_status moe_grouped_linear(const moe_linear_config* cfg, const moe_linear_args* a,
+                              void* workspace, size_t ws_bytes, void* stream);
+
+/* Gradients of L with respect to x, W and bias, given dy = dL/dy:
+ *   dz[r]    = dy[r] act'(z[r])       z decoded from its 8-bit checkpoint
+ *   dx[r]    = dz[r] W_e              one row for every row of y: rows read
+ *                                     through row_index are summed over a
+ *                                     token's slots by moe_combine
+ *   dw[e]    = sum_r dz[r]^T x[src(r)],  dbias[e] = sum_r dz[r]
+ * (the residual's gradient is dy).  Each output is optional, one at least
+ * is required; groups without rows get zeros; rows of dx at or past
+ * offsets[groups] are left as they were.  dz is held in dtype as operand of
+ * both products, dbias sums it before that rounding.  Weights in dtype only
+ * (MOE_WEIGHTS_DTYPE). */
+typedef struct {
+  const void* x;            /* as in the forward (NULL when dw is)                    */
+  const int32_t* row_index;
+  const int32_t* offsets;
+  const void* w;            /* (NULL when dx is)                                      */
+  const void* dy;           /* [rows, out_dim]                                        */
+  const uint8_t* z_codes;   /* required unless MOE_ACT_NONE                           */
+  const float* z_scale;
+  void* dx;                 /* [rows, in_dim] or NULL                                 */
+  void* dw;                 /* [groups, z_dim, in_dim] or NULL                        */
+  float* dbias;             /* [groups, z_dim] or NULL                                */
+} moe_linear_grad_args;
+
+size_t moe_linear_backward_workspace_size(const moe_linear_config* cfg);
+moe_status moe_grouped_linear_backward(const moe_linear_config* cfg,
+                                       const moe_linear_grad_args* a, void* workspace,
+                                       size_t ws_bytes, void* stream);
+
+/* 8-bit activation checkpoints.  x [rows, cols] (dtype a moe_dtype, cols a
+ * multiple of 64) is held as one OCP E4M3 code for each element and one fp32
+ * scale for each block of 64 columns of a row:
+ *   m = max(max |x| over the block, 1e-30),  scale = m / 448,
+ *   code = E4M3(x * (448 / m)), to nearest even;  unpack: code * scale,
+ * so an element is off by at most 2^-4 of itself, or scale 2^-10 where that
+ * is more.  NaN and infinities become the NaN code and do not enter m.
+ * codes [rows, cols], scale [rows, cols / 64].  rows = 0 launches nothing. */
+moe_status moe_checkpoint_pack(int64_t rows, int32_t cols, int32_t dtype, const void* x,
+                               uint8_t* codes, float* scale, void* stream);
+moe_status moe_checkpoint_unpack(int64_t rows, int32_t cols, int32_t dtype,
+                                 const uint8_t* codes, const float* scale, void* x,
+                                 void* stream);
+
+/* y[t] = sum_s gate[t, s] rows[slot_row[t, s]] over the slots that have a row
+ * (gate NULL: 1), summed in fp32 in slot order.  rows [n_rows, d], slot_row
+ * and gate [T, k], y [T, d]; a slot_row outside [0, n_rows) is a slot without
+ * a row.  d a multiple of 64, k <= 16.  y must not overlap rows. */
+moe_status moe_combine(int32_t T, int32_t k, int32_t n_rows, int32_t d, int32_t dtype,
+                       const void* rows, const int32_t* slot_row, const float* gate, void* y,
+                       void* stream);
+/* drows[slot_row[t, s]] = gate[t, s] dy[t],  dgate[t, s] = <dy[t], rows[...]>
+ * (0 for a slot without a row).  drows and dgate are optional, one at least
+ * is required; rows may be NULL when dgate is.  Rows that no slot names are
+ * left as they were; no row may be named twice. */
+moe_status moe_combine_backward(int32_t T, int32_t k, int32_t n_rows, int32_t d, int32_t dtype,
+                                const void* rows, const int32_t* slot_row, const float* gate,
+                                const void* dy, void* drows, float* dgate, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

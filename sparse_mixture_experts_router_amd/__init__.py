@@ -24,6 +24,12 @@ __all__ = [
     "MoEGrads", "moe_backward_workspace_size", "alloc_backward_workspace", "moe_layer_backward",
     "moe_update_select_bias", "MoEPlanInfo", "moe_forward_plan", "moe_layer_forward_noalloc",
     "NOALLOC_SCRATCH_BYTES",
+    "ACTIVATIONS", "CHECKPOINT_BLOCK", "MoELinearConfig", "MoELinearArgs", "MoELinearGradArgs",
+    "make_linear_config", "moe_linear_workspace_size", "alloc_linear_workspace",
+    "moe_grouped_linear", "moe_linear_backward_workspace_size", "alloc_linear_backward_workspace",
+    "moe_grouped_linear_backward", "moe_checkpoint_pack", "moe_checkpoint_unpack",
+    "moe_group_workspace_size", "alloc_group_workspace", "moe_group_rows", "moe_combine",
+    "moe_combine_backward",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -35,6 +41,8 @@ MOE_WEIGHTS_DTYPE, MOE_WEIGHTS_FP8_E4M3 = 0, 1
 NOALLOC_SCRATCH_BYTES = 64 << 20   # MOE_NOALLOC_SCRATCH_BYTES of include/moe.h
 _SCALES = ("w_gate_scale", "w_up_scale", "w_down_scale", "ws_gate_scale", "ws_up_scale",
            "ws_down_scale")
+ACTIVATIONS = ("none", "relu", "gelu", "silu", "swiglu")   # moe_activation, in its order
+CHECKPOINT_BLOCK = 64   # columns of a row that share one scale of an 8-bit checkpoint
 STAGES = ("route", "permute", "expert_up", "expert_down", "combine")
 BACKWARD_STAGES = ("route", "transpose_w", "recompute", "grad_h", "grad_x", "segments", "grad_w",
                    "grad_wr")
@@ -89,6 +97,24 @@ class MoEGrads(ctypes.Structure):
                 ("dws_down", ctypes.c_void_p)]
 
 
+class MoELinearConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("rows", "x_rows", "groups", "in_dim", "out_dim", "dtype", "weight_format",
+                 "activation")]
+
+
+class MoELinearArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("x", "row_index", "offsets", "w", "w_scale", "bias", "residual", "y", "z_codes",
+                 "z_scale")]
+
+
+class MoELinearGradArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("x", "row_index", "offsets", "w", "dy", "z_codes", "z_scale", "dx", "dw",
+                 "dbias")]
+
+
 _LIB = None
 
 
@@ -131,6 +157,26 @@ def lib() -> ctypes.CDLL:
         L.moe_forward_plan.restype = ctypes.c_int
         L.moe_layer_forward_noalloc.argtypes = [cfgp, vp, wp, vp, rp, vp]
         L.moe_layer_forward_noalloc.restype = ctypes.c_int
+        lcfg = ctypes.POINTER(MoELinearConfig)
+        i64 = ctypes.c_int64
+        L.moe_group_workspace_size.argtypes = [i32, i32, i32]
+        L.moe_group_workspace_size.restype = sz
+        L.moe_group_rows.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_linear_workspace_size.argtypes = [lcfg]
+        L.moe_linear_workspace_size.restype = sz
+        L.moe_grouped_linear.argtypes = [lcfg, ctypes.POINTER(MoELinearArgs), vp, sz, vp]
+        L.moe_linear_backward_workspace_size.argtypes = [lcfg]
+        L.moe_linear_backward_workspace_size.restype = sz
+        L.moe_grouped_linear_backward.argtypes = [lcfg, ctypes.POINTER(MoELinearGradArgs), vp, sz,
+                                                  vp]
+        L.moe_checkpoint_pack.argtypes = [i64, i32, i32, vp, vp, vp, vp]
+        L.moe_checkpoint_unpack.argtypes = [i64, i32, i32, vp, vp, vp, vp]
+        L.moe_combine.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp]
+        L.moe_combine_backward.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+        for fn in (L.moe_group_rows, L.moe_grouped_linear, L.moe_grouped_linear_backward,
+                   L.moe_checkpoint_pack, L.moe_checkpoint_unpack, L.moe_combine,
+                   L.moe_combine_backward):
+            fn.restype = ctypes.c_int
         _LIB = L
     return _LIB
 
@@ -379,6 +425,239 @@ def moe_update_select_bias(counts: torch.Tensor, rate: float, select_bias: torch
     _check(lib().moe_update_select_bias(
         n, _ptr(counts, torch.int32, "counts"), float(rate),
         _ptr(select_bias, torch.float32, "select_bias", n), _stream(stream)))
+
+
+# ---------------------------------------------------------------- experts of one's own
+_CODE = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+
+
+def _dtype_code(t: torch.Tensor, name: str) -> int:
+    try:
+        return _CODE[t.dtype]
+    except KeyError:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected bfloat16 or float32") from None
+
+
+class _Call:
+    """Marshals the tensors of one call, all on one device, and makes it there:
+    the C ABI launches on the current device, which may be another one."""
+
+    __slots__ = ("device",)
+
+    def __init__(self, first: torch.Tensor):
+        self.device = first.device
+
+    def ptr(self, t: Optional[torch.Tensor], dtype, name: str, shape) -> Optional[int]:
+        if t is None:
+            return None
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def workspace(self, t: torch.Tensor) -> int:
+        if not t.is_cuda or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
+        return t.data_ptr()
+
+    def run(self, fn, stream, *args):
+        if not self.device.type == "cuda":
+            raise ValueError("tensors must be on a GPU")
+        if torch.cuda.current_device() == self.device.index:
+            s = torch.cuda.current_stream() if stream is None else stream
+            _check(fn(*args, s.cuda_stream))
+            return
+        with torch.cuda.device(self.device):
+            s = torch.cuda.current_stream() if stream is None else stream
+            _check(fn(*args, s.cuda_stream))
+
+
+def _nbytes(workspace: torch.Tensor) -> int:
+    return workspace.numel() * workspace.element_size()
+
+
+def moe_group_workspace_size(T: int, n_experts: int, top_k: int) -> int:
+    return int(lib().moe_group_workspace_size(int(T), int(n_experts), int(top_k)))
+
+
+def _alloc(n: int, device) -> torch.Tensor:
+    if n == 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, "configuration rejected")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def alloc_group_workspace(T: int, n_experts: int, top_k: int, device="cuda") -> torch.Tensor:
+    return _alloc(moe_group_workspace_size(T, n_experts, top_k), device)
+
+
+def moe_group_rows(topk_idx: torch.Tensor, n_experts: int, offsets: torch.Tensor,
+                   row_token: torch.Tensor, slot_row: torch.Tensor, *, workspace: torch.Tensor,
+                   capacity: int = 0, stream=None) -> None:
+    """(token, slot) pairs grouped by expert: ``offsets`` [N + 1], ``row_token``
+    [T k] and ``slot_row`` [T, k] from ``topk_idx`` [T, k] (all int32); see
+    ``moe_group_rows`` in include/moe.h."""
+    T, k = topk_idx.shape
+    c = _Call(topk_idx)
+    i32 = torch.int32
+    c.run(lib().moe_group_rows, stream, T, int(n_experts), k, int(capacity),
+          c.ptr(topk_idx, i32, "topk_idx", (T, k)),
+          c.ptr(offsets, i32, "offsets", (int(n_experts) + 1,)),
+          c.ptr(row_token, i32, "row_token", (T * k,)), c.ptr(slot_row, i32, "slot_row", (T, k)),
+          c.workspace(workspace), _nbytes(workspace))
+
+
+def make_linear_config(rows: int, groups: int, in_dim: int, out_dim: int, *,
+                       dtype=torch.bfloat16, activation: str = "none", x_rows: int = 0,
+                       weight_format: int = MOE_WEIGHTS_DTYPE) -> MoELinearConfig:
+    """``activation``: one of ACTIVATIONS.  ``x_rows``: rows of x when a call
+    gives ``row_index``, else 0 (x has ``rows`` rows)."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation {activation!r} is none of {ACTIVATIONS}")
+    if dtype not in (torch.bfloat16, torch.float32, "bf16", "f32", MOE_BF16, MOE_F32):
+        raise ValueError(f"dtype {dtype}, expected bfloat16 or float32")
+    code = MOE_BF16 if dtype in (torch.bfloat16, "bf16", MOE_BF16) else MOE_F32
+    return MoELinearConfig(int(rows), int(x_rows), int(groups), int(in_dim), int(out_dim), code,
+                           int(weight_format), ACTIVATIONS.index(activation))
+
+
+def _z_dim(cfg: MoELinearConfig) -> int:
+    return cfg.out_dim * (2 if cfg.activation == ACTIVATIONS.index("swiglu") else 1)
+
+
+def _x_shape(cfg: MoELinearConfig):
+    return (cfg.x_rows if cfg.x_rows > 0 else cfg.rows, cfg.in_dim)
+
+
+def moe_linear_workspace_size(cfg: MoELinearConfig) -> int:
+    return int(lib().moe_linear_workspace_size(ctypes.byref(cfg)))
+
+
+def alloc_linear_workspace(cfg: MoELinearConfig, device="cuda") -> torch.Tensor:
+    return _alloc(moe_linear_workspace_size(cfg), device)
+
+
+def moe_grouped_linear(cfg: MoELinearConfig, x: torch.Tensor, offsets: torch.Tensor,
+                       w: torch.Tensor, y: torch.Tensor, *, workspace: torch.Tensor,
+                       row_index: Optional[torch.Tensor] = None,
+                       w_scale: Optional[torch.Tensor] = None,
+                       bias: Optional[torch.Tensor] = None,
+                       residual: Optional[torch.Tensor] = None,
+                       z_codes: Optional[torch.Tensor] = None,
+                       z_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y[r] = act(x[src(r)] W_e^T + bias[e]) + residual[r] for the rows of every
+    group, and the 8-bit checkpoint of the pre-activations when ``z_codes``
+    (uint8) and ``z_scale`` are given; see ``moe_grouped_linear`` in
+    include/moe.h."""
+    dt, z, f32 = _TORCH_DTYPE[cfg.dtype], _z_dim(cfg), torch.float32
+    wt = torch.uint8 if cfg.weight_format == MOE_WEIGHTS_FP8_E4M3 else dt
+    c = _Call(y)
+    a = MoELinearArgs(
+        c.ptr(x, dt, "x", _x_shape(cfg)),
+        c.ptr(row_index, torch.int32, "row_index", (cfg.rows,)),
+        c.ptr(offsets, torch.int32, "offsets", (cfg.groups + 1,)),
+        c.ptr(w, wt, "w", (cfg.groups, z, cfg.in_dim)),
+        c.ptr(w_scale, f32, "w_scale", (cfg.groups, z)),
+        c.ptr(bias, f32, "bias", (cfg.groups, z)),
+        c.ptr(residual, dt, "residual", (cfg.rows, cfg.out_dim)),
+        c.ptr(y, dt, "y", (cfg.rows, cfg.out_dim)),
+        c.ptr(z_codes, torch.uint8, "z_codes", (cfg.rows, z)),
+        c.ptr(z_scale, f32, "z_scale", (cfg.rows, z // CHECKPOINT_BLOCK)))
+    c.run(lib().moe_grouped_linear, stream, ctypes.byref(cfg), ctypes.byref(a),
+          c.workspace(workspace), _nbytes(workspace))
+
+
+def moe_linear_backward_workspace_size(cfg: MoELinearConfig) -> int:
+    return int(lib().moe_linear_backward_workspace_size(ctypes.byref(cfg)))
+
+
+def alloc_linear_backward_workspace(cfg: MoELinearConfig, device="cuda") -> torch.Tensor:
+    return _alloc(moe_linear_backward_workspace_size(cfg), device)
+
+
+def moe_grouped_linear_backward(cfg: MoELinearConfig, x: Optional[torch.Tensor],
+                                offsets: torch.Tensor, w: Optional[torch.Tensor],
+                                dy: torch.Tensor, *, workspace: torch.Tensor,
+                                row_index: Optional[torch.Tensor] = None,
+                                z_codes: Optional[torch.Tensor] = None,
+                                z_scale: Optional[torch.Tensor] = None,
+                                dx: Optional[torch.Tensor] = None,
+                                dw: Optional[torch.Tensor] = None,
+                                dbias: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of moe_grouped_linear into ``dx`` [rows, in_dim], ``dw`` and
+    ``dbias`` (fp32), those that are given; the pre-activations come from their
+    8-bit checkpoint; see ``moe_grouped_linear_backward`` in include/moe.h."""
+    dt, z, f32 = _TORCH_DTYPE[cfg.dtype], _z_dim(cfg), torch.float32
+    c = _Call(dy)
+    a = MoELinearGradArgs(
+        c.ptr(x, dt, "x", _x_shape(cfg)),
+        c.ptr(row_index, torch.int32, "row_index", (cfg.rows,)),
+        c.ptr(offsets, torch.int32, "offsets", (cfg.groups + 1,)),
+        c.ptr(w, dt, "w", (cfg.groups, z, cfg.in_dim)),
+        c.ptr(dy, dt, "dy", (cfg.rows, cfg.out_dim)),
+        c.ptr(z_codes, torch.uint8, "z_codes", (cfg.rows, z)),
+        c.ptr(z_scale, f32, "z_scale", (cfg.rows, z // CHECKPOINT_BLOCK)),
+        c.ptr(dx, dt, "dx", (cfg.rows, cfg.in_dim)),
+        c.ptr(dw, dt, "dw", (cfg.groups, z, cfg.in_dim)),
+        c.ptr(dbias, f32, "dbias", (cfg.groups, z)))
+    c.run(lib().moe_grouped_linear_backward, stream, ctypes.byref(cfg), ctypes.byref(a),
+          c.workspace(workspace), _nbytes(workspace))
+
+
+def moe_checkpoint_pack(x: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor,
+                        stream=None) -> None:
+    """x [rows, cols] as E4M3 ``codes`` (uint8) and one fp32 ``scale`` for each
+    64 columns of a row; see ``moe_checkpoint_pack`` in include/moe.h."""
+    rows, cols = x.shape
+    c = _Call(x)
+    c.run(lib().moe_checkpoint_pack, stream, rows, cols, _dtype_code(x, "x"),
+          c.ptr(x, x.dtype, "x", (rows, cols)), c.ptr(codes, torch.uint8, "codes", (rows, cols)),
+          c.ptr(scale, torch.float32, "scale", (rows, cols // CHECKPOINT_BLOCK)))
+
+
+def moe_checkpoint_unpack(codes: torch.Tensor, scale: torch.Tensor, x: torch.Tensor,
+                          stream=None) -> None:
+    """x [rows, cols] = codes * scale; see ``moe_checkpoint_unpack`` in include/moe.h."""
+    rows, cols = x.shape
+    c = _Call(x)
+    c.run(lib().moe_checkpoint_unpack, stream, rows, cols, _dtype_code(x, "x"),
+          c.ptr(codes, torch.uint8, "codes", (rows, cols)),
+          c.ptr(scale, torch.float32, "scale", (rows, cols // CHECKPOINT_BLOCK)),
+          c.ptr(x, x.dtype, "x", (rows, cols)))
+
+
+def moe_combine(rows: torch.Tensor, slot_row: torch.Tensor, y: torch.Tensor, *,
+                gate: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y[t] = sum_s gate[t, s] rows[slot_row[t, s]] (no gate: 1); see
+    ``moe_combine`` in include/moe.h."""
+    (n_rows, d), (T, k) = rows.shape, slot_row.shape
+    c = _Call(y)
+    c.run(lib().moe_combine, stream, T, k, n_rows, d, _dtype_code(rows, "rows"),
+          c.ptr(rows, rows.dtype, "rows", (n_rows, d)),
+          c.ptr(slot_row, torch.int32, "slot_row", (T, k)),
+          c.ptr(gate, torch.float32, "gate", (T, k)), c.ptr(y, rows.dtype, "y", (T, d)))
+
+
+def moe_combine_backward(rows: torch.Tensor, slot_row: torch.Tensor,
+                         gate: Optional[torch.Tensor], dy: torch.Tensor,
+                         drows: Optional[torch.Tensor], dgate: Optional[torch.Tensor],
+                         stream=None) -> None:
+    """Gradients of moe_combine with respect to its rows and gates; see
+    ``moe_combine_backward`` in include/moe.h."""
+    (n_rows, d), (T, k) = rows.shape, slot_row.shape
+    c = _Call(dy)
+    c.run(lib().moe_combine_backward, stream, T, k, n_rows, d, _dtype_code(rows, "rows"),
+          c.ptr(rows, rows.dtype, "rows", (n_rows, d)),
+          c.ptr(slot_row, torch.int32, "slot_row", (T, k)),
+          c.ptr(gate, torch.float32, "gate", (T, k)), c.ptr(dy, rows.dtype, "dy", (T, d)),
+          c.ptr(drows, rows.dtype, "drows", (n_rows, d)),
+          c.ptr(dgate, torch.float32, "dgate", (T, k)))
 
 
 class MoELayer:

@@ -1,0 +1,222 @@
+// Activation checkpoints in 8 bits, and the backward of an activation from
+// one.
+//
+// A checkpoint of a [rows, cols] array holds an E4M3 code for each element
+// and one fp32 scale for each block of 64 columns of a row: with m the
+// block's largest magnitude (at least 1e-30),
+//   scale = m / 448,  code = E4M3(v (448 / m)),  v' = code scale,
+// so |v' - v| <= max(2^-4 |v|, 2^-10 scale).  It takes 1.0625 bytes an element against 2 of bf16.
+//
+// Every kernel here moves each byte once and computes a few operations per
+// element: all are bound by HBM.
+#include "linear.h"
+
+namespace moe {
+namespace {
+
+constexpr int kUnroll = 4;  // 8-column chunks of one thread, loaded before the first is used
+
+template <typename T>
+__global__ __launch_bounds__(256) void pack_kernel(const T* __restrict__ x, long chunks,
+                                                   uint8_t* __restrict__ codes,
+                                                   float* __restrict__ scale) {
+  const long c0 = static_cast<long>(blockIdx.x) * (256 * kUnroll) + threadIdx.x;
+  float v[kUnroll][8];
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const long c = c0 + 256 * i;
+    load8<T>(x + (c < chunks ? c : 0) * 8, v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const long c = c0 + 256 * i;  // chunks is a multiple of 8: a block is whole or absent
+    pack_block(v[i], c < chunks, codes + c * 8, scale + c / 8);
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void unpack_kernel(const uint8_t* __restrict__ codes,
+                                                     const float* __restrict__ scale, long chunks,
+                                                     T* __restrict__ x) {
+  const long c0 = static_cast<long>(blockIdx.x) * (256 * kUnroll) + threadIdx.x;
+  uint2 q[kUnroll];
+  float s[kUnroll];
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const long c = c0 + 256 * i < chunks ? c0 + 256 * i : 0;
+    q[i] = *reinterpret_cast<const uint2*>(codes + c * 8);
+    s[i] = scale[c / 8];
+  }
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const long c = c0 + 256 * i;
+    if (c >= chunks) return;
+    float v[8];
+    decode8(q[i], s[i], v);
+    store8<T>(x + c * 8, v);
+  }
+}
+
+// dz = dy act'(z) for one row tile of kActRows rows of a group and up to 512
+// columns of y; z is decoded from its checkpoint.  `lpr` lanes (a power of
+// two) hold one row's columns, 8 each, so a wavefront takes 64 / lpr rows at
+// a time.  A lane keeps its columns through the tile and adds up its unrounded
+// dz; the workgroup's sums, in a fixed order, are the tile's row of partial.
+template <typename T, bool GATED>
+__global__ __launch_bounds__(256) void act_backward_kernel(LinearArgs g, const T* __restrict__ dy,
+                                                           T* __restrict__ dz,
+                                                           float* __restrict__ partial, int lpr) {
+  constexpr int NS = GATED ? 16 : 8;
+  __shared__ float s_sum[256][NS + 1];
+  const TileScan t = scan_tiles(g.offsets, g.groups, g.rows, kActRows);
+  const int tile = blockIdx.x;
+  if (tile >= t.total) return;
+  const TileAt at = find_tile(t, g.offsets, g.groups, g.rows, kActRows, tile);
+  const int row0 = at.begin + at.m * kActRows, row1 = min(row0 + kActRows, at.end);
+  const int tid = threadIdx.x;
+  const int c = (blockIdx.y * lpr + tid % lpr) * 8;
+  const bool in = c < g.out_dim;
+  float sum[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) sum[i] = 0.f;
+  if (in) {
+    for (int r = row0 + tid / lpr; r < row1; r += 256 / lpr) {
+      const size_t yo = static_cast<size_t>(r) * g.out_dim + c;
+      const size_t zo = static_cast<size_t>(r) * g.z_dim + c;
+      float d[8], o[NS];
+      load8<T>(dy + yo, d);
+      if (g.act == kActNone) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = d[i];
+      } else {
+        float z[8];
+        decode8(*reinterpret_cast<const uint2*>(g.z_codes + zo), g.z_scale[zo / kCkptBlock], z);
+        if constexpr (GATED) {
+          float u[8];
+          decode8(*reinterpret_cast<const uint2*>(g.z_codes + zo + g.out_dim),
+                  g.z_scale[(zo + g.out_dim) / kCkptBlock], u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float p = sigmoid<T>(z[i]);
+            o[i] = d[i] * u[i] * (p + z[i] * p * (1.f - p));
+            o[8 + i] = d[i] * z[i] * p;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = d[i] * activate_slope<T>(g.act, z[i]);
+        }
+      }
+      if (dz != nullptr) {
+        store8<T>(dz + zo, o);
+        if (GATED) store8<T>(dz + zo + g.out_dim, o + 8);
+      }
+#pragma unroll
+      for (int i = 0; i < NS; ++i) sum[i] += o[i];
+    }
+  }
+  if (partial == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < NS; ++i) s_sum[tid][i] = sum[i];
+  __syncthreads();
+  if (tid >= lpr || !in) return;
+  for (int q = tid + lpr; q < 256; q += lpr)
+#pragma unroll
+    for (int i = 0; i < NS; ++i) sum[i] += s_sum[q][i];
+  float* p = partial + static_cast<size_t>(tile) * g.z_dim + c;
+  store8<float>(p, sum);
+  if (GATED) store8<float>(p + g.out_dim, sum + 8);
+}
+
+// dbias of one group and 256 columns: its tiles' partial sums, in tile order.
+__global__ __launch_bounds__(256) void bias_grad_kernel(LinearArgs g,
+                                                        const float* __restrict__ partial,
+                                                        float* __restrict__ dbias) {
+  const int e = blockIdx.x, n = blockIdx.y * 256 + threadIdx.x;
+  // tiles of the groups before e
+  int before = 0;
+  const int lane = threadIdx.x & 63;
+  for (int i = lane; i < e; i += 64) {
+    const int2 r = group_range(g.offsets, i, g.rows);
+    before += (r.y - r.x + kActRows - 1) / kActRows;
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) before += __shfl_xor(before, off, 64);
+  const int2 r = group_range(g.offsets, e, g.rows);
+  const int tiles = (r.y - r.x + kActRows - 1) / kActRows;
+  if (n >= g.z_dim) return;
+  const float* p = partial + static_cast<size_t>(before) * g.z_dim + n;
+  float acc = 0.f;
+  for (int t0 = 0; t0 < tiles; t0 += 8) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = t0 + i < tiles ? p[static_cast<size_t>(t0 + i) * g.z_dim] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc += v[i];
+  }
+  dbias[static_cast<size_t>(e) * g.z_dim + n] = acc;
+}
+
+constexpr long kMaxBlocks = 1L << 23;  // 2^31 threads of 256-thread workgroups
+
+}  // namespace
+
+hipError_t launch_checkpoint_pack(int dtype, const void* x, long rows, int cols, uint8_t* codes,
+                                  float* scale, hipStream_t s) {
+  const long chunks = rows * (cols / 8), blocks = (chunks + 256 * kUnroll - 1) / (256 * kUnroll);
+  if (blocks > kMaxBlocks) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks));
+  if (dtype == 1)
+    hipLaunchKernelGGL(pack_kernel<bf16_t>, grid, dim3(256), 0, s, static_cast<const bf16_t*>(x),
+                       chunks, codes, scale);
+  else
+    hipLaunchKernelGGL(pack_kernel<float>, grid, dim3(256), 0, s, static_cast<const float*>(x),
+                       chunks, codes, scale);
+  return hipGetLastError();
+}
+
+hipError_t launch_checkpoint_unpack(int dtype, const uint8_t* codes, const float* scale,
+                                    long rows, int cols, void* x, hipStream_t s) {
+  const long chunks = rows * (cols / 8), blocks = (chunks + 256 * kUnroll - 1) / (256 * kUnroll);
+  if (blocks > kMaxBlocks) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks));
+  if (dtype == 1)
+    hipLaunchKernelGGL(unpack_kernel<bf16_t>, grid, dim3(256), 0, s, codes, scale, chunks,
+                       static_cast<bf16_t*>(x));
+  else
+    hipLaunchKernelGGL(unpack_kernel<float>, grid, dim3(256), 0, s, codes, scale, chunks,
+                       static_cast<float*>(x));
+  return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t act_backward_t(const LinearArgs& g, const void* dy, void* dz, float* partial,
+                                 hipStream_t s) {
+  int lpr = 8;  // a row's columns over 8 .. 64 lanes
+  while (lpr < 64 && lpr * 8 < g.out_dim) lpr *= 2;
+  const long tiles = act_tiles(g.rows, g.groups);
+  if (tiles > kMaxBlocks) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(tiles), (g.out_dim + lpr * 8 - 1) / (lpr * 8));
+  if (g.act == kActSwiglu)
+    hipLaunchKernelGGL((act_backward_kernel<T, true>), grid, dim3(256), 0, s, g,
+                       static_cast<const T*>(dy), static_cast<T*>(dz), partial, lpr);
+  else
+    hipLaunchKernelGGL((act_backward_kernel<T, false>), grid, dim3(256), 0, s, g,
+                       static_cast<const T*>(dy), static_cast<T*>(dz), partial, lpr);
+  return hipGetLastError();
+}
+
+hipError_t launch_act_backward(int dtype, const LinearArgs& g, const void* dy, void* dz,
+                               float* partial, hipStream_t s) {
+  return dtype == 1 ? act_backward_t<bf16_t>(g, dy, dz, partial, s)
+                    : act_backward_t<float>(g, dy, dz, partial, s);
+}
+
+hipError_t launch_bias_grad(const LinearArgs& g, const float* partial, float* dbias,
+                            hipStream_t s) {
+  const dim3 grid(g.groups, (g.z_dim + 255) / 256);
+  hipLaunchKernelGGL(bias_grad_kernel, grid, dim3(256), 0, s, g, partial, dbias);
+  return hipGetLastError();
+}
+
+}  // namespace moe

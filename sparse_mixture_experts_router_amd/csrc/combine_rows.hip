@@ -1,0 +1,146 @@
+// Combine of the experts' rows into tokens, and its gradient.
+//
+//   y[t]    = sum_s gate[t, s] rows[slot_row[t, s]]       (gate null: 1)
+//   drows[slot_row[t, s]] = gate[t, s] dy[t]
+//   dgate[t, s] = <dy[t], rows[slot_row[t, s]]>
+//
+// over the slots that have a row (slot_row inside [0, n_rows); a dropped slot
+// adds nothing and its dgate is 0).  Sums in fp32, slot after slot, rounded
+// once.  One workgroup per token and 16 bytes of a row per lane: every row is
+// read (and written) once, so HBM bounds both.  With gate null the combine is
+// also the gradient of reading x rows through row_token.
+#include "linear.h"
+
+namespace moe {
+namespace {
+
+constexpr int kSlots = 4;  // rows whose loads are in flight together
+
+template <typename T>
+__global__ __launch_bounds__(256) void combine_rows_kernel(const T* __restrict__ rows,
+                                                           const int32_t* __restrict__ slot_row,
+                                                           const float* __restrict__ gate,
+                                                           int n_rows, int k, int d,
+                                                           T* __restrict__ y) {
+  const size_t t = blockIdx.x;
+  const int32_t* sr = slot_row + t * k;
+  const float* gt = gate != nullptr ? gate + t * k : nullptr;
+  for (int c = threadIdx.x * 8; c < d; c += 256 * 8) {
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    for (int s0 = 0; s0 < k; s0 += kSlots) {
+      float v[kSlots][8], w[kSlots];
+      bool on[kSlots];
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        const int r = s0 + q < k ? sr[s0 + q] : -1;
+        on[q] = r >= 0 && r < n_rows;
+        w[q] = 1.f;
+        if (!on[q]) continue;  // uniform over the workgroup
+        if (gt != nullptr) w[q] = gt[s0 + q];
+        load8<T>(rows + static_cast<size_t>(r) * d + c, v[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        if (!on[q]) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[q], v[q][i], acc[i]);
+      }
+    }
+    store8<T>(y + t * d + c, acc);
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void combine_rows_backward_kernel(
+    const T* __restrict__ rows, const int32_t* __restrict__ slot_row,
+    const float* __restrict__ gate, const T* __restrict__ dy, int n_rows, int k, int d,
+    T* __restrict__ drows, float* __restrict__ dgate) {
+  __shared__ float s_dot[kSlots][4];
+  const size_t t = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t* sr = slot_row + t * k;
+  for (int s0 = 0; s0 < k; s0 += kSlots) {
+    int row[kSlots];
+    float w[kSlots], dot[kSlots];
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) {
+      const int r = s0 + q < k ? sr[s0 + q] : -1;
+      row[q] = r < n_rows ? r : -1;
+      w[q] = gate != nullptr && row[q] >= 0 ? gate[t * k + s0 + q] : 1.f;
+      dot[q] = 0.f;
+    }
+    for (int c = threadIdx.x * 8; c < d; c += 256 * 8) {
+      float g[8], v[kSlots][8];
+      load8<T>(dy + t * d + c, g);
+      if (dgate != nullptr) {
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q)
+          if (row[q] >= 0) load8<T>(rows + static_cast<size_t>(row[q]) * d + c, v[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        if (row[q] < 0) continue;  // uniform over the workgroup
+        if (dgate != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[q] = fmaf(g[i], v[q][i], dot[q]);
+        }
+        if (drows != nullptr) {
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = w[q] * g[i];
+          store8<T>(drows + static_cast<size_t>(row[q]) * d + c, o);
+        }
+      }
+    }
+    if (dgate == nullptr) continue;
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) {
+      float v = dot[q];
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+      if (lane == 0) s_dot[q][wave] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x < kSlots && s0 + static_cast<int>(threadIdx.x) < k) {
+      const float* p = s_dot[threadIdx.x];
+      dgate[t * k + s0 + threadIdx.x] = ((p[0] + p[1]) + p[2]) + p[3];
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+hipError_t launch_combine_rows(int dtype, const void* rows, const int32_t* slot_row,
+                               const float* gate, int n_rows, int T_, int k, int d, void* y,
+                               hipStream_t s) {
+  if (dtype == 1)
+    hipLaunchKernelGGL(combine_rows_kernel<bf16_t>, dim3(T_), dim3(256), 0, s,
+                       static_cast<const bf16_t*>(rows), slot_row, gate, n_rows, k, d,
+                       static_cast<bf16_t*>(y));
+  else
+    hipLaunchKernelGGL(combine_rows_kernel<float>, dim3(T_), dim3(256), 0, s,
+                       static_cast<const float*>(rows), slot_row, gate, n_rows, k, d,
+                       static_cast<float*>(y));
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_rows_backward(int dtype, const void* rows, const int32_t* slot_row,
+                                        const float* gate, const void* dy, int n_rows, int T_,
+                                        int k, int d, void* drows, float* dgate, hipStream_t s) {
+  if (dtype == 1)
+    hipLaunchKernelGGL(combine_rows_backward_kernel<bf16_t>, dim3(T_), dim3(256), 0, s,
+                       static_cast<const bf16_t*>(rows), slot_row, gate,
+                       static_cast<const bf16_t*>(dy), n_rows, k, d, static_cast<bf16_t*>(drows),
+                       dgate);
+  else
+    hipLaunchKernelGGL(combine_rows_backward_kernel<float>, dim3(T_), dim3(256), 0, s,
+                       static_cast<const float*>(rows), slot_row, gate,
+                       static_cast<const float*>(dy), n_rows, k, d, static_cast<float*>(drows),
+                       dgate);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,352 @@
+// Internal declarations of the grouped linear maps (products grouped by
+// expert, with their epilogue and gradients), the 8-bit checkpoints, the
+// row grouping and the combine.
+//
+// Row r of y belongs to group e when offsets[e] <= r < offsets[e + 1]; rows
+// at or past offsets[groups] belong to none and are neither read nor written.
+// The kernels take offsets as they find them on the device, but clamp each
+// group's range into [0, rows], so that no offset can send an access out of
+// bounds.
+#pragma once
+
+#include "mfma.h"
+#include "vec.h"
+
+namespace moe {
+
+// moe_activation (include/moe.h)
+enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3, kActSwiglu = 4 };
+
+constexpr int kCkptBlock = 64;       // columns of a row that share one scale
+constexpr float kCkptMax = 448.0f;   // largest finite E4M3 value
+constexpr float kCkptTiny = 1e-30f;  // smallest block maximum a scale is made from
+
+struct LinearArgs {
+  const void* x;             // forward: [x_rows or rows, in]; see launchers
+  const int32_t* row_index;  // source row of x for every row, or null
+  const int32_t* offsets;    // [groups + 1]
+  const void* w;             // [groups, z_dim, in]
+  const float* w_scale;      // [groups, z_dim] (FP8 weights) or null
+  const float* bias;         // [groups, z_dim] or null
+  const void* residual;      // [rows, out] or null
+  void* y;                   // [rows, out]
+  uint8_t* z_codes;          // [rows, z_dim] or null
+  float* z_scale;            // [rows, z_dim / 64] or null
+  int rows, groups;
+  int in_dim;                // columns of x
+  int out_dim;               // columns of y
+  int z_dim;                 // rows of a group's W: out_dim, or 2 out_dim (SwiGLU)
+  int x_rows;                // rows of x
+  int act;
+};
+
+// ---------------------------------------------------------------- launchers
+// Forward: y = act(x W^T + b) + residual on BM-row tiles; wfp8: E4M3 weights.
+hipError_t launch_linear_tile(int dtype, bool wfp8, const LinearArgs& g, hipStream_t s);
+// dX[r] = dz[r] W_e.  dz [rows, z_dim], dx [rows, in].
+hipError_t launch_linear_dx_tile(int dtype, const LinearArgs& g, const void* dz, void* dx,
+                                 hipStream_t s);
+// dW_e = sum_r dz[r]^T x[src(r)]; groups without rows get zeros.
+hipError_t launch_linear_dw_tile(int dtype, const LinearArgs& g, const void* dz, void* dw,
+                                 hipStream_t s);
+
+// Row tiles of kActRows rows that the activation's backward works in; the
+// most there can be for `rows` rows in `groups` groups.
+constexpr int kActRows = 64;
+inline long act_tiles(long rows, long groups) {
+  return rows / kActRows + (groups < rows ? groups : rows);
+}
+// dz = dy act'(z) from the checkpoint of z (dz null: dy itself is dz), and,
+// when partial is not null, the sum of every tile's unrounded dz rows:
+// partial [act_tiles, z_dim].
+hipError_t launch_act_backward(int dtype, const LinearArgs& g, const void* dy, void* dz,
+                               float* partial, hipStream_t s);
+// dbias[e] = the sum of group e's tiles of partial, in tile order.
+hipError_t launch_bias_grad(const LinearArgs& g, const float* partial, float* dbias,
+                            hipStream_t s);
+
+hipError_t launch_checkpoint_pack(int dtype, const void* x, long rows, int cols, uint8_t* codes,
+                                  float* scale, hipStream_t s);
+hipError_t launch_checkpoint_unpack(int dtype, const uint8_t* codes, const float* scale,
+                                    long rows, int cols, void* x, hipStream_t s);
+
+// Workgroups (and rows of the count table) that the grouping of n (token,
+// slot) pairs runs on.
+int group_blocks(long n);
+hipError_t launch_group_rows(const int32_t* topk_idx, int T, int N, int k, int capacity,
+                             int32_t* table, int32_t* offsets, int32_t* row_token,
+                             int32_t* slot_row, hipStream_t s);
+hipError_t launch_combine_rows(int dtype, const void* rows, const int32_t* slot_row,
+                               const float* gate, int n_rows, int T, int k, int d, void* y,
+                               hipStream_t s);
+hipError_t launch_combine_rows_backward(int dtype, const void* rows, const int32_t* slot_row,
+                                        const float* gate, const void* dy, int n_rows, int T,
+                                        int k, int d, void* drows, float* dgate, hipStream_t s);
+
+// ---------------------------------------------------------------- device helpers
+// Rows [begin, end) of group e, whatever the offsets hold.
+__device__ __forceinline__ int2 group_range(const int32_t* offsets, int e, int rows) {
+  const int b = min(max(offsets[e], 0), rows);
+  return make_int2(b, min(max(offsets[e + 1], b), rows));
+}
+
+// Row tiles of BM rows, group after group, found by every wavefront on its
+// own: lane l adds up the tiles of groups l per .. (l + 1) per - 1, one
+// wavefront scan gives the first tile of each lane's groups.
+struct TileScan {
+  int per;    // groups per lane
+  int first;  // tiles before this lane's groups
+  int mine;   // tiles of this lane's groups
+  int total;  // tiles in all
+};
+__device__ __forceinline__ TileScan scan_tiles(const int32_t* offsets, int groups, int rows,
+                                               int bm) {
+  TileScan t;
+  const int lane = threadIdx.x & 63;
+  t.per = (groups + 63) >> 6;
+  t.mine = 0;
+  for (int i = 0; i < t.per; ++i) {
+    const int e = lane * t.per + i;
+    if (e < groups) {
+      const int2 r = group_range(offsets, e, rows);
+      t.mine += (r.y - r.x + bm - 1) / bm;
+    }
+  }
+  int incl = t.mine;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int o = __shfl_up(incl, off, 64);
+    if (lane >= off) incl += o;
+  }
+  t.first = incl - t.mine;
+  t.total = __shfl(incl, 63, 64);
+  return t;
+}
+// Group e and the index of tile `tile` (0 <= tile < t.total) inside it;
+// `tiles`: the group's tiles, `before`: tiles of the groups before it.
+struct TileAt {
+  int e, m, tiles, before, begin, end;
+};
+__device__ __forceinline__ TileAt find_tile(const TileScan& t, const int32_t* offsets, int groups,
+                                            int rows, int bm, int tile) {
+  const unsigned long long hit = __ballot(t.first <= tile && tile < t.first + t.mine);
+  const int l = hit != 0 ? __ffsll(hit) - 1 : 0;
+  int before = __shfl(t.first, l, 64);
+  TileAt a{};
+  for (int i = 0; i < t.per; ++i) {
+    const int e = l * t.per + i;
+    if (e >= groups) break;
+    const int2 r = group_range(offsets, e, rows);
+    const int n = (r.y - r.x + bm - 1) / bm;
+    a = TileAt{e, tile - before, n, before, r.x, r.y};
+    if (tile < before + n) break;
+    before += n;
+  }
+  return a;
+}
+
+// Work item (group, row tile, column tile) of workgroup blockIdx.x on a grid
+// of 8 equal shares: workgroups take the 8 XCDs in turn, and each XCD walks a
+// contiguous share of the list, so the tiles it runs at once share rows of x
+// and of W in its L2.  Inside a group the tiles go in bands of 8 row tiles,
+// column by column.  False: nothing to do.
+__device__ __forceinline__ bool find_item(const int32_t* offsets, int groups, int rows, int bm,
+                                          int nt, TileAt& at, int& col) {
+  const TileScan t = scan_tiles(offsets, groups, rows, bm);
+  const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
+  const long items = static_cast<long>(t.total) * nt;
+  const long lo = items * xcd / 8, hi = items * (xcd + 1) / 8;
+  if (lo + idx >= hi) return false;
+  const long w = lo + idx;
+  at = find_tile(t, offsets, groups, rows, bm, static_cast<int>(w / nt));
+  const int q = static_cast<int>(w - static_cast<long>(at.before) * nt);
+  const int band = q / (8 * nt), tw = min(8, at.tiles - band * 8), r = q - band * 8 * nt;
+  col = r / tw;
+  at.m = band * 8 + r % tw;
+  return true;
+}
+inline long item_grid(long rows, long groups, int bm, long nt) {
+  const long tiles = rows / bm + (groups < rows ? groups : rows);
+  return 8 * ((tiles * nt + 7) / 8 + 1);
+}
+
+template <typename T> __device__ __forceinline__ void load8(const T* p, float* v);
+template <> __device__ __forceinline__ void load8<bf16_t>(const bf16_t* p, float* v) {
+  Vec<bf16_t>::load(p, v);
+}
+template <> __device__ __forceinline__ void load8<float>(const float* p, float* v) {
+  Vec<float>::load(p, v);
+  Vec<float>::load(p + 4, v + 4);
+}
+template <typename T> __device__ __forceinline__ void store8(T* p, const float* v);
+template <> __device__ __forceinline__ void store8<bf16_t>(bf16_t* p, const float* v) {
+  Vec<bf16_t>::store(p, v);
+}
+template <> __device__ __forceinline__ void store8<float>(float* p, const float* v) {
+  Vec<float>::store(p, v);
+  Vec<float>::store(p + 4, v + 4);
+}
+
+// 1 / (1 + e^-z).  fp32 layers take the exact exponential and division,
+// bf16 layers the hardware's (relative error below 2^-18 for |z| < 40, far
+// inside a bf16 rounding).  At z = -inf both give 0.
+template <typename T> __device__ __forceinline__ float sigmoid(float z);
+template <> __device__ __forceinline__ float sigmoid<float>(float z) {
+  return 1.0f / (1.0f + expf(-z));
+}
+template <> __device__ __forceinline__ float sigmoid<bf16_t>(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+// The normal distribution's CDF.
+__device__ __forceinline__ float normal_cdf(float z) {
+  return 0.5f * (1.0f + erff(z * 0.70710678118654752f));
+}
+
+template <typename T> __device__ __forceinline__ float activate(int act, float z) {
+  switch (act) {
+    case kActRelu: return z < 0.f ? 0.f : z;  // keeps NaN
+    case kActGelu: return z * normal_cdf(z);
+    case kActSilu: return z * sigmoid<T>(z);
+    default: return z;
+  }
+}
+// d act / dz.  ReLU: 0 at z = 0.
+template <typename T> __device__ __forceinline__ float activate_slope(int act, float z) {
+  switch (act) {
+    case kActRelu: return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
+    case kActGelu:
+      return normal_cdf(z) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+    case kActSilu: {
+      const float p = sigmoid<T>(z);
+      return p + z * p * (1.f - p);
+    }
+    default: return 1.f;
+  }
+}
+
+// Largest finite magnitude of 8 values (NaN and infinities do not count).
+__device__ __forceinline__ float max_finite8(const float* v) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = fabsf(v[i]);
+    m = a < INFINITY ? fmaxf(m, a) : m;
+  }
+  return m;
+}
+// 8 values as E4M3 codes of v * inv, round to nearest even; a value that is
+// not finite becomes the NaN code (E4M3 has no infinity).
+__device__ __forceinline__ uint2 encode8(const float* v, float inv) {
+  float s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // |v| <= the block's maximum, so |v inv| <= 448 up to a rounding, which
+    // the clamp takes back; fminf and fmaxf would turn NaN into a number
+    const float t = fabsf(v[i]) < INFINITY ? fminf(fmaxf(v[i] * inv, -kCkptMax), kCkptMax)
+                                           : __builtin_nanf("");
+    s[i] = t;
+  }
+  uint2 r;
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(s[0], s[1], 0, false);
+  r.x = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(s[2], s[3], lo, true));
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(s[4], s[5], 0, false);
+  r.y = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(s[6], s[7], hi, true));
+  return r;
+}
+__device__ __forceinline__ void decode8(uint2 c, float scale, float* v) {
+  typedef __attribute__((ext_vector_type(2))) float f32x2;
+  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c.x), false);
+  const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c.x), true);
+  const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c.y), false);
+  const f32x2 e = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c.y), true);
+  v[0] = a[0] * scale; v[1] = a[1] * scale; v[2] = b[0] * scale; v[3] = b[1] * scale;
+  v[4] = d[0] * scale; v[5] = d[1] * scale; v[6] = e[0] * scale; v[7] = e[1] * scale;
+}
+// One 64-column block of a row, 8 columns in each of 8 neighbouring lanes
+// (lane mod 8 in column order): its codes, and its scale from the first of
+// them.  `ok` is the same for the 8 lanes.
+__device__ __forceinline__ void pack_block(const float* v, bool ok, uint8_t* codes, float* scale) {
+  float m = max_finite8(v);
+  m = fmaxf(m, __shfl_xor(m, 1, 64));
+  m = fmaxf(m, __shfl_xor(m, 2, 64));
+  m = fmaxf(m, __shfl_xor(m, 4, 64));
+  m = fmaxf(m, kCkptTiny);
+  if (!ok) return;
+  *reinterpret_cast<uint2*>(codes) = encode8(v, kCkptMax / m);
+  if ((threadIdx.x & 7) == 0) *scale = m / kCkptMax;
+}
+
+// The epilogue of the forward on 8 columns of one row: columns n .. n + 7 of
+// y, n a multiple of 8, 8 neighbouring lanes holding a whole 64-column block.
+// v: the products x W^T (SwiGLU: v the gate's, u the up projection's).
+template <typename T, bool GATED>
+__device__ __forceinline__ void linear_epilogue8(const LinearArgs& g, int e, long row, int n,
+                                                 bool ok, float* v, float* u) {
+  const size_t eo = static_cast<size_t>(e) * g.z_dim;
+  if (ok) {
+    if (g.w_scale != nullptr) {
+      float t[8];
+      load8<float>(g.w_scale + eo + n, t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= t[i];
+      if (GATED) {
+        load8<float>(g.w_scale + eo + g.out_dim + n, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] *= t[i];
+      }
+    }
+    if (g.bias != nullptr) {
+      float t[8];
+      load8<float>(g.bias + eo + n, t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += t[i];
+      if (GATED) {
+        load8<float>(g.bias + eo + g.out_dim + n, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] += t[i];
+      }
+    }
+  }
+  if (g.z_codes != nullptr) {
+    const size_t zo = static_cast<size_t>(row) * g.z_dim;
+    uint8_t* c = g.z_codes + zo;
+    float* sc = g.z_scale + zo / kCkptBlock;
+    pack_block(v, ok, c + n, sc + n / kCkptBlock);
+    if (GATED) pack_block(u, ok, c + g.out_dim + n, sc + (g.out_dim + n) / kCkptBlock);
+  }
+  if (!ok) return;
+  float h[8];
+  if (GATED) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = v[i] * sigmoid<T>(v[i]) * u[i];
+  } else {
+    // one uniform branch for the 8 values
+    switch (g.act) {
+      case kActRelu:
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = activate<T>(kActRelu, v[i]);
+        break;
+      case kActGelu:
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = activate<T>(kActGelu, v[i]);
+        break;
+      case kActSilu:
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = activate<T>(kActSilu, v[i]);
+        break;
+      default:
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = v[i];
+    }
+  }
+  const size_t yo = static_cast<size_t>(row) * g.out_dim + n;
+  if (g.residual != nullptr) {
+    float t[8];
+    load8<T>(static_cast<const T*>(g.residual) + yo, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] += t[i];
+  }
+  store8<T>(static_cast<T*>(g.y) + yo, h);
+}
+
+}  // namespace moe

@@ -1,0 +1,312 @@
+// Host side of the calls for experts of one's own (include/moe.h): argument
+// checks, workspace layout and launch sequences.  Nothing here allocates,
+// frees or waits on the device.
+#include "moe.h"
+#include "api_error.h"
+#include "linear.h"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int z_dim(const moe_linear_config& c) {
+  return c.activation == MOE_ACT_SWIGLU ? 2 * c.out_dim : c.out_dim;
+}
+
+moe_status check_dtype(int dtype) {
+  return dtype == MOE_F32 || dtype == MOE_BF16 ? MOE_OK : fail(MOE_ERR_INVALID_ARG, "bad dtype");
+}
+
+moe_status check_linear(const moe_linear_config* c) {
+  if (c == nullptr) return fail(MOE_ERR_INVALID_ARG, "cfg is NULL");
+  if (c->rows < 0 || c->x_rows < 0 || c->groups <= 0 || c->in_dim <= 0 || c->out_dim <= 0)
+    return fail(MOE_ERR_INVALID_ARG, "sizes must be positive (rows, x_rows >= 0)");
+  if (check_dtype(c->dtype) != MOE_OK) return MOE_ERR_INVALID_ARG;
+  if (c->weight_format != MOE_WEIGHTS_DTYPE && c->weight_format != MOE_WEIGHTS_FP8_E4M3)
+    return fail(MOE_ERR_INVALID_ARG, "bad weight_format");
+  if (c->activation < MOE_ACT_NONE || c->activation > MOE_ACT_SWIGLU)
+    return fail(MOE_ERR_INVALID_ARG, "bad activation");
+  if (c->weight_format == MOE_WEIGHTS_FP8_E4M3 && c->dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "FP8 weights need dtype MOE_BF16");
+  if (c->groups > kMaxExperts) return fail(MOE_ERR_UNSUPPORTED, "groups > 512");
+  if (c->in_dim % 64 != 0 || c->out_dim % 64 != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "in_dim and out_dim must be multiples of 64");
+  if (c->in_dim > (1 << 20) || c->out_dim > (1 << 20))
+    return fail(MOE_ERR_UNSUPPORTED, "in_dim or out_dim > 2^20");
+  if (c->rows >= (1 << 30) || c->x_rows >= (1 << 30))
+    return fail(MOE_ERR_UNSUPPORTED, "too many rows");
+  // grids: at most 2^23 tiles of 128 rows by 64 columns (forward and dX), or
+  // of 128 by 128 (dW)
+  const long wide = std::max(c->in_dim, z_dim(*c));
+  if ((c->rows / 128 + c->groups) * (wide / 64) > (1L << 23) ||
+      static_cast<long>(c->groups) * (z_dim(*c) / 64) * (c->in_dim / 64) > (1L << 24))
+    return fail(MOE_ERR_UNSUPPORTED, "too many tiles");
+  return MOE_OK;
+}
+
+moe_status check_rows_of_x(const moe_linear_config& c, const int32_t* row_index) {
+  if ((c.x_rows > 0) != (row_index != nullptr) && c.rows > 0)
+    return fail(MOE_ERR_INVALID_ARG, "row_index and x_rows go together");
+  return MOE_OK;
+}
+
+moe_status check_space(const void* ws, size_t have, size_t need) {
+  if (ws == nullptr) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+  if ((reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0)
+    return fail(MOE_ERR_WORKSPACE, "workspace not 256-byte aligned");
+  if (have < need) return fail(MOE_ERR_WORKSPACE, "workspace smaller than its size function says");
+  return MOE_OK;
+}
+
+LinearArgs linear_args(const moe_linear_config& c) {
+  LinearArgs g{};
+  g.rows = c.rows;
+  g.groups = c.groups;
+  g.in_dim = c.in_dim;
+  g.out_dim = c.out_dim;
+  g.z_dim = z_dim(c);
+  g.x_rows = c.x_rows > 0 ? c.x_rows : c.rows;
+  g.act = c.activation;
+  return g;
+}
+
+// Workspace of the backward.
+struct BackSpace {
+  size_t dz, partial, total;
+};
+BackSpace back_space(const moe_linear_config& c) {
+  const size_t eb = c.dtype == MOE_BF16 ? 2 : 4, z = z_dim(c);
+  BackSpace b{};
+  size_t o = 0;
+  b.dz = o;
+  if (c.activation != MOE_ACT_NONE) o += align_up(static_cast<size_t>(c.rows) * z * eb);
+  b.partial = o;
+  o += align_up(static_cast<size_t>(act_tiles(c.rows, c.groups)) * z * 4);
+  b.total = o > 0 ? o : kAlign;
+  return b;
+}
+
+constexpr long kMaxGroupPairs = 1L << 30;
+
+moe_status check_group(int32_t T, int32_t N, int32_t k) {
+  if (T < 0 || N <= 0 || k <= 0) return fail(MOE_ERR_INVALID_ARG, "bad T, N or k");
+  if (N > kMaxExperts) return fail(MOE_ERR_UNSUPPORTED, "n_experts > 512");
+  if (k > kMaxTopK) return fail(MOE_ERR_UNSUPPORTED, "top_k > 16");
+  if (static_cast<long>(T) * k >= kMaxGroupPairs) return fail(MOE_ERR_UNSUPPORTED, "T * k too large");
+  return MOE_OK;
+}
+
+moe_status check_combine(int32_t T, int32_t k, int32_t n_rows, int32_t d, int32_t dtype) {
+  if (T < 0 || k <= 0 || n_rows < 0 || d <= 0) return fail(MOE_ERR_INVALID_ARG, "bad T, k, n_rows or d");
+  if (check_dtype(dtype) != MOE_OK) return MOE_ERR_INVALID_ARG;
+  if (k > kMaxTopK) return fail(MOE_ERR_UNSUPPORTED, "top_k > 16");
+  if (d % 64 != 0) return fail(MOE_ERR_UNSUPPORTED, "d must be a multiple of 64");
+  if (T >= (1 << 24)) return fail(MOE_ERR_UNSUPPORTED, "T >= 2^24");
+  return MOE_OK;
+}
+
+moe_status check_checkpoint(int64_t rows, int32_t cols, int32_t dtype, const void* x,
+                            const void* codes, const void* scale) {
+  if (rows < 0 || cols <= 0) return fail(MOE_ERR_INVALID_ARG, "bad rows or cols");
+  if (check_dtype(dtype) != MOE_OK) return MOE_ERR_INVALID_ARG;
+  if (cols % kCkptBlock != 0) return fail(MOE_ERR_UNSUPPORTED, "cols must be a multiple of 64");
+  if (rows > (int64_t{1} << 36) / cols) return fail(MOE_ERR_UNSUPPORTED, "rows * cols too large");
+  if (rows == 0) return MOE_OK;
+  if (x == nullptr || codes == nullptr || scale == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "x, codes or scale is NULL");
+  if (!aligned16(x) || !aligned16(codes))
+    return fail(MOE_ERR_INVALID_ARG, "x or codes not 16-byte aligned");
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_group_workspace_size(int32_t T, int32_t N, int32_t k) {
+  if (check_group(T, N, k) != MOE_OK) return 0;
+  return align_up(static_cast<size_t>(group_blocks(static_cast<long>(T) * k)) * N * 4);
+}
+
+moe_status moe_group_rows(int32_t T, int32_t N, int32_t k, int32_t capacity,
+                          const int32_t* topk_idx, int32_t* offsets, int32_t* row_token,
+                          int32_t* slot_row, void* workspace, size_t ws_bytes, void* stream) {
+  clear_error();
+  moe_status st = check_group(T, N, k);
+  if (st != MOE_OK) return st;
+  if (capacity < 0) return fail(MOE_ERR_INVALID_ARG, "capacity < 0");
+  if (offsets == nullptr) return fail(MOE_ERR_INVALID_ARG, "offsets is NULL");
+  if (T > 0 && (topk_idx == nullptr || row_token == nullptr || slot_row == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "topk_idx, row_token or slot_row is NULL");
+  if ((st = check_space(workspace, ws_bytes, moe_group_workspace_size(T, N, k))) != MOE_OK)
+    return st;
+  const hipError_t err =
+      launch_group_rows(topk_idx, T, N, k, capacity, static_cast<int32_t*>(workspace), offsets,
+                        row_token, slot_row, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? MOE_OK : hip_fail(err, "grouping kernel");
+}
+
+size_t moe_linear_workspace_size(const moe_linear_config* cfg) {
+  if (check_linear(cfg) != MOE_OK) return 0;
+  return kAlign;
+}
+
+moe_status moe_grouped_linear(const moe_linear_config* cfg, const moe_linear_args* a,
+                              void* workspace, size_t ws_bytes, void* stream) {
+  clear_error();
+  moe_status st = check_linear(cfg);
+  if (st != MOE_OK) return st;
+  const moe_linear_config& c = *cfg;
+  if (a == nullptr) return fail(MOE_ERR_INVALID_ARG, "args is NULL");
+  if (c.rows == 0) return MOE_OK;
+  const bool fp8 = c.weight_format == MOE_WEIGHTS_FP8_E4M3;
+  if (a->x == nullptr || a->offsets == nullptr || a->w == nullptr || a->y == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "x, offsets, w or y is NULL");
+  if (fp8 != (a->w_scale != nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "w_scale goes with FP8 weights");
+  if ((a->z_codes != nullptr) != (a->z_scale != nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "z_codes and z_scale go together");
+  if (!aligned16(a->x) || !aligned16(a->w) || !aligned16(a->y) || !aligned16(a->residual) ||
+      !aligned16(a->bias) || !aligned16(a->w_scale) || !aligned16(a->z_codes))
+    return fail(MOE_ERR_INVALID_ARG, "a tensor is not 16-byte aligned");
+  if ((st = check_rows_of_x(c, a->row_index)) != MOE_OK) return st;
+  if ((st = check_space(workspace, ws_bytes, moe_linear_workspace_size(cfg))) != MOE_OK) return st;
+  LinearArgs g = linear_args(c);
+  g.x = a->x;
+  g.row_index = a->row_index;
+  g.offsets = a->offsets;
+  g.w = a->w;
+  g.w_scale = a->w_scale;
+  g.bias = a->bias;
+  g.residual = a->residual;
+  g.y = a->y;
+  g.z_codes = a->z_codes;
+  g.z_scale = a->z_scale;
+  const hipError_t err = launch_linear_tile(c.dtype, fp8, g, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? MOE_OK : hip_fail(err, "grouped linear kernel");
+}
+
+size_t moe_linear_backward_workspace_size(const moe_linear_config* cfg) {
+  if (check_linear(cfg) != MOE_OK) return 0;
+  return back_space(*cfg).total;
+}
+
+moe_status moe_grouped_linear_backward(const moe_linear_config* cfg,
+                                       const moe_linear_grad_args* a, void* workspace,
+                                       size_t ws_bytes, void* stream) {
+  clear_error();
+  moe_status st = check_linear(cfg);
+  if (st != MOE_OK) return st;
+  const moe_linear_config& c = *cfg;
+  if (c.weight_format != MOE_WEIGHTS_DTYPE)
+    return fail(MOE_ERR_UNSUPPORTED, "the backward needs weights in dtype");
+  if (a == nullptr) return fail(MOE_ERR_INVALID_ARG, "args is NULL");
+  // (without rows the only gradients there can be are those of w and bias)
+  if (a->dw == nullptr && a->dbias == nullptr && c.rows == 0) return MOE_OK;
+  if (a->dx == nullptr && a->dw == nullptr && a->dbias == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "no gradient asked for");
+  if (a->offsets == nullptr) return fail(MOE_ERR_INVALID_ARG, "offsets is NULL");
+  const bool act = c.activation != MOE_ACT_NONE;
+  if (c.rows > 0) {
+    if (a->dy == nullptr || (a->dx != nullptr && a->w == nullptr) ||
+        (a->dw != nullptr && a->x == nullptr))
+      return fail(MOE_ERR_INVALID_ARG, "dy, w or x is NULL");
+    if (act && (a->z_codes == nullptr || a->z_scale == nullptr))
+      return fail(MOE_ERR_INVALID_ARG, "the activation's backward needs z_codes and z_scale");
+    if (a->dw != nullptr && (st = check_rows_of_x(c, a->row_index)) != MOE_OK) return st;
+  }
+  if (!aligned16(a->x) || !aligned16(a->w) || !aligned16(a->dy) || !aligned16(a->dx) ||
+      !aligned16(a->dw) || !aligned16(a->dbias) || !aligned16(a->z_codes))
+    return fail(MOE_ERR_INVALID_ARG, "a tensor is not 16-byte aligned");
+  const BackSpace b = back_space(c);
+  if ((st = check_space(workspace, ws_bytes, b.total)) != MOE_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LinearArgs g = linear_args(c);
+  g.x = a->x;
+  g.row_index = a->row_index;
+  g.offsets = a->offsets;
+  g.w = a->w;
+  g.z_codes = const_cast<uint8_t*>(a->z_codes);
+  g.z_scale = const_cast<float*>(a->z_scale);
+  char* base = static_cast<char*>(workspace);
+  float* partial = a->dbias != nullptr ? reinterpret_cast<float*>(base + b.partial) : nullptr;
+  const bool products = a->dx != nullptr || a->dw != nullptr;
+  const void* dz = act ? base + b.dz : a->dy;
+  hipError_t err;
+  if (c.rows > 0 && ((act && products) || partial != nullptr)) {
+    err = launch_act_backward(c.dtype, g, a->dy, act && products ? base + b.dz : nullptr, partial,
+                              s);
+    if (err != hipSuccess) return hip_fail(err, "activation backward");
+  }
+  if (a->dbias != nullptr && (err = launch_bias_grad(g, partial, a->dbias, s)) != hipSuccess)
+    return hip_fail(err, "bias gradient");
+  if (c.rows > 0 && a->dx != nullptr &&
+      (err = launch_linear_dx_tile(c.dtype, g, dz, a->dx, s)) != hipSuccess)
+    return hip_fail(err, "dx");
+  if (a->dw != nullptr && (err = launch_linear_dw_tile(c.dtype, g, dz, a->dw, s)) != hipSuccess)
+    return hip_fail(err, "dw");
+  return MOE_OK;
+}
+
+moe_status moe_checkpoint_pack(int64_t rows, int32_t cols, int32_t dtype, const void* x,
+                               uint8_t* codes, float* scale, void* stream) {
+  clear_error();
+  const moe_status st = check_checkpoint(rows, cols, dtype, x, codes, scale);
+  if (st != MOE_OK || rows == 0) return st;
+  const hipError_t err =
+      launch_checkpoint_pack(dtype, x, rows, cols, codes, scale, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? MOE_OK : hip_fail(err, "checkpoint kernel");
+}
+
+moe_status moe_checkpoint_unpack(int64_t rows, int32_t cols, int32_t dtype, const uint8_t* codes,
+                                 const float* scale, void* x, void* stream) {
+  clear_error();
+  const moe_status st = check_checkpoint(rows, cols, dtype, x, codes, scale);
+  if (st != MOE_OK || rows == 0) return st;
+  const hipError_t err = launch_checkpoint_unpack(dtype, codes, scale, rows, cols, x,
+                                                  static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? MOE_OK : hip_fail(err, "checkpoint kernel");
+}
+
+moe_status moe_combine(int32_t T, int32_t k, int32_t n_rows, int32_t d, int32_t dtype,
+                       const void* rows, const int32_t* slot_row, const float* gate, void* y,
+                       void* stream) {
+  clear_error();
+  const moe_status st = check_combine(T, k, n_rows, d, dtype);
+  if (st != MOE_OK || T == 0) return st;
+  if ((rows == nullptr && n_rows > 0) || slot_row == nullptr || y == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "rows, slot_row or y is NULL");
+  if (!aligned16(rows) || !aligned16(y))
+    return fail(MOE_ERR_INVALID_ARG, "rows or y not 16-byte aligned");
+  const hipError_t err = launch_combine_rows(dtype, rows, slot_row, gate, n_rows, T, k, d, y,
+                                             static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? MOE_OK : hip_fail(err, "combine kernel");
+}
+
+moe_status moe_combine_backward(int32_t T, int32_t k, int32_t n_rows, int32_t d, int32_t dtype,
+                                const void* rows, const int32_t* slot_row, const float* gate,
+                                const void* dy, void* drows, float* dgate, void* stream) {
+  clear_error();
+  const moe_status st = check_combine(T, k, n_rows, d, dtype);
+  if (st != MOE_OK || T == 0) return st;
+  if (drows == nullptr && dgate == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "no gradient asked for");
+  if (slot_row == nullptr || dy == nullptr || (dgate != nullptr && rows == nullptr && n_rows > 0))
+    return fail(MOE_ERR_INVALID_ARG, "slot_row, dy or rows is NULL");
+  if (!aligned16(rows) || !aligned16(dy) || !aligned16(drows))
+    return fail(MOE_ERR_INVALID_ARG, "rows, dy or drows not 16-byte aligned");
+  const hipError_t err =
+      launch_combine_rows_backward(dtype, rows, slot_row, gate, dy, n_rows, T, k, d, drows, dgate,
+                                   static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? MOE_OK : hip_fail(err, "combine backward kernel");
+}
+
+}  // extern "C"

@@ -1,0 +1,296 @@
+// Grouped linear maps on register-staged 128 x 128 tiles: every type and
+// direction in one kernel.
+//
+//   forward  z[r] = x[src(r)] W_e^T + b_e,  y[r] = act(z[r]) + residual[r]
+//   dX       dX[r] = dz[r] W_e
+//   dW       dW_e = sum_r dz[r]^T x[src(r)]
+//
+// All three are C = A B^T over K, where an operand lies in memory either by
+// its rows (K contiguous: x, dz and W of the forward, dz of dX) or by its
+// K-rows (the rows of C's side contiguous: W of dX, dz and x of dW).  A
+// K-row operand is turned while it is stored to LDS, so both kinds feed the
+// same 16-byte MFMA fragments.
+//
+// One workgroup owns a 128 x 128 tile of one group, 4 wavefronts of 64 x 64;
+// a K step is 128 bytes of every row, fetched into registers while the step
+// before it is multiplied out of the other of two LDS buffers.  Rows past a
+// group's end repeat its last row (results not written); K-rows past it are
+// zeros in both operands, so that no NaN of a neighbouring group enters.
+#include "linear.h"
+#include "lds_ring.h"
+
+namespace moe {
+namespace {
+
+constexpr int kFwd = 0, kDx = 1, kDw = 2;
+constexpr int kBM = 128, kBN = 128;
+constexpr int kStgRow = kBN + 4;  // floats of a staged result row
+
+// One operand tile: 128 rows x 128 bytes.
+template <typename T, typename TW, bool KROW>
+struct Operand;
+
+// K contiguous: chunk c = tid + 256 i is 16 bytes (8 codes of an FP8 weight)
+// ch = c % 8 of tile row c / 8.
+template <typename T, typename TW>
+struct Operand<T, TW, false> {
+  static constexpr int CB = 16 * static_cast<int>(sizeof(TW)) / static_cast<int>(sizeof(T));
+  const char* p[4];
+  u32x4 v[4];
+  __device__ __forceinline__ void load(int step) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const char* q = p[i] + static_cast<size_t>(step) * 8 * CB;
+      if constexpr (sizeof(TW) == sizeof(T)) {
+        v[i] = *reinterpret_cast<const u32x4*>(q);
+      } else {
+        v[i] = e4m3x8_to_bf16(*reinterpret_cast<const uint2*>(q));
+      }
+    }
+  }
+  __device__ __forceinline__ void store(char* lds) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = threadIdx.x + 256 * i;
+      *reinterpret_cast<u32x4*>(lds + lds_swz(c >> 3, c & 7)) = v[i];
+    }
+  }
+};
+
+// K-rows: chunk c is 16 bytes (V columns) of K-row c % KE of the step.
+template <typename T>
+struct Operand<T, T, true> {
+  static constexpr int V = 16 / static_cast<int>(sizeof(T)), KE = 128 / static_cast<int>(sizeof(T));
+  const T* base;              // K-row 0 of the tile's first column
+  size_t ld;                  // elements of a K-row
+  int cols, krows;            // columns of the operand from the tile's first; K-rows there are
+  const int32_t* index;       // source row of K-row j, or null
+  int index_rows;             // rows the index may name
+  u32x4 v[4];
+  __device__ __forceinline__ void load(int step) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = threadIdx.x + 256 * i;
+      const int kk = step * KE + c % KE, col = c / KE * V;
+      v[i] = u32x4{0u, 0u, 0u, 0u};
+      if (kk < krows && col < cols) {
+        const int src = index != nullptr ? min(max(index[kk], 0), index_rows - 1) : kk;
+        v[i] = *reinterpret_cast<const u32x4*>(base + static_cast<size_t>(src) * ld + col);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(char* lds) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = threadIdx.x + 256 * i;
+      const int kb = c % KE * static_cast<int>(sizeof(T)), col = c / KE * V;
+      const T* e = reinterpret_cast<const T*>(&v[i]);
+#pragma unroll
+      for (int q = 0; q < V; ++q)
+        *reinterpret_cast<T*>(lds + lds_swz(col + q, kb >> 4) + (kb & 15)) = e[q];
+    }
+  }
+};
+
+template <typename T, typename TW, int MODE, bool GATED>
+__global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs g, const T* __restrict__ dz,
+                                                          T* __restrict__ out) {
+  constexpr int TILE = kBM * 128;
+  constexpr int STG = kBM * kStgRow * 4;
+  __shared__ __attribute__((aligned(1024))) char smem[4 * TILE > STG ? 4 * TILE : STG];
+  constexpr int COLS = GATED ? kBN / 2 : kBN;  // output columns of a tile
+
+  const int n_dim = MODE == kFwd ? g.out_dim : g.in_dim;  // columns of C
+  const int nt = (n_dim + COLS - 1) / COLS;
+  int e, m0, n0, valid, seg, count;
+  if constexpr (MODE == kDw) {
+    const int mt = (g.z_dim + kBM - 1) / kBM;
+    const int per = mt * nt;
+    e = blockIdx.x / per;
+    const int r = blockIdx.x - e * per;
+    m0 = (r % mt) * kBM;
+    n0 = (r / mt) * COLS;
+    const int2 range = group_range(g.offsets, e, g.rows);
+    seg = range.x;
+    count = range.y - range.x;
+    valid = min(kBM, g.z_dim - m0);
+  } else {
+    TileAt at;
+    int col;
+    if (!find_item(g.offsets, g.groups, g.rows, kBM, nt, at, col)) return;
+    e = at.e;
+    m0 = at.m * kBM;
+    n0 = col * COLS;
+    seg = at.begin;
+    count = at.end - at.begin;
+    valid = min(kBM, count - m0);
+  }
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 1, wn = wave & 1;
+  const size_t wmat = static_cast<size_t>(g.z_dim) * g.in_dim;
+
+  Operand<T, T, MODE == kDw> A;
+  Operand<T, TW, MODE != kFwd> B;
+  int nsteps;
+  if constexpr (MODE == kDw) {
+    A.base = dz + static_cast<size_t>(seg) * g.z_dim + m0;
+    A.ld = g.z_dim;
+    A.cols = g.z_dim - m0;
+    A.krows = count;
+    A.index = nullptr;
+    A.index_rows = 0;
+    const bool gather = g.row_index != nullptr;
+    B.base = static_cast<const T*>(g.x) + (gather ? 0 : static_cast<size_t>(seg) * g.in_dim) + n0;
+    B.ld = g.in_dim;
+    B.cols = g.in_dim - n0;
+    B.krows = count;
+    B.index = gather ? g.row_index + seg : nullptr;
+    B.index_rows = g.x_rows;
+    nsteps = (count + B.KE - 1) / B.KE;
+  } else {
+    const int k_dim = MODE == kFwd ? g.in_dim : g.z_dim;
+    const char* src = MODE == kFwd ? static_cast<const char*>(g.x)
+                                   : reinterpret_cast<const char*>(dz);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = tid + 256 * i;
+      const int row = seg + m0 + min(c >> 3, valid - 1);
+      int srow = row;
+      if (MODE == kFwd && g.row_index != nullptr)
+        srow = min(max(g.row_index[row], 0), g.x_rows - 1);
+      A.p[i] = src + static_cast<size_t>(srow) * k_dim * sizeof(T) + (c & 7) * 16;
+    }
+    nsteps = static_cast<int>(static_cast<size_t>(k_dim) * sizeof(T) / 128);
+    if constexpr (MODE == kFwd) {
+      const char* w = static_cast<const char*>(g.w) + e * wmat * sizeof(TW);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = tid + 256 * i, r = c >> 3;
+        // SwiGLU: the tile's gate rows, then the up rows of the same columns
+        const bool up = GATED && r >= COLS;
+        const int n = min(n0 + (up ? r - COLS : r), g.out_dim - 1) + (up ? g.out_dim : 0);
+        B.p[i] = w + (static_cast<size_t>(n) * g.in_dim) * sizeof(TW) + (c & 7) * B.CB;
+      }
+    } else {
+      B.base = static_cast<const T*>(g.w) + e * wmat + n0;
+      B.ld = g.in_dim;
+      B.cols = g.in_dim - n0;
+      B.krows = g.z_dim;
+      B.index = nullptr;
+      B.index_rows = 0;
+    }
+  }
+
+  f32x4 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  auto stage = [&](int q) -> char* { return smem + q * 2 * TILE; };
+  if (nsteps > 0) {
+    A.load(0);
+    B.load(0);
+    A.store(stage(0));
+    B.store(stage(0) + TILE);
+    lds_barrier();
+    for (int s = 0; s < nsteps; ++s) {
+      const bool more = s + 1 < nsteps;
+      if (more) {
+        A.load(s + 1);
+        B.load(s + 1);
+      }
+      const char* st = stage(s & 1);
+#pragma unroll
+      for (int kc = 0; kc < 2; ++kc) {
+        const int ch = kc * 4 + (lane >> 4);
+        u32x4 af[4], bf[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          af[i] = *reinterpret_cast<const u32x4*>(st + lds_swz(wm * 64 + i * 16 + (lane & 15), ch));
+          bf[i] = *reinterpret_cast<const u32x4*>(st + TILE +
+                                                  lds_swz(wn * 64 + i * 16 + (lane & 15), ch));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = Mfma<T>::step(af[i], bf[j], acc[i][j]);
+      }
+      if (more) {
+        A.store(stage((s + 1) & 1));
+        B.store(stage((s + 1) & 1) + TILE);
+      }
+      lds_barrier();
+    }
+  }
+
+  // the tile as fp32 rows in LDS, then 8 columns of a row per lane
+  float* const stg = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        stg[(wm * 64 + i * 16 + 4 * (lane >> 4) + r) * kStgRow + wn * 64 + j * 16 + (lane & 15)] =
+            acc[i][j][r];
+  lds_barrier();
+  for (int q = tid; q < kBM * COLS / 8; q += 256) {
+    const int row = q / (COLS / 8), c = q % (COLS / 8) * 8;
+    const bool ok = row < valid && n0 + c < n_dim;
+    float v[8], u[8];
+    load8<float>(stg + row * kStgRow + c, v);
+    if constexpr (MODE == kFwd) {
+      if (GATED) load8<float>(stg + row * kStgRow + COLS + c, u);
+      linear_epilogue8<T, GATED>(g, e, seg + m0 + row, n0 + c, ok, v, u);
+    } else if (ok) {
+      const size_t row0 = MODE == kDx ? static_cast<size_t>(seg) + m0 + row
+                                      : static_cast<size_t>(e) * g.z_dim + m0 + row;
+      store8<T>(out + row0 * g.in_dim + n0 + c, v);
+    }
+  }
+}
+
+template <typename T, typename TW, int MODE>
+hipError_t launch_t(const LinearArgs& g, const void* dz, void* out, hipStream_t s) {
+  const bool gated = MODE == kFwd && g.act == kActSwiglu;
+  const int cols = gated ? kBN / 2 : kBN;
+  const long nt = ((MODE == kFwd ? g.out_dim : g.in_dim) + cols - 1) / cols;
+  const long blocks = MODE == kDw ? static_cast<long>(g.groups) * ((g.z_dim + kBM - 1) / kBM) * nt
+                                  : item_grid(g.rows, g.groups, kBM, nt);
+  if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks));
+  if constexpr (MODE == kFwd) {
+    if (gated) {
+      hipLaunchKernelGGL((linear_tile_kernel<T, TW, MODE, true>), grid, dim3(256), 0, s, g,
+                         static_cast<const T*>(dz), static_cast<T*>(out));
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((linear_tile_kernel<T, TW, MODE, false>), grid, dim3(256), 0, s, g,
+                     static_cast<const T*>(dz), static_cast<T*>(out));
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_linear_tile(int dtype, bool wfp8, const LinearArgs& g, hipStream_t s) {
+  if (wfp8) return launch_t<bf16_t, uint8_t, kFwd>(g, nullptr, nullptr, s);
+  if (dtype == 1) return launch_t<bf16_t, bf16_t, kFwd>(g, nullptr, nullptr, s);
+  return launch_t<float, float, kFwd>(g, nullptr, nullptr, s);
+}
+
+hipError_t launch_linear_dx_tile(int dtype, const LinearArgs& g, const void* dz, void* dx,
+                                 hipStream_t s) {
+  if (dtype == 1) return launch_t<bf16_t, bf16_t, kDx>(g, dz, dx, s);
+  return launch_t<float, float, kDx>(g, dz, dx, s);
+}
+
+hipError_t launch_linear_dw_tile(int dtype, const LinearArgs& g, const void* dz, void* dw,
+                                 hipStream_t s) {
+  if (dtype == 1) return launch_t<bf16_t, bf16_t, kDw>(g, dz, dw, s);
+  return launch_t<float, float, kDw>(g, dz, dw, s);
+}
+
+}  // namespace moe

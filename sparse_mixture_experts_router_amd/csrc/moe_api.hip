@@ -2,6 +2,7 @@
 // launch sequence of the layer forward.  Every launch goes on the caller's
 // stream; nothing here allocates, frees or waits on the device.
 #include "moe.h"
+#include "api_error.h"
 #include "moe_internal.h"
 #include "lds_ring.h"  // kRowBytes: the routing block's K step
 
@@ -12,9 +13,10 @@
 #include <string.h>
 
 namespace moe {
-namespace {
 
-thread_local char g_last_error[256] = "";
+static thread_local char g_last_error[256] = "";
+
+void clear_error() { g_last_error[0] = '\0'; }
 
 moe_status fail(moe_status st, const char* what) {
   snprintf(g_last_error, sizeof(g_last_error), "%s", what);
@@ -26,18 +28,11 @@ moe_status hip_fail(hipError_t err, const char* where) {
   return MOE_ERR_HIP;
 }
 
-constexpr size_t kAlign = 256;
-constexpr int R_COUNT_MAX = 32;
-
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // Compute units of the current device, asked of the runtime once per device:
 // the attribute query costs a host round trip that every decode step would
 // otherwise pay.  Devices past the table are asked on every call.
 constexpr int kCuCacheDevices = 64;
-std::atomic<int> g_cus[kCuCacheDevices];  // 0: not asked yet
+static std::atomic<int> g_cus[kCuCacheDevices];  // 0: not asked yet
 
 int device_cus() {
   int dev = 0;
@@ -53,6 +48,15 @@ int device_cus() {
   if (dev < kCuCacheDevices) g_cus[dev].store(cus, std::memory_order_relaxed);
   return cus;
 }
+
+namespace {
+
+constexpr size_t kAlign = 256;
+constexpr int R_COUNT_MAX = 32;
+
+size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Row tiles that a grouped GEMM with `bm`-row tiles can need in the worst
 // case: each routed expert with c_e > 0 rows needs ceil(c_e / bm) tiles, and

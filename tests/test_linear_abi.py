@@ -1,0 +1,227 @@
+"""The calls for experts of one's own without a GPU: their structs mirror the
+header, sizes are answered, and bad arguments are refused on the host before
+anything is launched."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import sparse_mixture_experts_router_amd as moe
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "moe.h")
+
+pytestmark = pytest.mark.skipif(not os.path.exists(moe.LIB_PATH),
+                                reason="libmoe.so not built (run __graft_entry__.build())")
+
+FAKE = 1 << 20  # a 256-byte aligned non-null address; never dereferenced on these paths
+BIG = 1 << 40
+INVALID, UNSUPPORTED, WORKSPACE = (moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED,
+                                   moe.MOE_ERR_WORKSPACE)
+
+
+def _body(name):
+    with open(HEADER) as fh:
+        text = re.sub(r"/\*.*?\*/", "", fh.read(), flags=re.S)
+    return re.search(r"typedef struct \{([^}]*)\} " + name + ";", text).group(1)
+
+
+@pytest.mark.parametrize("name,struct", [("moe_linear_config", moe.MoELinearConfig),
+                                         ("moe_linear_args", moe.MoELinearArgs),
+                                         ("moe_linear_grad_args", moe.MoELinearGradArgs)])
+def test_structs_match_the_header(name, struct):
+    assert re.findall(r"(\w+);", _body(name)) == [f for f, _ in struct._fields_]
+
+
+def test_activation_codes_match_the_header():
+    with open(HEADER) as fh:
+        codes = dict(re.findall(r"MOE_ACT_(\w+) = (\d+)", fh.read()))
+    assert [codes[a.upper()] for a in moe.ACTIVATIONS] == [str(i) for i in range(5)]
+
+
+def cfg(**over):
+    c = moe.make_linear_config(100, 4, 128, 192, activation="gelu")
+    for k, v in over.items():
+        setattr(c, k, v)
+    return c
+
+
+BAD_CONFIGS = [
+    (dict(rows=-1), INVALID), (dict(x_rows=-1), INVALID), (dict(groups=0), INVALID),
+    (dict(in_dim=0), INVALID), (dict(out_dim=-64), INVALID), (dict(dtype=2), INVALID),
+    (dict(weight_format=2), INVALID), (dict(activation=5), INVALID), (dict(activation=-1), INVALID),
+    (dict(groups=513), UNSUPPORTED), (dict(in_dim=96), UNSUPPORTED), (dict(out_dim=100), UNSUPPORTED),
+    (dict(in_dim=(1 << 20) + 64), UNSUPPORTED), (dict(rows=1 << 30), UNSUPPORTED),
+    (dict(x_rows=1 << 30), UNSUPPORTED),
+    (dict(dtype=moe.MOE_F32, weight_format=moe.MOE_WEIGHTS_FP8_E4M3), UNSUPPORTED),
+    (dict(rows=(1 << 30) - 1, out_dim=1 << 20), UNSUPPORTED),          # too many tiles
+    (dict(groups=512, in_dim=1 << 20, out_dim=1 << 20), UNSUPPORTED),  # too many tiles of dw
+]
+
+
+def forward(c, a, ws=FAKE, nbytes=BIG):
+    return moe.lib().moe_grouped_linear(None if c is None else ctypes.byref(c),
+                                        None if a is None else ctypes.byref(a), ws, nbytes, None)
+
+
+def backward(c, a, ws=FAKE, nbytes=BIG):
+    return moe.lib().moe_grouped_linear_backward(None if c is None else ctypes.byref(c),
+                                                 None if a is None else ctypes.byref(a), ws,
+                                                 nbytes, None)
+
+
+def args(**over):
+    a = dict(x=FAKE, offsets=FAKE, w=FAKE, y=FAKE)
+    a.update(over)
+    return moe.MoELinearArgs(**a)
+
+
+def grads(**over):
+    a = dict(x=FAKE, offsets=FAKE, w=FAKE, dy=FAKE, z_codes=FAKE, z_scale=FAKE, dx=FAKE, dw=FAKE,
+             dbias=FAKE)
+    a.update(over)
+    return moe.MoELinearGradArgs(**a)
+
+
+@pytest.mark.parametrize("over,status", BAD_CONFIGS, ids=[str(o) for o, _ in BAD_CONFIGS])
+def test_bad_configurations(over, status):
+    c = cfg(**over)
+    assert forward(c, args()) == status and moe.lib().moe_last_error()
+    assert moe.moe_linear_workspace_size(c) == 0
+    assert moe.moe_linear_backward_workspace_size(c) == 0
+    assert backward(c, grads()) == status
+
+
+def test_workspace_sizes():
+    c = cfg()
+    assert moe.moe_linear_workspace_size(c) % 256 == 0
+    n = moe.moe_linear_backward_workspace_size(c)
+    assert n % 256 == 0 and n >= 100 * 192 * 2
+    assert moe.moe_linear_backward_workspace_size(cfg(rows=0)) > 0
+    assert moe.moe_group_workspace_size(0, 8, 2) > 0
+    assert moe.moe_group_workspace_size(1 << 20, 512, 16) >= 512 * 4
+    for bad in ((-1, 8, 2), (4, 0, 2), (4, 8, 0), (4, 513, 2), (4, 32, 17), (1 << 27, 32, 16)):
+        assert moe.moe_group_workspace_size(*bad) == 0
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(x=None), INVALID), (dict(offsets=None), INVALID), (dict(w=None), INVALID),
+    (dict(y=None), INVALID), (dict(y=FAKE + 8), INVALID), (dict(x=FAKE + 2), INVALID),
+    (dict(bias=FAKE + 4), INVALID), (dict(residual=FAKE + 8), INVALID),
+    (dict(w_scale=FAKE), INVALID),            # weights are not FP8
+    (dict(z_codes=FAKE), INVALID), (dict(z_scale=FAKE), INVALID),
+    (dict(row_index=FAKE), INVALID),          # x_rows is 0
+])
+def test_forward_refusals(over, status):
+    assert forward(cfg(), args(**over)) == status
+    assert moe.lib().moe_last_error()
+
+
+def test_forward_refusals_by_configuration():
+    assert forward(None, args()) == INVALID
+    assert forward(cfg(), None) == INVALID
+    assert forward(cfg(x_rows=7), args()) == INVALID  # no row_index
+    assert forward(cfg(weight_format=moe.MOE_WEIGHTS_FP8_E4M3), args()) == INVALID  # no scales
+    assert forward(cfg(), args(), ws=None) == WORKSPACE
+    assert forward(cfg(), args(), ws=FAKE + 64) == WORKSPACE
+    assert forward(cfg(), args(), nbytes=0) == WORKSPACE
+    assert forward(cfg(rows=0), args(x=None, y=None)) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dx=None, dw=None, dbias=None), INVALID), (dict(offsets=None), INVALID),
+    (dict(dy=None), INVALID), (dict(w=None), INVALID), (dict(x=None), INVALID),
+    (dict(z_codes=None), INVALID), (dict(z_scale=None), INVALID), (dict(row_index=FAKE), INVALID),
+    (dict(dx=FAKE + 8), INVALID), (dict(dw=FAKE + 2), INVALID), (dict(dbias=FAKE + 4), INVALID),
+])
+def test_backward_refusals(over, status):
+    assert backward(cfg(), grads(**over)) == status
+    assert moe.lib().moe_last_error()
+
+
+def test_backward_refusals_by_configuration():
+    assert backward(None, grads()) == INVALID
+    assert backward(cfg(), None) == INVALID
+    assert backward(cfg(weight_format=moe.MOE_WEIGHTS_FP8_E4M3), grads()) == UNSUPPORTED
+    assert backward(cfg(x_rows=5), grads()) == INVALID
+    need = moe.moe_linear_backward_workspace_size(cfg())
+    assert backward(cfg(), grads(), nbytes=need - 1) == WORKSPACE
+    assert backward(cfg(), grads(), ws=None) == WORKSPACE
+    assert backward(cfg(rows=0), grads(dw=None, dbias=None, dx=None)) == moe.MOE_OK
+
+
+def test_group_refusals():
+    lib = moe.lib()
+
+    def call(T=8, N=4, k=2, cap=0, idx=FAKE, off=FAKE, tok=FAKE, slot=FAKE, ws=FAKE, n=BIG):
+        return lib.moe_group_rows(T, N, k, cap, idx, off, tok, slot, ws, n, None)
+
+    assert call(T=-1) == INVALID and call(N=0) == INVALID and call(k=0) == INVALID
+    assert call(cap=-1) == INVALID and call(N=513) == UNSUPPORTED and call(k=17) == UNSUPPORTED
+    assert call(T=1 << 29) == UNSUPPORTED
+    for name in ("idx", "off", "tok", "slot"):
+        assert call(**{name: None}) == INVALID
+    assert call(ws=None) == WORKSPACE and call(ws=FAKE + 4) == WORKSPACE
+    assert call(n=8) == WORKSPACE
+
+
+def test_checkpoint_refusals():
+    lib = moe.lib()
+    for fn in (lib.moe_checkpoint_pack, lib.moe_checkpoint_unpack):
+        assert fn(-1, 64, 1, FAKE, FAKE, FAKE, None) == INVALID
+        assert fn(4, 0, 1, FAKE, FAKE, FAKE, None) == INVALID
+        assert fn(4, 100, 1, FAKE, FAKE, FAKE, None) == UNSUPPORTED
+        assert fn(1 << 40, 64, 1, FAKE, FAKE, FAKE, None) == UNSUPPORTED
+        assert fn(4, 64, 3, FAKE, FAKE, FAKE, None) == INVALID
+        for i in range(3):
+            p = [FAKE] * 3
+            p[i] = None
+            assert fn(4, 64, 1, *p, None) == INVALID
+        assert fn(0, 64, 1, None, None, None, None) == moe.MOE_OK
+    assert lib.moe_checkpoint_pack(4, 64, 1, FAKE + 8, FAKE, FAKE, None) == INVALID
+    assert lib.moe_checkpoint_unpack(4, 64, 1, FAKE + 8, FAKE, FAKE, None) == INVALID
+
+
+def test_combine_refusals():
+    lib = moe.lib()
+
+    def fwd(T=4, k=2, n=8, d=64, dt=1, rows=FAKE, slot=FAKE, gate=FAKE, y=FAKE):
+        return lib.moe_combine(T, k, n, d, dt, rows, slot, gate, y, None)
+
+    def bwd(T=4, k=2, n=8, d=64, dt=1, rows=FAKE, slot=FAKE, gate=FAKE, dy=FAKE, dr=FAKE, dg=FAKE):
+        return lib.moe_combine_backward(T, k, n, d, dt, rows, slot, gate, dy, dr, dg, None)
+
+    for call in (fwd, bwd):
+        assert call(T=-1) == INVALID and call(k=0) == INVALID and call(n=-1) == INVALID
+        assert call(d=0) == INVALID and call(dt=4) == INVALID
+        assert call(d=96) == UNSUPPORTED and call(k=17) == UNSUPPORTED
+        assert call(T=1 << 24) == UNSUPPORTED
+        assert call(rows=None) == INVALID and call(slot=None) == INVALID
+        assert call(rows=FAKE + 8) == INVALID
+        assert call(T=0) == moe.MOE_OK
+    assert fwd(y=None) == INVALID and fwd(y=FAKE + 4) == INVALID
+    assert bwd(dy=None) == INVALID and bwd(dr=None, dg=None) == INVALID
+    assert bwd(dr=FAKE + 8) == INVALID
+
+
+def test_binding_refuses_tensors():
+    """What the C ABI cannot see: placement, type, shape and layout."""
+    c = moe.make_linear_config(8, 2, 64, 64)
+    t = dict(x=torch.zeros(8, 64, dtype=torch.bfloat16), offsets=torch.zeros(3, dtype=torch.int32),
+             w=torch.zeros(2, 64, 64, dtype=torch.bfloat16),
+             y=torch.zeros(8, 64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="device tensor"):
+        moe.moe_grouped_linear(c, t["x"], t["offsets"], t["w"], t["y"],
+                               workspace=torch.zeros(256, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="device tensor"):
+        moe.moe_checkpoint_pack(t["x"], torch.zeros(8, 64, dtype=torch.uint8), torch.zeros(8, 1))
+    with pytest.raises(ValueError):
+        moe.make_linear_config(8, 2, 64, 64, activation="tanh")
+    with pytest.raises(ValueError):
+        moe.make_linear_config(8, 2, 64, 64, dtype=torch.float16)
+    with pytest.raises(moe.MoEError):
+        moe.alloc_linear_workspace(moe.make_linear_config(8, 2, 60, 64), "cpu")
+    with pytest.raises(moe.MoEError):
+        moe.alloc_group_workspace(8, 1000, 2, "cpu")
