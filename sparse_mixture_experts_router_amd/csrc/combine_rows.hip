@@ -111,7 +111,24 @@ __global__ __launch_bounds__(256) void combine_rows_backward_kernel(
   }
 }
 
+// One wavefront per row.
+__global__ __launch_bounds__(256) void gather_rows_kernel(LinearArgs g, bf16_t* __restrict__ xg) {
+  const int r = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (r >= min(g.offsets[g.groups], g.rows)) return;
+  const size_t src = min(max(g.row_index[r], 0), g.x_rows - 1);
+  const bf16_t* const x = static_cast<const bf16_t*>(g.x) + src * g.in_dim;
+  bf16_t* const o = xg + static_cast<size_t>(r) * g.in_dim;
+  for (int c = lane * 8; c < g.in_dim; c += 512)
+    *reinterpret_cast<u32x4*>(o + c) = *reinterpret_cast<const u32x4*>(x + c);
+}
+
 }  // namespace
+
+hipError_t launch_gather_rows(const LinearArgs& g, void* xg, hipStream_t s) {
+  hipLaunchKernelGGL(gather_rows_kernel, dim3((g.rows + 3) / 4), dim3(256), 0, s, g,
+                     static_cast<bf16_t*>(xg));
+  return hipGetLastError();
+}
 
 hipError_t launch_combine_rows(int dtype, const void* rows, const int32_t* slot_row,
                                const float* gate, int n_rows, int T_, int k, int d, void* y,

@@ -50,6 +50,15 @@ hipError_t launch_linear_dx_tile(int dtype, const LinearArgs& g, const void* dz,
 hipError_t launch_linear_dw_tile(int dtype, const LinearArgs& g, const void* dz, void* dw,
                                  hipStream_t s);
 
+// The same three on 256 x 256 tiles (bf16, weights in bf16): dW takes x's
+// rows in order, without row_index.
+bool linear_mfma_fits(const LinearArgs& g);
+hipError_t launch_linear_mfma(const LinearArgs& g, hipStream_t s);
+hipError_t launch_linear_mfma_dx(const LinearArgs& g, const void* dz, void* dx, hipStream_t s);
+hipError_t launch_linear_mfma_dw(const LinearArgs& g, const void* dz, void* dw, hipStream_t s);
+// xg[r] = x[row_index[r]] for the rows that belong to a group (bf16).
+hipError_t launch_gather_rows(const LinearArgs& g, void* xg, hipStream_t s);
+
 // Row tiles of kActRows rows that the activation's backward works in; the
 // most there can be for `rows` rows in `groups` groups.
 constexpr int kActRows = 64;

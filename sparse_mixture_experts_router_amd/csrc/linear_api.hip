@@ -77,7 +77,7 @@ LinearArgs linear_args(const moe_linear_config& c) {
 
 // Workspace of the backward.
 struct BackSpace {
-  size_t dz, partial, total;
+  size_t dz, partial, xg, total;
 };
 BackSpace back_space(const moe_linear_config& c) {
   const size_t eb = c.dtype == MOE_BF16 ? 2 : 4, z = z_dim(c);
@@ -87,6 +87,8 @@ BackSpace back_space(const moe_linear_config& c) {
   if (c.activation != MOE_ACT_NONE) o += align_up(static_cast<size_t>(c.rows) * z * eb);
   b.partial = o;
   o += align_up(static_cast<size_t>(act_tiles(c.rows, c.groups)) * z * 4);
+  b.xg = o;
+  if (c.dtype == MOE_BF16 && c.x_rows > 0) o += align_up(static_cast<size_t>(c.rows) * c.in_dim * eb);
   b.total = o > 0 ? o : kAlign;
   return b;
 }
@@ -190,7 +192,11 @@ moe_status moe_grouped_linear(const moe_linear_config* cfg, const moe_linear_arg
   g.y = a->y;
   g.z_codes = a->z_codes;
   g.z_scale = a->z_scale;
-  const hipError_t err = launch_linear_tile(c.dtype, fp8, g, static_cast<hipStream_t>(stream));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool many = c.rows > 48L * c.groups;
+  const hipError_t err = many && c.dtype == MOE_BF16 && !fp8 && linear_mfma_fits(g)
+                             ? launch_linear_mfma(g, s)
+                             : launch_linear_tile(c.dtype, fp8, g, s);
   return err == hipSuccess ? MOE_OK : hip_fail(err, "grouped linear kernel");
 }
 
@@ -248,11 +254,24 @@ moe_status moe_grouped_linear_backward(const moe_linear_config* cfg,
   }
   if (a->dbias != nullptr && (err = launch_bias_grad(g, partial, a->dbias, s)) != hipSuccess)
     return hip_fail(err, "bias gradient");
-  if (c.rows > 0 && a->dx != nullptr &&
-      (err = launch_linear_dx_tile(c.dtype, g, dz, a->dx, s)) != hipSuccess)
-    return hip_fail(err, "dx");
-  if (a->dw != nullptr && (err = launch_linear_dw_tile(c.dtype, g, dz, a->dw, s)) != hipSuccess)
-    return hip_fail(err, "dw");
+  const bool bf16 = c.dtype == MOE_BF16;
+  if (c.rows > 0 && a->dx != nullptr) {
+    err = bf16 ? launch_linear_mfma_dx(g, dz, a->dx, s)
+               : launch_linear_dx_tile(c.dtype, g, dz, a->dx, s);
+    if (err != hipSuccess) return hip_fail(err, "dx");
+  }
+  if (a->dw != nullptr) {
+    if (bf16 && g.row_index != nullptr && c.rows > 0) {
+      // the large tiles stage x by its rows in order
+      if ((err = launch_gather_rows(g, base + b.xg, s)) != hipSuccess)
+        return hip_fail(err, "gather of x");
+      g.x = base + b.xg;
+    }
+    if (bf16) g.row_index = nullptr;
+    err = bf16 ? launch_linear_mfma_dw(g, dz, a->dw, s)
+               : launch_linear_dw_tile(c.dtype, g, dz, a->dw, s);
+    if (err != hipSuccess) return hip_fail(err, "dw");
+  }
   return MOE_OK;
 }
 
