@@ -285,37 +285,69 @@ __device__ __forceinline__ void pack_block(const float* v, bool ok, uint8_t* cod
   if ((threadIdx.x & 7) == 0) *scale = m / kCkptMax;
 }
 
+// 8 floats at p (fill where p is null or the columns lie past the end): the
+// bias or the FP8 scales of a lane's columns.
+__device__ __forceinline__ void load_cols8(const float* p, size_t at, bool ok, float fill,
+                                           float* v) {
+  if (p != nullptr && ok) {
+    load8<float>(p + at, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fill;
+  }
+}
+// 8 values of the residual (0 where there is none), widened by unpack8 when
+// they are used, so that a caller can have many in flight.
+template <typename T> struct Raw8;
+template <> struct Raw8<bf16_t> {
+  u32x4 r;
+  __device__ __forceinline__ void load(const bf16_t* p) {
+    r = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  }
+  __device__ __forceinline__ void zero() { r = u32x4{0u, 0u, 0u, 0u}; }
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float(i & 1 ? r[i / 2] & 0xffff0000u : r[i / 2] << 16);
+  }
+};
+template <> struct Raw8<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const f32x4*>(p);
+    b = *reinterpret_cast<const f32x4*>(p + 4);
+  }
+  __device__ __forceinline__ void zero() { a = b = f32x4{0.f, 0.f, 0.f, 0.f}; }
+  __device__ __forceinline__ float get(int i) const { return i < 4 ? a[i] : b[i - 4]; }
+};
+template <typename T>
+__device__ __forceinline__ void load_residual(const LinearArgs& g, long row, int n, bool ok,
+                                              Raw8<T>& r) {
+  if (g.residual != nullptr && ok)
+    r.load(static_cast<const T*>(g.residual) + static_cast<size_t>(row) * g.out_dim + n);
+  else
+    r.zero();
+}
+// y is not read again by the launch that writes it: past the caches, where
+// the rows of x and W that other tiles use stay longer.
+template <typename T> __device__ __forceinline__ void store_once8(T* p, const float* v);
+template <> __device__ __forceinline__ void store_once8<bf16_t>(bf16_t* p, const float* v) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = static_cast<uint32_t>(f32_to_bf16(v[2 * i])) |
+           (static_cast<uint32_t>(f32_to_bf16(v[2 * i + 1])) << 16);
+  __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p));
+}
+template <> __device__ __forceinline__ void store_once8<float>(float* p, const float* v) {
+  store8<float>(p, v);
+}
+
 // The epilogue of the forward on 8 columns of one row: columns n .. n + 7 of
 // y, n a multiple of 8, 8 neighbouring lanes holding a whole 64-column block.
-// v: the products x W^T (SwiGLU: v the gate's, u the up projection's).
+// v: z's columns (SwiGLU: v the gate's, u the up projection's), bias included.
 template <typename T, bool GATED>
-__device__ __forceinline__ void linear_epilogue8(const LinearArgs& g, int e, long row, int n,
-                                                 bool ok, float* v, float* u) {
-  const size_t eo = static_cast<size_t>(e) * g.z_dim;
-  if (ok) {
-    if (g.w_scale != nullptr) {
-      float t[8];
-      load8<float>(g.w_scale + eo + n, t);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= t[i];
-      if (GATED) {
-        load8<float>(g.w_scale + eo + g.out_dim + n, t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] *= t[i];
-      }
-    }
-    if (g.bias != nullptr) {
-      float t[8];
-      load8<float>(g.bias + eo + n, t);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += t[i];
-      if (GATED) {
-        load8<float>(g.bias + eo + g.out_dim + n, t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] += t[i];
-      }
-    }
-  }
+__device__ __forceinline__ void linear_epilogue8(const LinearArgs& g, long row, int n, bool ok,
+                                                 const float* v, const float* u,
+                                                 const Raw8<T>& res) {
   if (g.z_codes != nullptr) {
     const size_t zo = static_cast<size_t>(row) * g.z_dim;
     uint8_t* c = g.z_codes + zo;
@@ -348,14 +380,9 @@ __device__ __forceinline__ void linear_epilogue8(const LinearArgs& g, int e, lon
         for (int i = 0; i < 8; ++i) h[i] = v[i];
     }
   }
-  const size_t yo = static_cast<size_t>(row) * g.out_dim + n;
-  if (g.residual != nullptr) {
-    float t[8];
-    load8<T>(static_cast<const T*>(g.residual) + yo, t);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] += t[i];
-  }
-  store8<T>(static_cast<T*>(g.y) + yo, h);
+  for (int i = 0; i < 8; ++i) h[i] += res.get(i);
+  store_once8<T>(static_cast<T*>(g.y) + static_cast<size_t>(row) * g.out_dim + n, h);
 }
 
 }  // namespace moe

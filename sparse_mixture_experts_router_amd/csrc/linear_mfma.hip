@@ -7,7 +7,8 @@
 //
 // bound by the matrix cores: a tile does 512 operations for each byte that it
 // stages.  One workgroup of 8 wavefronts, two on each SIMD, owns a tile and
-// the whole LDS; a wavefront accumulates 64 x 128 of it in AGPRs.  A stage is
+// the whole LDS; a wavefront accumulates a quarter of the rows and half of the
+// columns in AGPRs.  A stage is
 // 64 elements of K.  The wavefronts of a SIMD take turns: while one runs its
 // 64 MFMAs of a stage from registers, the other issues its loads (global ->
 // LDS, no registers) and reads its 24 fragments of the next stage; a barrier
@@ -31,7 +32,7 @@ constexpr int kT = 256;                 // rows and (effective) columns of a til
 constexpr int kBuf = kT * kLineBytes;   // bytes of a staged operand
 constexpr int kABufs = 2, kBBufs = 3;
 constexpr int kLds = (kABufs + kBBufs) * kBuf;  // 160 KB
-constexpr int kWM = 64, kWN = 128, kMB = kWM / 16, kNB = kWN / 16;
+constexpr int kMB = 4, kWN = 128, kNB = kWN / 16;  // a wavefront's 16-row and 16-column blocks
 constexpr int kStgPitch = 64 * 4 + 16;  // bytes of a staged result row of 64 columns
 static_assert(8 * 2 * 32 * kStgPitch <= kLds, "staging space");
 
@@ -152,9 +153,11 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int grp = wave >> 2, q = wave & 3;  // rows 64 q .., effective columns 128 grp ..
-  const int mlive =
-      __builtin_amdgcn_readfirstlane(min(max((valid - q * kWM + 15) / 16, 0), kMB));
+  // Wavefront (grp, q) computes the 16-row blocks q, q + 4, q + 8, q + 12 of
+  // the tile, effective columns 128 grp ...  Taking turns, the four share the
+  // rows of a partly filled tile: its phases run the MFMAs of `mlive` blocks.
+  const int grp = wave >> 2, q = wave & 3;
+  const int mlive = __builtin_amdgcn_readfirstlane(min(max((valid - q * 16 + 63) / 64, 0), kMB));
   const size_t wmat = static_cast<size_t>(g.z_dim) * g.in_dim;
   const bf16_t* const w = static_cast<const bf16_t*>(g.w) + e * wmat;
 
@@ -256,11 +259,11 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
     if (GATED) return (j < kNB / 2 ? 0 : COLS) + grp * 64 + (j % (kNB / 2)) * 16;
     return grp * kWN + j * 16;
   };
-  // K-row operand: N blocks from tile column c0 + 16 i into fr[0 .. 1][first + i].
+  // K-row operand: N blocks from tile column c0 + i dc into fr[0 .. 1][first + i].
   // The addresses are made anew from an opaque key, so that none lives in a
   // register through the loop.
   u32x4 fr[2][kMB + kNB];
-  auto read_krows = [&](const char* buf, auto n_, int first, int c0) {
+  auto read_krows = [&](const char* buf, auto n_, int first, int c0, int dc) {
     constexpr int N = decltype(n_)::value;
     uint32_t kx = static_cast<uint32_t>(kkey) << 4;
     uint32_t la = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
@@ -270,7 +273,7 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
     uint32_t addr[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      addr[i] = la + ((static_cast<uint32_t>((c0 + i * 16) >> 3) << 4) ^ kx);
+      addr[i] = la + ((static_cast<uint32_t>((c0 + i * dc) >> 3) << 4) ^ kx);
     read_krow_blocks<N>(&fr[0][first], &fr[1][first], addr);
   };
 
@@ -318,7 +321,7 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
 #pragma unroll
               for (int i = 0; i < LIVE; ++i)
                 fr[t][i] =
-                    *reinterpret_cast<const u32x4*>(a + (q * kWM + i * 16) * kLineBytes + fl);
+                    *reinterpret_cast<const u32x4*>(a + (i * 64 + q * 16) * kLineBytes + fl);
             }
             if constexpr (!BK) {
 #pragma unroll
@@ -326,10 +329,10 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
                 fr[t][kMB + j] = *reinterpret_cast<const u32x4*>(b + b_row(j) * kLineBytes + fl);
             }
           }
-          if constexpr (AK) read_krows(a, live_, 0, q * kWM);
+          if constexpr (AK) read_krows(a, live_, 0, q * 16, 64);
           if constexpr (BK) {
-            read_krows(b, CInt<4>{}, kMB, grp * kWN);
-            read_krows(b, CInt<4>{}, kMB + 4, grp * kWN + 64);
+            read_krows(b, CInt<4>{}, kMB, grp * kWN, 16);
+            read_krows(b, CInt<4>{}, kMB + 4, grp * kWN + 64, 16);
           }
         }
         // fragments are in registers; half 0 leaves A(p + 1) in flight, half 1
@@ -369,9 +372,10 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
       stage_barrier();  // nothing is in flight, nobody reads the buffers
     };
     auto run_live = [&](auto grp_, auto nt_) {
-      if (mlive > kMB / 2) run(CInt<kMB>{}, grp_, nt_);
-      else if (mlive > kMB / 4) run(CInt<kMB / 2>{}, grp_, nt_);
-      else if (mlive > 0) run(CInt<kMB / 4>{}, grp_, nt_);
+      if (mlive == 4 || (AK && mlive == 3)) run(CInt<4>{}, grp_, nt_);
+      else if (mlive == 3) run(CInt<AK ? 4 : 3>{}, grp_, nt_);
+      else if (mlive == 2) run(CInt<2>{}, grp_, nt_);
+      else if (mlive == 1) run(CInt<1>{}, grp_, nt_);
       else run(CInt<0>{}, grp_, nt_);
     };
     if (grp == 0) run_live(CInt<0>{}, CInt<0>{});
@@ -383,11 +387,35 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
   // 32 rows of the wavefront's block at a time through LDS, as two fp32
   // arrays of 64 columns (SwiGLU: gate and up of the same columns), then 8
   // columns of a row per lane: whole 128-byte lines of y, and the 8 lanes of
-  // a 64-column block agree on its checkpoint scale.
+  // a 64-column block agree on its checkpoint scale.  A lane's columns are the
+  // same throughout, so the bias is read once; the residual's rows are asked
+  // for before the staging.
   mfma_drain();
   char* const stg = smem + wave * 2 * 32 * kStgPitch;
+  const int c = (lane & 7) * 8;
+  const int n = n0 + (GATED ? grp * 64 : grp * kWN) + c;
+  const bool in0 = n < n_dim, in1 = !GATED && n + 64 < n_dim;
+  float b0[8], b1[8];
+  if constexpr (MODE == kFwd) {
+    const size_t eo = static_cast<size_t>(e) * g.z_dim + n;
+    load_cols8(g.bias, eo, in0, 0.f, b0);
+    load_cols8(g.bias, eo + (GATED ? g.out_dim : 64), GATED ? in0 : in1, 0.f, b1);
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    auto tile_row = [&](int k) {
+      const int lr = k * 8 + (lane >> 3);
+      return (2 * h + (lr >> 4)) * 64 + q * 16 + (lr & 15);
+    };
+    Raw8<bf16_t> r0[4], r1[4];
+    if constexpr (MODE == kFwd) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = tile_row(k);
+        load_residual<bf16_t>(g, seg + m0 + row, n, row < valid && in0, r0[k]);
+        if (!GATED) load_residual<bf16_t>(g, seg + m0 + row, n + 64, row < valid && in1, r1[k]);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -397,33 +425,31 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
           *reinterpret_cast<float*>(stg + (j / 4 * 32 + i * 16 + 4 * (lane >> 4) + r) * kStgPitch +
                                     ((j % 4) * 16 + (lane & 15)) * 4) = acc[2 * h + i][j][r];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // own rows only: no barrier
-#pragma unroll 1
+#pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int lr = k * 8 + (lane >> 3), c = (lane & 7) * 8;
-      const int row = q * kWM + h * 32 + lr;
-      const float* const s0 = reinterpret_cast<const float*>(stg + lr * kStgPitch) + c;
-      const float* const s1 = reinterpret_cast<const float*>(stg + (32 + lr) * kStgPitch) + c;
-      float v[8];
-      load8<float>(s0, v);
-      if constexpr (GATED) {
-        float u[8];
-        load8<float>(s1, u);
-        const int n = n0 + grp * 64 + c;
-        linear_epilogue8<bf16_t, true>(g, e, seg + m0 + row, n, row < valid && n < n_dim, v, u);
-      } else {
-#pragma unroll 1
-        for (int b = 0; b < 2; ++b) {  // the two 64-column blocks
-          const int n = n0 + grp * kWN + b * 64 + c;
-          const bool ok = row < valid && n < n_dim;
-          if (b == 1) load8<float>(s1, v);
-          if constexpr (MODE == kFwd) {
-            linear_epilogue8<bf16_t, false>(g, e, seg + m0 + row, n, ok, v, nullptr);
-          } else if (ok) {
-            const size_t r0 = MODE == kDx ? static_cast<size_t>(seg) + m0 + row
-                                          : static_cast<size_t>(e) * g.z_dim + m0 + row;
-            store8<bf16_t>(out + r0 * g.in_dim + n, v);
-          }
+      const int lr = k * 8 + (lane >> 3), row = tile_row(k);
+      float v[8], u[8];
+      load8<float>(reinterpret_cast<const float*>(stg + lr * kStgPitch) + c, v);
+      load8<float>(reinterpret_cast<const float*>(stg + (32 + lr) * kStgPitch) + c, u);
+      if constexpr (MODE == kFwd) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] += b0[i];
+          u[i] += b1[i];
         }
+        const long r = static_cast<long>(seg) + m0 + row;
+        if constexpr (GATED) {
+          linear_epilogue8<bf16_t, true>(g, r, n, row < valid && in0, v, u, r0[k]);
+        } else {
+          linear_epilogue8<bf16_t, false>(g, r, n, row < valid && in0, v, nullptr, r0[k]);
+          linear_epilogue8<bf16_t, false>(g, r, n + 64, row < valid && in1, u, nullptr, r1[k]);
+        }
+      } else {
+        const size_t r = MODE == kDx ? static_cast<size_t>(seg) + m0 + row
+                                     : static_cast<size_t>(e) * g.z_dim + m0 + row;
+        bf16_t* const o = out + r * g.in_dim + n;
+        if (row < valid && in0) store_once8<bf16_t>(o, v);
+        if (row < valid && in1) store_once8<bf16_t>(o + 64, u);
       }
     }
     asm volatile("" ::: "memory");

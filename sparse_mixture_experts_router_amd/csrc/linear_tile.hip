@@ -236,14 +236,32 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs g, const T*
         stg[(wm * 64 + i * 16 + 4 * (lane >> 4) + r) * kStgRow + wn * 64 + j * 16 + (lane & 15)] =
             acc[i][j][r];
   lds_barrier();
-  for (int q = tid; q < kBM * COLS / 8; q += 256) {
-    const int row = q / (COLS / 8), c = q % (COLS / 8) * 8;
-    const bool ok = row < valid && n0 + c < n_dim;
+  // a lane keeps its columns: 256 is a multiple of COLS / 8
+  const int c = tid % (COLS / 8) * 8, n = n0 + c;
+  float sv[8], su[8], bv[8], bu[8];
+  if constexpr (MODE == kFwd) {
+    const size_t eo = static_cast<size_t>(e) * g.z_dim + n;
+    load_cols8(g.w_scale, eo, n < n_dim, 1.f, sv);
+    load_cols8(g.bias, eo, n < n_dim, 0.f, bv);
+    if (GATED) {
+      load_cols8(g.w_scale, eo + g.out_dim, n < n_dim, 1.f, su);
+      load_cols8(g.bias, eo + g.out_dim, n < n_dim, 0.f, bu);
+    }
+  }
+  for (int row = tid / (COLS / 8); row < kBM; row += 256 * 8 / COLS) {
+    const bool ok = row < valid && n < n_dim;
     float v[8], u[8];
     load8<float>(stg + row * kStgRow + c, v);
     if constexpr (MODE == kFwd) {
+      Raw8<T> res;
+      load_residual<T>(g, seg + m0 + row, n, ok, res);
       if (GATED) load8<float>(stg + row * kStgRow + COLS + c, u);
-      linear_epilogue8<T, GATED>(g, e, seg + m0 + row, n0 + c, ok, v, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = v[i] * sv[i] + bv[i];
+        if (GATED) u[i] = u[i] * su[i] + bu[i];
+      }
+      linear_epilogue8<T, GATED>(g, seg + m0 + row, n, ok, v, u, res);
     } else if (ok) {
       const size_t row0 = MODE == kDx ? static_cast<size_t>(seg) + m0 + row
                                       : static_cast<size_t>(e) * g.z_dim + m0 + row;
