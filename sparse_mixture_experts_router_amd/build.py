@@ -20,7 +20,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libmoe.so")
 
 SOURCES = ["route.hip", "permute.hip", "grouped_gemm.hip", "expert_gemm.hip", "combine.hip",
-           "backward.hip", "moe_api.hip", "linear_tile.hip", "linear_mfma.hip", "checkpoint.hip", "group_rows.hip",
+           "backward.hip", "moe_api.hip", "linear_tile.hip", "linear_mfma.hip", "linear_rows.hip", "checkpoint.hip", "group_rows.hip",
            "combine_rows.hip", "linear_api.hip"]
 
 ARCH = "gfx950"

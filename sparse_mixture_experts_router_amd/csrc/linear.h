@@ -50,10 +50,13 @@ hipError_t launch_linear_dx_tile(int dtype, const LinearArgs& g, const void* dz,
 hipError_t launch_linear_dw_tile(int dtype, const LinearArgs& g, const void* dz, void* dw,
                                  hipStream_t s);
 
-// The same three on 256 x 256 tiles (bf16, weights in bf16): dW takes x's
-// rows in order, without row_index.
-bool linear_mfma_fits(const LinearArgs& g);
-hipError_t launch_linear_mfma(const LinearArgs& g, hipStream_t s);
+// Forward for few rows a group: 32-row tiles, W streamed through registers.
+// cus: compute units of the device.
+hipError_t launch_linear_rows(int dtype, bool wfp8, const LinearArgs& g, int cus, hipStream_t s);
+// The same three on 256 x 256 tiles (bf16; forward: weights in bf16 or FP8):
+// dW takes x's rows in order, without row_index.
+bool linear_mfma_fits(bool wfp8, const LinearArgs& g);
+hipError_t launch_linear_mfma(bool wfp8, const LinearArgs& g, hipStream_t s);
 hipError_t launch_linear_mfma_dx(const LinearArgs& g, const void* dz, void* dx, hipStream_t s);
 hipError_t launch_linear_mfma_dw(const LinearArgs& g, const void* dz, void* dw, hipStream_t s);
 // xg[r] = x[row_index[r]] for the rows that belong to a group (bf16).

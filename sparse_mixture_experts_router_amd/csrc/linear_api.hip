@@ -75,6 +75,18 @@ LinearArgs linear_args(const moe_linear_config& c) {
   return g;
 }
 
+// Rows a group, on average, up to which the forward streams W through
+// registers (linear_rows.hip) instead of large tiles.  Mixtral-shaped gate and
+// up projection (8 experts, 4096 -> 14336, SwiGLU), us with few-row / with
+// large tiles:
+//   bf16  8 rows a group 327 / 339, 12: 341 / 334, 16: 376 / 346, 32: 620 / 330
+//   FP8   8 rows 193 / 244, 12: 227 / 239, 16: 255 / 239, 32: 448 / 239
+//   fp32  8 rows 636 / 2069, 16: 957 / 2069, 32: 1558 / 2072, 48: 2060 / 2078
+long few_rows(const moe_linear_config& c) {
+  if (c.dtype == MOE_F32) return 48;
+  return c.weight_format == MOE_WEIGHTS_FP8_E4M3 ? 12 : 8;
+}
+
 // Workspace of the backward.
 struct BackSpace {
   size_t dz, partial, xg, total;
@@ -193,10 +205,13 @@ moe_status moe_grouped_linear(const moe_linear_config* cfg, const moe_linear_arg
   g.z_codes = a->z_codes;
   g.z_scale = a->z_scale;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool many = c.rows > 48L * c.groups;
-  const hipError_t err = many && c.dtype == MOE_BF16 && !fp8 && linear_mfma_fits(g)
-                             ? launch_linear_mfma(g, s)
-                             : launch_linear_tile(c.dtype, fp8, g, s);
+  hipError_t err;
+  if (c.rows <= few_rows(c) * c.groups)
+    err = launch_linear_rows(c.dtype, fp8, g, device_cus(), s);
+  else if (c.dtype == MOE_BF16 && linear_mfma_fits(fp8, g))
+    err = launch_linear_mfma(fp8, g, s);
+  else
+    err = launch_linear_tile(c.dtype, fp8, g, s);
   return err == hipSuccess ? MOE_OK : hip_fail(err, "grouped linear kernel");
 }
 

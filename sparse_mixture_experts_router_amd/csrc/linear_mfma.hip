@@ -21,6 +21,12 @@
 // their K-rows (W of dX; dz and x of dW): 512 contiguous bytes of each of 64
 // K-rows, and the fragments are turned on the way out of LDS by
 // ds_read_b64_tr_b16, so nothing is ever transposed in memory.
+//
+// FP8 weights (forward): a buffer of the B operand holds 128 codes of each row,
+// two stages, and is loaded every other stage.  One 16-byte read gives a lane
+// the codes of both K steps of a stage, 16 consecutive elements, so the rows of
+// x are read in that order too; a fragment is widened to bf16 right before its
+// MFMAs, and the scales multiply the sums in the epilogue.
 #include "linear.h"
 #include "lds_ring.h"
 
@@ -105,10 +111,11 @@ struct Feed {
   int kcount;       // K-rows there are (those past it read zeros)
 };
 
-template <int MODE, bool GATED>
+template <int MODE, bool GATED, bool FP8W>
 __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
                                                              const bf16_t* __restrict__ dz,
                                                              bf16_t* __restrict__ out) {
+  static_assert(!FP8W || MODE == kFwd, "FP8 weights: forward");
   constexpr bool AK = MODE == kDw, BK = MODE != kFwd;
   constexpr int COLS = GATED ? kT / 2 : kT;
   __shared__ __attribute__((aligned(1024))) char smem[kLds];
@@ -159,7 +166,7 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
   const int grp = wave >> 2, q = wave & 3;
   const int mlive = __builtin_amdgcn_readfirstlane(min(max((valid - q * 16 + 63) / 64, 0), kMB));
   const size_t wmat = static_cast<size_t>(g.z_dim) * g.in_dim;
-  const bf16_t* const w = static_cast<const bf16_t*>(g.w) + e * wmat;
+  const char* const w = static_cast<const char*>(g.w) + e * wmat * (FP8W ? 1 : 2);
 
   // --------------------------------------------------- this lane's sources
   // Row operand: load j of wavefront q stages rows 64 q + 8 j .. + 7, lane l
@@ -199,14 +206,13 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
   } else if constexpr (MODE == kDw) {
     krow_feed(static_cast<const bf16_t*>(g.x) + static_cast<size_t>(seg) * g.in_dim, g.in_dim, n0);
   } else if constexpr (MODE == kDx) {
-    krow_feed(w, g.in_dim, n0);
+    krow_feed(reinterpret_cast<const bf16_t*>(w), g.in_dim, n0);
   } else {
     // SwiGLU: staged rows 0 .. 127 are gate rows, 128 .. 255 the up rows of
     // the same columns
-    const uint32_t row_bytes = static_cast<uint32_t>(g.in_dim) * 2;
+    const uint32_t row_bytes = static_cast<uint32_t>(g.in_dim) * (FP8W ? 1 : 2);
     const bool up = GATED && q >= 2;
-    f.base = reinterpret_cast<const char*>(w) +
-             (static_cast<size_t>(n0) + (up ? g.out_dim : 0)) * row_bytes;
+    f.base = w + (static_cast<size_t>(n0) + (up ? g.out_dim : 0)) * row_bytes;
     f.step = kLineBytes;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -223,10 +229,11 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
   }
   const int nst = MODE == kDw ? (count + 63) / 64
                               : (MODE == kFwd ? g.in_dim : g.z_dim) / 64;  // stages
-  // The loads of stage p into `ring`; past the end the last stage again, into
-  // a buffer that nobody reads any more.  NTL: with the non-temporal policy.
+  const int last = (FP8W && grp == 1 ? nst / 2 : nst) - 1;  // last buffer of this operand
+  // The loads of buffer p into `ring`; past the end the last one again, into
+  // a buffer that nobody reads any more.  nt_: with the non-temporal policy.
   auto issue = [&](int p, char* ring, auto nt_) {
-    const int pc = min(p, nst - 1);
+    const int pc = min(p, last);
     const char* const src = f.base + pc * f.step;
     char* const dst = ring + q * 8192;
     if (MODE == kDw && pc * 64 + 64 > f.kcount) {  // the group's last, partial stage
@@ -250,8 +257,13 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
 
   // ------------------------------------------------------- fragment addresses
   const int frow = lane & 15, fkey = swz128_key(frow);
-  const int fl0 = frow * kLineBytes + (((lane >> 4) ^ fkey) << 4);
-  const int fl1 = frow * kLineBytes + (((4 + (lane >> 4)) ^ fkey) << 4);
+  // a row's chunk of K step 0 and 1 of a stage; of codes: of the first and the
+  // second stage of a buffer
+  const int ch0 = FP8W ? 2 * (lane >> 4) : lane >> 4, ch1 = FP8W ? ch0 + 1 : ch0 + 4;
+  const int fl0 = frow * kLineBytes + ((ch0 ^ fkey) << 4);
+  const int fl1 = frow * kLineBytes + ((ch1 ^ fkey) << 4);
+  const int f8l0 = frow * kLineBytes + (((lane >> 4) ^ fkey) << 4);
+  const int f8l1 = frow * kLineBytes + (((4 + (lane >> 4)) ^ fkey) << 4);
   const int krow = 8 * (lane >> 4) + ((lane & 15) >> 2);
   const int klane = krow * 512 + ((lane & 3) >> 1) * 16 + (lane & 1) * 8;
   const int kkey = krow_key(krow);
@@ -310,9 +322,10 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
       constexpr int LIVE = decltype(live_)::value, G = decltype(grp_)::value;
       auto read = [&](int p) {
         const char* const a = abuf(p & 1);
-        const char* const b = bbuf(p % 3);
+        const char* const b = bbuf(FP8W ? (p >> 1) % 3 : p % 3);
         if (G == 0) issue(p + 1, abuf((p + 1) & 1), nt_);
-        else issue(p + 2, bbuf((p + 2) % 3), nt_);
+        else if (!FP8W) issue(p + 2, bbuf((p + 2) % 3), nt_);
+        else if ((p & 1) == 0) issue((p >> 1) + 2, bbuf(((p >> 1) + 2) % 3), nt_);
         if constexpr (LIVE > 0) {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -324,9 +337,12 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
                     *reinterpret_cast<const u32x4*>(a + (i * 64 + q * 16) * kLineBytes + fl);
             }
             if constexpr (!BK) {
+              if (!FP8W || t == 0) {
 #pragma unroll
-              for (int j = 0; j < kNB; ++j)
-                fr[t][kMB + j] = *reinterpret_cast<const u32x4*>(b + b_row(j) * kLineBytes + fl);
+                for (int j = 0; j < kNB; ++j)
+                  fr[t][kMB + j] = *reinterpret_cast<const u32x4*>(
+                      b + b_row(j) * kLineBytes + (FP8W ? ((p & 1) ? f8l1 : f8l0) : fl));
+              }
             }
           }
           if constexpr (AK) read_krows(a, live_, 0, q * 16, 64);
@@ -336,18 +352,38 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
           }
         }
         // fragments are in registers; half 0 leaves A(p + 1) in flight, half 1
-        // waits for B(p + 1) and leaves B(p + 2)
-        if (G == 0) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        // waits for B(p + 1) and leaves B(p + 2) (codes: the next two stages'
+        // buffer after an odd stage; after an even one it is there already)
+        if (G == 0 || (FP8W && (p & 1) == 0)) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         else wait_vmem<8>();
       };
       auto compute = [&]() {
         __builtin_amdgcn_s_setprio(2);
+        if constexpr (FP8W && LIVE > 0) {
+          // the first MFMA of a widened fragment waits out the VALU's write;
+          // the fragment before stays allocated until this one's MFMAs are
+          // issued, so no widening writes what an MFMA just issued still reads
+          u32x4 before = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int j = 0; j < kNB; ++j)
+            for (int j = 0; j < kNB; ++j) {
+              const u32x4 c = fr[0][kMB + j];
+              const u32x4 v = e4m3x8_to_bf16(t ? make_uint2(c[2], c[3]) : make_uint2(c[0], c[1]));
+              mfma_bf16_agpr_after_valu(acc[0][j], fr[t][0], v);
 #pragma unroll
-            for (int i = 0; i < LIVE; ++i) mfma_bf16_agpr(acc[i][j], fr[t][i], fr[t][kMB + j]);
+              for (int i = 1; i < LIVE; ++i) mfma_bf16_agpr(acc[i][j], fr[t][i], v);
+              asm volatile("" ::"v"(before));
+              before = v;
+            }
+        } else {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < kNB; ++j)
+#pragma unroll
+              for (int i = 0; i < LIVE; ++i) mfma_bf16_agpr(acc[i][j], fr[t][i], fr[t][kMB + j]);
+        }
         __builtin_amdgcn_s_setprio(0);
       };
       if (G == 0) {
@@ -395,9 +431,13 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
   const int c = (lane & 7) * 8;
   const int n = n0 + (GATED ? grp * 64 : grp * kWN) + c;
   const bool in0 = n < n_dim, in1 = !GATED && n + 64 < n_dim;
-  float b0[8], b1[8];
+  float b0[8], b1[8], s0[8], s1[8];
   if constexpr (MODE == kFwd) {
     const size_t eo = static_cast<size_t>(e) * g.z_dim + n;
+    if constexpr (FP8W) {
+      load_cols8(g.w_scale, eo, in0, 1.f, s0);
+      load_cols8(g.w_scale, eo + (GATED ? g.out_dim : 64), GATED ? in0 : in1, 1.f, s1);
+    }
     load_cols8(g.bias, eo, in0, 0.f, b0);
     load_cols8(g.bias, eo + (GATED ? g.out_dim : 64), GATED ? in0 : in1, 0.f, b1);
   }
@@ -434,8 +474,8 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
       if constexpr (MODE == kFwd) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          v[i] += b0[i];
-          u[i] += b1[i];
+          v[i] = (FP8W ? v[i] * s0[i] : v[i]) + b0[i];
+          u[i] = (FP8W ? u[i] * s1[i] : u[i]) + b1[i];
         }
         const long r = static_cast<long>(seg) + m0 + row;
         if constexpr (GATED) {
@@ -456,7 +496,7 @@ __global__ __launch_bounds__(512, 1) void linear_mfma_kernel(LinearArgs g,
   }
 }
 
-template <int MODE, bool GATED>
+template <int MODE, bool GATED, bool FP8W = false>
 hipError_t launch_t(const LinearArgs& g, const void* dz, void* out, hipStream_t s) {
   constexpr int COLS = GATED ? kT / 2 : kT;
   const long nt = ((MODE == kFwd ? g.out_dim : g.in_dim) + COLS - 1) / COLS;
@@ -467,7 +507,7 @@ hipError_t launch_t(const LinearArgs& g, const void* dz, void* out, hipStream_t 
   } else {
     blocks = item_grid(g.rows, g.groups, kT, nt);
   }
-  hipLaunchKernelGGL((linear_mfma_kernel<MODE, GATED>), dim3(static_cast<unsigned>(blocks)),
+  hipLaunchKernelGGL((linear_mfma_kernel<MODE, GATED, FP8W>), dim3(static_cast<unsigned>(blocks)),
                      dim3(512), 0, s, g, static_cast<const bf16_t*>(dz),
                      static_cast<bf16_t*>(out));
   return hipGetLastError();
@@ -475,14 +515,18 @@ hipError_t launch_t(const LinearArgs& g, const void* dz, void* out, hipStream_t 
 
 }  // namespace
 
-bool linear_mfma_fits(const LinearArgs& g) {
-  // 32-bit offsets into x when its rows are gathered
-  return g.row_index == nullptr ||
-         static_cast<size_t>(g.x_rows) * g.in_dim * 2 < (size_t{1} << 32);
+bool linear_mfma_fits(bool wfp8, const LinearArgs& g) {
+  // 32-bit offsets into x when its rows are gathered; whole buffers of codes
+  return (g.row_index == nullptr ||
+          static_cast<size_t>(g.x_rows) * g.in_dim * 2 < (size_t{1} << 32)) &&
+         (!wfp8 || g.in_dim % 128 == 0);
 }
 
-hipError_t launch_linear_mfma(const LinearArgs& g, hipStream_t s) {
-  if (!linear_mfma_fits(g)) return hipErrorInvalidValue;
+hipError_t launch_linear_mfma(bool wfp8, const LinearArgs& g, hipStream_t s) {
+  if (!linear_mfma_fits(wfp8, g)) return hipErrorInvalidValue;
+  if (wfp8)
+    return g.act == kActSwiglu ? launch_t<kFwd, true, true>(g, nullptr, nullptr, s)
+                               : launch_t<kFwd, false, true>(g, nullptr, nullptr, s);
   return g.act == kActSwiglu ? launch_t<kFwd, true>(g, nullptr, nullptr, s)
                              : launch_t<kFwd, false>(g, nullptr, nullptr, s);
 }

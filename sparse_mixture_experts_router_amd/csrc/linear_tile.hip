@@ -16,6 +16,8 @@
 // before it is multiplied out of the other of two LDS buffers.  Rows past a
 // group's end repeat its last row (results not written); K-rows past it are
 // zeros in both operands, so that no NaN of a neighbouring group enters.
+#include <type_traits>
+
 #include "linear.h"
 #include "lds_ring.h"
 
@@ -127,7 +129,11 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs g, const T*
   }
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // wavefront (wm, wn): 16-row blocks wm, wm + 2, ..., columns 64 wn ..; taking
+  // turns, the two share the rows of a partly filled tile, and run the MFMAs
+  // of the `live` blocks that hold rows
   const int wm = wave >> 1, wn = wave & 1;
+  const int live = __builtin_amdgcn_readfirstlane(min(max((valid - wm * 16 + 31) / 32, 0), 4));
   const size_t wmat = static_cast<size_t>(g.z_dim) * g.in_dim;
 
   Operand<T, T, MODE == kDw> A;
@@ -189,6 +195,25 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs g, const T*
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   auto stage = [&](int q) -> char* { return smem + q * 2 * TILE; };
+  auto compute = [&](const char* st, auto full_) {
+#pragma unroll
+    for (int kc = 0; kc < 2; ++kc) {
+      const int ch = kc * 4 + (lane >> 4);
+      u32x4 af[4], bf[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        af[i] = *reinterpret_cast<const u32x4*>(st + lds_swz(i * 32 + wm * 16 + (lane & 15), ch));
+        bf[i] = *reinterpret_cast<const u32x4*>(st + TILE +
+                                                lds_swz(wn * 64 + i * 16 + (lane & 15), ch));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (decltype(full_)::value || i < live) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = Mfma<T>::step(af[i], bf[j], acc[i][j]);
+        }
+    }
+  };
   if (nsteps > 0) {
     A.load(0);
     B.load(0);
@@ -202,21 +227,10 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs g, const T*
         B.load(s + 1);
       }
       const char* st = stage(s & 1);
-#pragma unroll
-      for (int kc = 0; kc < 2; ++kc) {
-        const int ch = kc * 4 + (lane >> 4);
-        u32x4 af[4], bf[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          af[i] = *reinterpret_cast<const u32x4*>(st + lds_swz(wm * 64 + i * 16 + (lane & 15), ch));
-          bf[i] = *reinterpret_cast<const u32x4*>(st + TILE +
-                                                  lds_swz(wn * 64 + i * 16 + (lane & 15), ch));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = Mfma<T>::step(af[i], bf[j], acc[i][j]);
-      }
+      // (only the forward has tiles of few rows by rule: fp32 with up to 48 rows
+      // a group does not come here; dX and dW run faster without the branches)
+      if (MODE != kFwd || live == 4) compute(st, std::true_type{});
+      else if (live > 0) compute(st, std::false_type{});
       if (more) {
         A.store(stage((s + 1) & 1));
         B.store(stage((s + 1) & 1) + TILE);
@@ -233,7 +247,7 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs g, const T*
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        stg[(wm * 64 + i * 16 + 4 * (lane >> 4) + r) * kStgRow + wn * 64 + j * 16 + (lane & 15)] =
+        stg[(i * 32 + wm * 16 + 4 * (lane >> 4) + r) * kStgRow + wn * 64 + j * 16 + (lane & 15)] =
             acc[i][j][r];
   lds_barrier();
   // a lane keeps its columns: 256 is a multiple of COLS / 8
