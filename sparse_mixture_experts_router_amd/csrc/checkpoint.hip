@@ -59,9 +59,11 @@ __global__ __launch_bounds__(256) void unpack_kernel(const uint8_t* __restrict__
 
 // dz = dy act'(z) for one row tile of kActRows rows of a group and up to 512
 // columns of y; z is decoded from its checkpoint.  `lpr` lanes (a power of
-// two) hold one row's columns, 8 each, so a wavefront takes 64 / lpr rows at
-// a time.  A lane keeps its columns through the tile and adds up its unrounded
-// dz; the workgroup's sums, in a fixed order, are the tile's row of partial.
+// two) hold one row's columns, 8 each, so the workgroup takes 256 / lpr rows
+// at a time, kActUnroll of them with their loads in flight together.  A lane
+// keeps its columns through the tile and adds up its unrounded dz; the
+// workgroup's sums, in a fixed order, are the tile's row of partial.
+constexpr int kActUnroll = 4;
 template <typename T, bool GATED>
 __global__ __launch_bounds__(256) void act_backward_kernel(LinearArgs g, const T* __restrict__ dy,
                                                            T* __restrict__ dz,
@@ -73,45 +75,65 @@ __global__ __launch_bounds__(256) void act_backward_kernel(LinearArgs g, const T
   if (tile >= t.total) return;
   const TileAt at = find_tile(t, g.offsets, g.groups, g.rows, kActRows, tile);
   const int row0 = at.begin + at.m * kActRows, row1 = min(row0 + kActRows, at.end);
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, rpp = 256 / lpr;  // rows of a pass
   const int c = (blockIdx.y * lpr + tid % lpr) * 8;
   const bool in = c < g.out_dim;
   float sum[NS];
 #pragma unroll
   for (int i = 0; i < NS; ++i) sum[i] = 0.f;
   if (in) {
-    for (int r = row0 + tid / lpr; r < row1; r += 256 / lpr) {
-      const size_t yo = static_cast<size_t>(r) * g.out_dim + c;
-      const size_t zo = static_cast<size_t>(r) * g.z_dim + c;
-      float d[8], o[NS];
-      load8<T>(dy + yo, d);
-      if (g.act == kActNone) {
+    for (int r0 = row0 + tid / lpr; r0 < row1; r0 += kActUnroll * rpp) {
+      Raw8<T> d[kActUnroll];
+      uint2 qz[kActUnroll], qu[kActUnroll];
+      float sz[kActUnroll], su[kActUnroll];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = d[i];
-      } else {
-        float z[8];
-        decode8(*reinterpret_cast<const uint2*>(g.z_codes + zo), g.z_scale[zo / kCkptBlock], z);
-        if constexpr (GATED) {
-          float u[8];
-          decode8(*reinterpret_cast<const uint2*>(g.z_codes + zo + g.out_dim),
-                  g.z_scale[(zo + g.out_dim) / kCkptBlock], u);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float p = sigmoid<T>(z[i]);
-            o[i] = d[i] * u[i] * (p + z[i] * p * (1.f - p));
-            o[8 + i] = d[i] * z[i] * p;
+      for (int k = 0; k < kActUnroll; ++k) {
+        const int r = min(r0 + k * rpp, row1 - 1);
+        const size_t zo = static_cast<size_t>(r) * g.z_dim + c;
+        d[k].load(dy + static_cast<size_t>(r) * g.out_dim + c);
+        if (g.act != kActNone) {
+          qz[k] = *reinterpret_cast<const uint2*>(g.z_codes + zo);
+          sz[k] = g.z_scale[zo / kCkptBlock];
+          if (GATED) {
+            qu[k] = *reinterpret_cast<const uint2*>(g.z_codes + zo + g.out_dim);
+            su[k] = g.z_scale[(zo + g.out_dim) / kCkptBlock];
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = d[i] * activate_slope<T>(g.act, z[i]);
         }
       }
-      if (dz != nullptr) {
-        store8<T>(dz + zo, o);
-        if (GATED) store8<T>(dz + zo + g.out_dim, o + 8);
-      }
 #pragma unroll
-      for (int i = 0; i < NS; ++i) sum[i] += o[i];
+      for (int k = 0; k < kActUnroll; ++k) {
+        const int r = r0 + k * rpp;
+        if (r >= row1) break;
+        const size_t zo = static_cast<size_t>(r) * g.z_dim + c;
+        float o[NS];
+        if (g.act == kActNone) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = d[k].get(i);
+        } else {
+          float z[8];
+          decode8(qz[k], sz[k], z);
+          if constexpr (GATED) {
+            float u[8];
+            decode8(qu[k], su[k], u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float p = sigmoid<T>(z[i]), dh = d[k].get(i);
+              o[i] = dh * u[i] * (p + z[i] * p * (1.f - p));
+              o[8 + i] = dh * z[i] * p;
+            }
+          } else {
+            activate_slope8<T>(g.act, z, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] *= d[k].get(i);
+          }
+        }
+        if (dz != nullptr) {
+          store8<T>(dz + zo, o);
+          if (GATED) store8<T>(dz + zo + g.out_dim, o + 8);
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) sum[i] += o[i];
+      }
     }
   }
   if (partial == nullptr) return;

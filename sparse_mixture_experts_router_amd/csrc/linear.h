@@ -41,17 +41,17 @@ struct LinearArgs {
 };
 
 // ---------------------------------------------------------------- launchers
-// Forward: y = act(x W^T + b) + residual on BM-row tiles; wfp8: E4M3 weights.
-hipError_t launch_linear_tile(int dtype, bool wfp8, const LinearArgs& g, hipStream_t s);
+// Forward: y = act(x W^T + b) + residual; wfp8: E4M3 weights; cus: compute
+// units of the device.
+hipError_t launch_linear_tile(int dtype, bool wfp8, const LinearArgs& g, int cus, hipStream_t s);
 // dX[r] = dz[r] W_e.  dz [rows, z_dim], dx [rows, in].
-hipError_t launch_linear_dx_tile(int dtype, const LinearArgs& g, const void* dz, void* dx,
+hipError_t launch_linear_dx_tile(int dtype, const LinearArgs& g, const void* dz, void* dx, int cus,
                                  hipStream_t s);
 // dW_e = sum_r dz[r]^T x[src(r)]; groups without rows get zeros.
-hipError_t launch_linear_dw_tile(int dtype, const LinearArgs& g, const void* dz, void* dw,
+hipError_t launch_linear_dw_tile(int dtype, const LinearArgs& g, const void* dz, void* dw, int cus,
                                  hipStream_t s);
 
 // Forward for few rows a group: 32-row tiles, W streamed through registers.
-// cus: compute units of the device.
 hipError_t launch_linear_rows(int dtype, bool wfp8, const LinearArgs& g, int cus, hipStream_t s);
 // The same three on 256 x 256 tiles (bf16; forward: weights in bf16 or FP8):
 // dW takes x's rows in order, without row_index.
@@ -64,7 +64,7 @@ hipError_t launch_gather_rows(const LinearArgs& g, void* xg, hipStream_t s);
 
 // Row tiles of kActRows rows that the activation's backward works in; the
 // most there can be for `rows` rows in `groups` groups.
-constexpr int kActRows = 64;
+constexpr int kActRows = 16;
 inline long act_tiles(long rows, long groups) {
   return rows / kActRows + (groups < rows ? groups : rows);
 }
@@ -233,6 +233,24 @@ template <typename T> __device__ __forceinline__ float activate_slope(int act, f
       return p + z * p * (1.f - p);
     }
     default: return 1.f;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void activate_slope8(int act, const float* z, float* o) {
+  // one uniform branch for the 8 values
+  switch (act) {
+    case kActRelu:
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = activate_slope<T>(kActRelu, z[i]);
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = activate_slope<T>(kActGelu, z[i]);
+      break;
+    default:
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = activate_slope<T>(kActSilu, z[i]);
   }
 }
 

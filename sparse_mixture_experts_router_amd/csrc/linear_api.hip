@@ -87,6 +87,18 @@ long few_rows(const moe_linear_config& c) {
   return c.weight_format == MOE_WEIGHTS_FP8_E4M3 ? 12 : 8;
 }
 
+// Whether a bf16 product has enough 256 x 256 tiles for the large-tile kernel
+// (linear_mfma.hip): with no more than an eighth of the compute units, the 64
+// x 64 tiles of linear_tile.hip spread it over more of them.  Backward, us with
+// large / with small tiles: 600 rows, 4 experts, 512 -> 1024: 47 / 35; 2000
+// rows, one expert, 1024 -> 2 x 4096: 200 / 223 (dX, 32 tiles, alone on the
+// small ones 169); 1600 rows, 64 experts, 512 -> 512: 48 / 64.
+bool large_tiles(long row_tiles, int cols) {
+  return row_tiles * ((cols + 255) / 256) > device_cus() / 8;
+}
+// Row tiles of 256 rows that the rows of all groups can need.
+long row_tiles(const moe_linear_config& c) { return c.rows / 256 + std::min(c.groups, c.rows); }
+
 // Workspace of the backward.
 struct BackSpace {
   size_t dz, partial, xg, total;
@@ -208,10 +220,10 @@ moe_status moe_grouped_linear(const moe_linear_config* cfg, const moe_linear_arg
   hipError_t err;
   if (c.rows <= few_rows(c) * c.groups)
     err = launch_linear_rows(c.dtype, fp8, g, device_cus(), s);
-  else if (c.dtype == MOE_BF16 && linear_mfma_fits(fp8, g))
+  else if (c.dtype == MOE_BF16 && large_tiles(row_tiles(c), g.z_dim) && linear_mfma_fits(fp8, g))
     err = launch_linear_mfma(fp8, g, s);
   else
-    err = launch_linear_tile(c.dtype, fp8, g, s);
+    err = launch_linear_tile(c.dtype, fp8, g, device_cus(), s);
   return err == hipSuccess ? MOE_OK : hip_fail(err, "grouped linear kernel");
 }
 
@@ -271,20 +283,22 @@ moe_status moe_grouped_linear_backward(const moe_linear_config* cfg,
     return hip_fail(err, "bias gradient");
   const bool bf16 = c.dtype == MOE_BF16;
   if (c.rows > 0 && a->dx != nullptr) {
-    err = bf16 ? launch_linear_mfma_dx(g, dz, a->dx, s)
-               : launch_linear_dx_tile(c.dtype, g, dz, a->dx, s);
+    const bool large = bf16 && large_tiles(row_tiles(c), c.in_dim);
+    err = large ? launch_linear_mfma_dx(g, dz, a->dx, s)
+               : launch_linear_dx_tile(c.dtype, g, dz, a->dx, device_cus(), s);
     if (err != hipSuccess) return hip_fail(err, "dx");
   }
   if (a->dw != nullptr) {
-    if (bf16 && g.row_index != nullptr && c.rows > 0) {
+    const bool large = bf16 && large_tiles(c.groups * ((g.z_dim + 255L) / 256), c.in_dim);
+    if (large && g.row_index != nullptr && c.rows > 0) {
       // the large tiles stage x by its rows in order
       if ((err = launch_gather_rows(g, base + b.xg, s)) != hipSuccess)
         return hip_fail(err, "gather of x");
       g.x = base + b.xg;
     }
-    if (bf16) g.row_index = nullptr;
-    err = bf16 ? launch_linear_mfma_dw(g, dz, a->dw, s)
-               : launch_linear_dw_tile(c.dtype, g, dz, a->dw, s);
+    if (large) g.row_index = nullptr;
+    err = large ? launch_linear_mfma_dw(g, dz, a->dw, s)
+               : launch_linear_dw_tile(c.dtype, g, dz, a->dw, device_cus(), s);
     if (err != hipSuccess) return hip_fail(err, "dw");
   }
   return MOE_OK;

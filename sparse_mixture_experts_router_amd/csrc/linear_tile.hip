@@ -1,5 +1,5 @@
-// Grouped linear maps on register-staged 128 x 128 tiles: every type and
-// direction in one kernel.
+// Grouped linear maps on register-staged 128 x 128 or 64 x 64 tiles: every
+// type and direction in one kernel.
 //
 //   forward  z[r] = x[src(r)] W_e^T + b_e,  y[r] = act(z[r]) + residual[r]
 //   dX       dX[r] = dz[r] W_e
@@ -11,11 +11,13 @@
 // K-row operand is turned while it is stored to LDS, so both kinds feed the
 // same 16-byte MFMA fragments.
 //
-// One workgroup owns a 128 x 128 tile of one group, 4 wavefronts of 64 x 64;
-// a K step is 128 bytes of every row, fetched into registers while the step
+// One workgroup owns a B x B tile of one group (B = 128, or 64 where the
+// larger tiles would leave compute units without work), its 4 wavefronts a
+// quarter each; a K step is 128 bytes of every row, fetched into registers while the step
 // before it is multiplied out of the other of two LDS buffers.  Rows past a
 // group's end repeat its last row (results not written); K-rows past it are
 // zeros in both operands, so that no NaN of a neighbouring group enters.
+#include <algorithm>
 #include <type_traits>
 
 #include "linear.h"
@@ -25,23 +27,21 @@ namespace moe {
 namespace {
 
 constexpr int kFwd = 0, kDx = 1, kDw = 2;
-constexpr int kBM = 128, kBN = 128;
-constexpr int kStgRow = kBN + 4;  // floats of a staged result row
 
-// One operand tile: 128 rows x 128 bytes.
-template <typename T, typename TW, bool KROW>
+// One operand tile: L x 32 rows of 128 bytes, L 16-byte chunks a thread.
+template <typename T, typename TW, bool KROW, int L>
 struct Operand;
 
 // K contiguous: chunk c = tid + 256 i is 16 bytes (8 codes of an FP8 weight)
 // ch = c % 8 of tile row c / 8.
-template <typename T, typename TW>
-struct Operand<T, TW, false> {
+template <typename T, typename TW, int L>
+struct Operand<T, TW, false, L> {
   static constexpr int CB = 16 * static_cast<int>(sizeof(TW)) / static_cast<int>(sizeof(T));
-  const char* p[4];
-  u32x4 v[4];
+  const char* p[L];
+  u32x4 v[L];
   __device__ __forceinline__ void load(int step) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < L; ++i) {
       const char* q = p[i] + static_cast<size_t>(step) * 8 * CB;
       if constexpr (sizeof(TW) == sizeof(T)) {
         v[i] = *reinterpret_cast<const u32x4*>(q);
@@ -52,7 +52,7 @@ struct Operand<T, TW, false> {
   }
   __device__ __forceinline__ void store(char* lds) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < L; ++i) {
       const int c = threadIdx.x + 256 * i;
       *reinterpret_cast<u32x4*>(lds + lds_swz(c >> 3, c & 7)) = v[i];
     }
@@ -60,18 +60,18 @@ struct Operand<T, TW, false> {
 };
 
 // K-rows: chunk c is 16 bytes (V columns) of K-row c % KE of the step.
-template <typename T>
-struct Operand<T, T, true> {
+template <typename T, int L>
+struct Operand<T, T, true, L> {
   static constexpr int V = 16 / static_cast<int>(sizeof(T)), KE = 128 / static_cast<int>(sizeof(T));
   const T* base;              // K-row 0 of the tile's first column
   size_t ld;                  // elements of a K-row
   int cols, krows;            // columns of the operand from the tile's first; K-rows there are
   const int32_t* index;       // source row of K-row j, or null
   int index_rows;             // rows the index may name
-  u32x4 v[4];
+  u32x4 v[L];
   __device__ __forceinline__ void load(int step) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < L; ++i) {
       const int c = threadIdx.x + 256 * i;
       const int kk = step * KE + c % KE, col = c / KE * V;
       v[i] = u32x4{0u, 0u, 0u, 0u};
@@ -83,7 +83,7 @@ struct Operand<T, T, true> {
   }
   __device__ __forceinline__ void store(char* lds) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < L; ++i) {
       const int c = threadIdx.x + 256 * i;
       const int kb = c % KE * static_cast<int>(sizeof(T)), col = c / KE * V;
       const T* e = reinterpret_cast<const T*>(&v[i]);
@@ -94,146 +94,149 @@ struct Operand<T, T, true> {
   }
 };
 
-template <typename T, typename TW, int MODE, bool GATED>
+template <typename T, typename TW, int MODE, bool GATED, int B>
 __global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs g, const T* __restrict__ dz,
                                                           T* __restrict__ out) {
-  constexpr int TILE = kBM * 128;
-  constexpr int STG = kBM * kStgRow * 4;
+  constexpr int TILE = B * 128;
+  constexpr int NB = B / 32;           // 16-row and 16-column blocks of a wavefront
+  constexpr int L = B / 32;            // 16-byte chunks of an operand tile a thread
+  constexpr int PITCH = B + 4;         // floats of a staged result row
+  constexpr int STG = B * PITCH * 4;
   __shared__ __attribute__((aligned(1024))) char smem[4 * TILE > STG ? 4 * TILE : STG];
-  constexpr int COLS = GATED ? kBN / 2 : kBN;  // output columns of a tile
+  constexpr int COLS = GATED ? B / 2 : B;  // output columns of a tile
 
   const int n_dim = MODE == kFwd ? g.out_dim : g.in_dim;  // columns of C
   const int nt = (n_dim + COLS - 1) / COLS;
   int e, m0, n0, valid, seg, count;
   if constexpr (MODE == kDw) {
-    const int mt = (g.z_dim + kBM - 1) / kBM;
+    const int mt = (g.z_dim + B - 1) / B;
     const int per = mt * nt;
     e = blockIdx.x / per;
     const int r = blockIdx.x - e * per;
-    m0 = (r % mt) * kBM;
+    m0 = (r % mt) * B;
     n0 = (r / mt) * COLS;
     const int2 range = group_range(g.offsets, e, g.rows);
     seg = range.x;
     count = range.y - range.x;
-    valid = min(kBM, g.z_dim - m0);
+    valid = min(B, g.z_dim - m0);
   } else {
     TileAt at;
     int col;
-    if (!find_item(g.offsets, g.groups, g.rows, kBM, nt, at, col)) return;
+    if (!find_item(g.offsets, g.groups, g.rows, B, nt, at, col)) return;
     e = at.e;
-    m0 = at.m * kBM;
+    m0 = at.m * B;
     n0 = col * COLS;
     seg = at.begin;
     count = at.end - at.begin;
-    valid = min(kBM, count - m0);
+    valid = min(B, count - m0);
   }
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  // wavefront (wm, wn): 16-row blocks wm, wm + 2, ..., columns 64 wn ..; taking
+  // wavefront (wm, wn): 16-row blocks wm, wm + 2, ..., columns B / 2 wn ..; taking
   // turns, the two share the rows of a partly filled tile, and run the MFMAs
   // of the `live` blocks that hold rows
   const int wm = wave >> 1, wn = wave & 1;
-  const int live = __builtin_amdgcn_readfirstlane(min(max((valid - wm * 16 + 31) / 32, 0), 4));
+  const int live = __builtin_amdgcn_readfirstlane(min(max((valid - wm * 16 + 31) / 32, 0), NB));
   const size_t wmat = static_cast<size_t>(g.z_dim) * g.in_dim;
 
-  Operand<T, T, MODE == kDw> A;
-  Operand<T, TW, MODE != kFwd> B;
+  Operand<T, T, MODE == kDw, L> opa;
+  Operand<T, TW, MODE != kFwd, L> opb;
   int nsteps;
   if constexpr (MODE == kDw) {
-    A.base = dz + static_cast<size_t>(seg) * g.z_dim + m0;
-    A.ld = g.z_dim;
-    A.cols = g.z_dim - m0;
-    A.krows = count;
-    A.index = nullptr;
-    A.index_rows = 0;
+    opa.base = dz + static_cast<size_t>(seg) * g.z_dim + m0;
+    opa.ld = g.z_dim;
+    opa.cols = g.z_dim - m0;
+    opa.krows = count;
+    opa.index = nullptr;
+    opa.index_rows = 0;
     const bool gather = g.row_index != nullptr;
-    B.base = static_cast<const T*>(g.x) + (gather ? 0 : static_cast<size_t>(seg) * g.in_dim) + n0;
-    B.ld = g.in_dim;
-    B.cols = g.in_dim - n0;
-    B.krows = count;
-    B.index = gather ? g.row_index + seg : nullptr;
-    B.index_rows = g.x_rows;
-    nsteps = (count + B.KE - 1) / B.KE;
+    opb.base = static_cast<const T*>(g.x) + (gather ? 0 : static_cast<size_t>(seg) * g.in_dim) + n0;
+    opb.ld = g.in_dim;
+    opb.cols = g.in_dim - n0;
+    opb.krows = count;
+    opb.index = gather ? g.row_index + seg : nullptr;
+    opb.index_rows = g.x_rows;
+    nsteps = (count + opb.KE - 1) / opb.KE;
   } else {
     const int k_dim = MODE == kFwd ? g.in_dim : g.z_dim;
     const char* src = MODE == kFwd ? static_cast<const char*>(g.x)
                                    : reinterpret_cast<const char*>(dz);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < L; ++i) {
       const int c = tid + 256 * i;
       const int row = seg + m0 + min(c >> 3, valid - 1);
       int srow = row;
       if (MODE == kFwd && g.row_index != nullptr)
         srow = min(max(g.row_index[row], 0), g.x_rows - 1);
-      A.p[i] = src + static_cast<size_t>(srow) * k_dim * sizeof(T) + (c & 7) * 16;
+      opa.p[i] = src + static_cast<size_t>(srow) * k_dim * sizeof(T) + (c & 7) * 16;
     }
     nsteps = static_cast<int>(static_cast<size_t>(k_dim) * sizeof(T) / 128);
     if constexpr (MODE == kFwd) {
       const char* w = static_cast<const char*>(g.w) + e * wmat * sizeof(TW);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < L; ++i) {
         const int c = tid + 256 * i, r = c >> 3;
         // SwiGLU: the tile's gate rows, then the up rows of the same columns
         const bool up = GATED && r >= COLS;
         const int n = min(n0 + (up ? r - COLS : r), g.out_dim - 1) + (up ? g.out_dim : 0);
-        B.p[i] = w + (static_cast<size_t>(n) * g.in_dim) * sizeof(TW) + (c & 7) * B.CB;
+        opb.p[i] = w + (static_cast<size_t>(n) * g.in_dim) * sizeof(TW) + (c & 7) * opb.CB;
       }
     } else {
-      B.base = static_cast<const T*>(g.w) + e * wmat + n0;
-      B.ld = g.in_dim;
-      B.cols = g.in_dim - n0;
-      B.krows = g.z_dim;
-      B.index = nullptr;
-      B.index_rows = 0;
+      opb.base = static_cast<const T*>(g.w) + e * wmat + n0;
+      opb.ld = g.in_dim;
+      opb.cols = g.in_dim - n0;
+      opb.krows = g.z_dim;
+      opb.index = nullptr;
+      opb.index_rows = 0;
     }
   }
 
-  f32x4 acc[4][4];
+  f32x4 acc[NB][NB];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   auto stage = [&](int q) -> char* { return smem + q * 2 * TILE; };
   auto compute = [&](const char* st, auto full_) {
 #pragma unroll
     for (int kc = 0; kc < 2; ++kc) {
       const int ch = kc * 4 + (lane >> 4);
-      u32x4 af[4], bf[4];
+      u32x4 af[NB], bf[NB];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < NB; ++i) {
         af[i] = *reinterpret_cast<const u32x4*>(st + lds_swz(i * 32 + wm * 16 + (lane & 15), ch));
         bf[i] = *reinterpret_cast<const u32x4*>(st + TILE +
-                                                lds_swz(wn * 64 + i * 16 + (lane & 15), ch));
+                                                lds_swz(wn * (B / 2) + i * 16 + (lane & 15), ch));
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < NB; ++i)
         if (decltype(full_)::value || i < live) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = Mfma<T>::step(af[i], bf[j], acc[i][j]);
+          for (int j = 0; j < NB; ++j) acc[i][j] = Mfma<T>::step(af[i], bf[j], acc[i][j]);
         }
     }
   };
   if (nsteps > 0) {
-    A.load(0);
-    B.load(0);
-    A.store(stage(0));
-    B.store(stage(0) + TILE);
+    opa.load(0);
+    opb.load(0);
+    opa.store(stage(0));
+    opb.store(stage(0) + TILE);
     lds_barrier();
     for (int s = 0; s < nsteps; ++s) {
       const bool more = s + 1 < nsteps;
       if (more) {
-        A.load(s + 1);
-        B.load(s + 1);
+        opa.load(s + 1);
+        opb.load(s + 1);
       }
       const char* st = stage(s & 1);
       // (only the forward has tiles of few rows by rule: fp32 with up to 48 rows
       // a group does not come here; dX and dW run faster without the branches)
-      if (MODE != kFwd || live == 4) compute(st, std::true_type{});
+      if (MODE != kFwd || live == NB) compute(st, std::true_type{});
       else if (live > 0) compute(st, std::false_type{});
       if (more) {
-        A.store(stage((s + 1) & 1));
-        B.store(stage((s + 1) & 1) + TILE);
+        opa.store(stage((s + 1) & 1));
+        opb.store(stage((s + 1) & 1) + TILE);
       }
       lds_barrier();
     }
@@ -242,12 +245,12 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs g, const T*
   // the tile as fp32 rows in LDS, then 8 columns of a row per lane
   float* const stg = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NB; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        stg[(i * 32 + wm * 16 + 4 * (lane >> 4) + r) * kStgRow + wn * 64 + j * 16 + (lane & 15)] =
+        stg[(i * 32 + wm * 16 + 4 * (lane >> 4) + r) * PITCH + wn * (B / 2) + j * 16 + (lane & 15)] =
             acc[i][j][r];
   lds_barrier();
   // a lane keeps its columns: 256 is a multiple of COLS / 8
@@ -262,14 +265,14 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs g, const T*
       load_cols8(g.bias, eo + g.out_dim, n < n_dim, 0.f, bu);
     }
   }
-  for (int row = tid / (COLS / 8); row < kBM; row += 256 * 8 / COLS) {
+  for (int row = tid / (COLS / 8); row < B; row += 256 * 8 / COLS) {
     const bool ok = row < valid && n < n_dim;
     float v[8], u[8];
-    load8<float>(stg + row * kStgRow + c, v);
+    load8<float>(stg + row * PITCH + c, v);
     if constexpr (MODE == kFwd) {
       Raw8<T> res;
       load_residual<T>(g, seg + m0 + row, n, ok, res);
-      if (GATED) load8<float>(stg + row * kStgRow + COLS + c, u);
+      if (GATED) load8<float>(stg + row * PITCH + COLS + c, u);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         v[i] = v[i] * sv[i] + bv[i];
@@ -284,45 +287,59 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs g, const T*
   }
 }
 
-template <typename T, typename TW, int MODE>
-hipError_t launch_t(const LinearArgs& g, const void* dz, void* out, hipStream_t s) {
+template <typename T, typename TW, int MODE, int B>
+hipError_t launch_b(const LinearArgs& g, const void* dz, void* out, hipStream_t s) {
   const bool gated = MODE == kFwd && g.act == kActSwiglu;
-  const int cols = gated ? kBN / 2 : kBN;
+  const int cols = gated ? B / 2 : B;
   const long nt = ((MODE == kFwd ? g.out_dim : g.in_dim) + cols - 1) / cols;
-  const long blocks = MODE == kDw ? static_cast<long>(g.groups) * ((g.z_dim + kBM - 1) / kBM) * nt
-                                  : item_grid(g.rows, g.groups, kBM, nt);
+  const long blocks = MODE == kDw ? static_cast<long>(g.groups) * ((g.z_dim + B - 1) / B) * nt
+                                  : item_grid(g.rows, g.groups, B, nt);
   if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks));
-  if constexpr (MODE == kFwd) {
+  if constexpr (MODE == kFwd && B == 128) {
     if (gated) {
-      hipLaunchKernelGGL((linear_tile_kernel<T, TW, MODE, true>), grid, dim3(256), 0, s, g,
+      hipLaunchKernelGGL((linear_tile_kernel<T, TW, MODE, true, B>), grid, dim3(256), 0, s, g,
                          static_cast<const T*>(dz), static_cast<T*>(out));
       return hipGetLastError();
     }
   }
-  hipLaunchKernelGGL((linear_tile_kernel<T, TW, MODE, false>), grid, dim3(256), 0, s, g,
+  if (gated) return hipErrorInvalidValue;  // half a 64-column tile is no checkpoint block
+  hipLaunchKernelGGL((linear_tile_kernel<T, TW, MODE, false, B>), grid, dim3(256), 0, s, g,
                      static_cast<const T*>(dz), static_cast<T*>(out));
   return hipGetLastError();
 }
 
+// 64 x 64 tiles where the 128 x 128 ones are fewer than the compute units: a
+// small product is bound by one tile's chain of steps, and theirs is a
+// quarter as long.
+template <typename T, typename TW, int MODE>
+hipError_t launch_t(const LinearArgs& g, const void* dz, void* out, int cus, hipStream_t s) {
+  const long nt = ((MODE == kFwd ? g.out_dim : g.in_dim) + 127) / 128;
+  const long mt = MODE == kDw ? static_cast<long>(g.groups) * ((g.z_dim + 127) / 128)
+                              : g.rows / 128 + std::min(g.groups, g.rows);
+  if (mt * nt < cus && !(MODE == kFwd && g.act == kActSwiglu))
+    return launch_b<T, TW, MODE, 64>(g, dz, out, s);
+  return launch_b<T, TW, MODE, 128>(g, dz, out, s);
+}
+
 }  // namespace
 
-hipError_t launch_linear_tile(int dtype, bool wfp8, const LinearArgs& g, hipStream_t s) {
-  if (wfp8) return launch_t<bf16_t, uint8_t, kFwd>(g, nullptr, nullptr, s);
-  if (dtype == 1) return launch_t<bf16_t, bf16_t, kFwd>(g, nullptr, nullptr, s);
-  return launch_t<float, float, kFwd>(g, nullptr, nullptr, s);
+hipError_t launch_linear_tile(int dtype, bool wfp8, const LinearArgs& g, int cus, hipStream_t s) {
+  if (wfp8) return launch_t<bf16_t, uint8_t, kFwd>(g, nullptr, nullptr, cus, s);
+  if (dtype == 1) return launch_t<bf16_t, bf16_t, kFwd>(g, nullptr, nullptr, cus, s);
+  return launch_t<float, float, kFwd>(g, nullptr, nullptr, cus, s);
 }
 
-hipError_t launch_linear_dx_tile(int dtype, const LinearArgs& g, const void* dz, void* dx,
+hipError_t launch_linear_dx_tile(int dtype, const LinearArgs& g, const void* dz, void* dx, int cus,
                                  hipStream_t s) {
-  if (dtype == 1) return launch_t<bf16_t, bf16_t, kDx>(g, dz, dx, s);
-  return launch_t<float, float, kDx>(g, dz, dx, s);
+  if (dtype == 1) return launch_t<bf16_t, bf16_t, kDx>(g, dz, dx, cus, s);
+  return launch_t<float, float, kDx>(g, dz, dx, cus, s);
 }
 
-hipError_t launch_linear_dw_tile(int dtype, const LinearArgs& g, const void* dz, void* dw,
+hipError_t launch_linear_dw_tile(int dtype, const LinearArgs& g, const void* dz, void* dw, int cus,
                                  hipStream_t s) {
-  if (dtype == 1) return launch_t<bf16_t, bf16_t, kDw>(g, dz, dw, s);
-  return launch_t<float, float, kDw>(g, dz, dw, s);
+  if (dtype == 1) return launch_t<bf16_t, bf16_t, kDw>(g, dz, dw, cus, s);
+  return launch_t<float, float, kDw>(g, dz, dw, cus, s);
 }
 
 }  // namespace moe

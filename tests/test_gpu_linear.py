@@ -221,6 +221,7 @@ class Case:
         return out
 
 
+RAGGED = [130, 257, 0, 64, 300, 1, 0, 31, 16, 17, 33, 512]
 FORWARD = [
     # sizes, K, F, act, options
     ([1], 64, 64, "none", {}),
@@ -234,6 +235,13 @@ FORWARD = [
     ([511, 1, 300], 512, 448, "swiglu", dict(gather=True, bias=True, spare=9)),
     ([260, 513], 1024, 256, "gelu", dict()),
     ([2, 300, 0, 1], 640, 320, "silu", dict(bias=True, gather=True)),
+    # enough 256 x 256 tiles (more than an eighth of the compute units) for the
+    # large-tile kernel in every product, groups of all fillings
+    (RAGGED, 448, 1088, "silu", dict(gather=True, bias=True)),
+    (RAGGED, 512, 576, "swiglu", dict(gather=True, bias=True, spare=9)),
+    (RAGGED, 640, 832, "none", dict(bias=True, residual=True, spare=1)),
+    (RAGGED, 1152, 640, "gelu", dict(residual=True)),
+    ([0] * 20 + [160] + [0] * 9 + [96] * 2, 512, 320, "relu", dict()),
 ]
 IDS = [f"{len(s)}g{sum(s)}r_{K}x{F}_{a}" for s, K, F, a, _ in FORWARD]
 
@@ -264,16 +272,17 @@ def test_backward_of_some(act, want):
 
 def test_residual_in_place():
     say("[linear] y is the residual")
-    for sizes in ([9, 4], [300, 270]):
-        Case(sizes, 128, 192, "gelu", residual=True, spare=3).check_forward("in place", inplace=True)
+    for sizes, F in (([9, 4], 192), ([300, 270], 192), (RAGGED, 1088)):
+        Case(sizes, 128, F, "gelu", residual=True, spare=3).check_forward("in place", inplace=True)
 
 
+@pytest.mark.parametrize("groups", [3, 40], ids=["small", "large"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_neighbours_stay_apart(dtype):
+def test_neighbours_stay_apart(dtype, groups):
     """One group's NaN and infinities reach none of the others' outputs,
     whatever tiles they share."""
     say(f"[linear] neighbours {dtype}")
-    c = Case([37, 70, 5], 128, 192, "silu", dtype)
+    c = Case([37, 70, 5] + [9] * (groups - 3), 128 if groups == 3 else 512, 192, "silu", dtype)
     a, b = int(c.off[1]), int(c.off[2])
     ref = c.check_backward("before")
     y0, codes, scale = c.forward(True)
@@ -281,15 +290,15 @@ def test_neighbours_stay_apart(dtype):
     c.x[a:b], c.dy[a:b] = float("inf"), float("nan")
     c.w[1] = float("nan")
     y, _, _ = c.forward()
-    out = {"dx": poison((c.rows, c.K), c.dt), "dw": poison((3, c.zd, c.K), c.dt),
-           "dbias": poison((3, c.zd), torch.float32)}
+    out = {"dx": poison((c.rows, c.K), c.dt), "dw": poison((groups, c.zd, c.K), c.dt),
+           "dbias": poison((groups, c.zd), torch.float32)}
     moe.moe_grouped_linear_backward(c.cfg, c.x, c.offsets, c.w, c.dy, z_codes=codes,
                                     z_scale=scale, workspace=workspace(
                                         moe.alloc_linear_backward_workspace(c.cfg, DEV)), **out)
     torch.cuda.synchronize()
     for r in (slice(0, a), slice(b, c.rows)):
         assert torch.equal(y[r], y0[r]) and torch.equal(out["dx"][r], ref["dx"][r])
-    for e in (0, 2):
+    for e in [0] + list(range(2, groups)):
         assert torch.equal(out["dw"][e], ref["dw"][e])
         assert torch.equal(out["dbias"][e], ref["dbias"][e])
 
@@ -316,8 +325,8 @@ def test_offsets_are_clamped(rows, groups):
 
 def test_results_repeat_and_streams_do_not_matter():
     say("[linear] repeat, another stream")
-    for sizes in ([3, 17, 0, 9], [300, 40, 600]):
-        c = Case(sizes, 256, 192, "swiglu", gather=True, bias=True)
+    for sizes, F in (([3, 17, 0, 9], 192), ([300, 40, 600], 192), (RAGGED, 576)):
+        c = Case(sizes, 256 if F == 192 else 512, F, "swiglu", gather=True, bias=True)
         y0, codes, scale = c.forward(True)
         torch.cuda.synchronize()
         side = torch.cuda.Stream()
@@ -544,7 +553,8 @@ class Mlp:
 
 @pytest.mark.parametrize("T,N,k,d,F,act,dtype,capacity", [
     (5, 8, 2, 128, 192, "gelu", "bf16", 0), (300, 4, 2, 256, 320, "swiglu", "bf16", 0),
-    (64, 4, 2, 128, 256, "silu", "f32", 0), (900, 3, 2, 192, 256, "relu", "bf16", 500)])
+    (64, 4, 2, 128, 256, "silu", "f32", 0), (900, 3, 2, 192, 256, "relu", "bf16", 500),
+    (700, 16, 2, 576, 640, "swiglu", "bf16", 0)])
 def test_a_training_step(T, N, k, d, F, act, dtype, capacity):
     """Every output of the chain against float64, the saved activations being
     the only 8-bit values: the 2-norms differ by at most 2^-6 (bf16: six
@@ -609,7 +619,7 @@ def test_a_step_replays_from_a_graph():
     """Captured once, replayed with other inputs between eager work; two
     graphs with workspaces of their own; every replay equals the eager step."""
     say("[step] graph")
-    for shape in ((6, 8, 2, 128, 192), (400, 4, 2, 256, 320)):
+    for shape in ((6, 8, 2, 128, 192), (400, 4, 2, 256, 320), (500, 16, 2, 576, 640)):
         a, b = Mlp(*shape, act="swiglu", seed=1), Mlp(*shape, act="gelu", seed=2)
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
