@@ -14,10 +14,17 @@
 namespace moe {
 namespace {
 
-constexpr int kSlots = 4;  // rows whose loads are in flight together
+// Threads of a token's workgroup: each takes 8 columns at a time, in as few
+// passes as 512 threads need, with no wavefront idle in the last one.
+inline int token_threads(int d) {
+  const int chunks = d / 8, passes = (chunks + 511) / 512;
+  return ((chunks + passes - 1) / passes + 63) / 64 * 64;
+}
 
-template <typename T>
-__global__ __launch_bounds__(256) void combine_rows_kernel(const T* __restrict__ rows,
+// KS: slots whose rows are asked for together.  Rows are read once: past the
+// caches.
+template <typename T, int KS>
+__global__ __launch_bounds__(512) void combine_rows_kernel(const T* __restrict__ rows,
                                                            const int32_t* __restrict__ slot_row,
                                                            const float* __restrict__ gate,
                                                            int n_rows, int k, int d,
@@ -25,66 +32,68 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(const T* __restrict__
   const size_t t = blockIdx.x;
   const int32_t* sr = slot_row + t * k;
   const float* gt = gate != nullptr ? gate + t * k : nullptr;
-  for (int c = threadIdx.x * 8; c < d; c += 256 * 8) {
+  for (int c = threadIdx.x * 8; c < d; c += blockDim.x * 8) {
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    for (int s0 = 0; s0 < k; s0 += kSlots) {
-      float v[kSlots][8], w[kSlots];
-      bool on[kSlots];
+    for (int s0 = 0; s0 < k; s0 += KS) {
+      Raw8<T> v[KS];
+      float w[KS];
+      bool on[KS];
 #pragma unroll
-      for (int q = 0; q < kSlots; ++q) {
+      for (int q = 0; q < KS; ++q) {
         const int r = s0 + q < k ? sr[s0 + q] : -1;
-        on[q] = r >= 0 && r < n_rows;
+        on[q] = r >= 0 && r < n_rows;  // uniform over the workgroup
         w[q] = 1.f;
-        if (!on[q]) continue;  // uniform over the workgroup
+        if (!on[q]) continue;
         if (gt != nullptr) w[q] = gt[s0 + q];
-        load8<T>(rows + static_cast<size_t>(r) * d + c, v[q]);
+        v[q].load(rows + static_cast<size_t>(r) * d + c);
       }
 #pragma unroll
-      for (int q = 0; q < kSlots; ++q) {
+      for (int q = 0; q < KS; ++q) {
         if (!on[q]) continue;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[q], v[q][i], acc[i]);
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[q], v[q].get(i), acc[i]);
       }
     }
     store8<T>(y + t * d + c, acc);
   }
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void combine_rows_backward_kernel(
+template <typename T, int KS>
+__global__ __launch_bounds__(512) void combine_rows_backward_kernel(
     const T* __restrict__ rows, const int32_t* __restrict__ slot_row,
     const float* __restrict__ gate, const T* __restrict__ dy, int n_rows, int k, int d,
     T* __restrict__ drows, float* __restrict__ dgate) {
-  __shared__ float s_dot[kSlots][4];
+  __shared__ float s_dot[KS][8];
   const size_t t = blockIdx.x;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int32_t* sr = slot_row + t * k;
-  for (int s0 = 0; s0 < k; s0 += kSlots) {
-    int row[kSlots];
-    float w[kSlots], dot[kSlots];
+  for (int s0 = 0; s0 < k; s0 += KS) {
+    int row[KS];
+    float w[KS], dot[KS];
 #pragma unroll
-    for (int q = 0; q < kSlots; ++q) {
+    for (int q = 0; q < KS; ++q) {
       const int r = s0 + q < k ? sr[s0 + q] : -1;
       row[q] = r < n_rows ? r : -1;
       w[q] = gate != nullptr && row[q] >= 0 ? gate[t * k + s0 + q] : 1.f;
       dot[q] = 0.f;
     }
-    for (int c = threadIdx.x * 8; c < d; c += 256 * 8) {
-      float g[8], v[kSlots][8];
-      load8<T>(dy + t * d + c, g);
+    for (int c = threadIdx.x * 8; c < d; c += blockDim.x * 8) {
+      float g[8];
+      Raw8<T> v[KS];
       if (dgate != nullptr) {
 #pragma unroll
-        for (int q = 0; q < kSlots; ++q)
-          if (row[q] >= 0) load8<T>(rows + static_cast<size_t>(row[q]) * d + c, v[q]);
+        for (int q = 0; q < KS; ++q)
+          if (row[q] >= 0) v[q].load(rows + static_cast<size_t>(row[q]) * d + c);
       }
+      load8<T>(dy + t * d + c, g);
 #pragma unroll
-      for (int q = 0; q < kSlots; ++q) {
+      for (int q = 0; q < KS; ++q) {
         if (row[q] < 0) continue;  // uniform over the workgroup
         if (dgate != nullptr) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot[q] = fmaf(g[i], v[q][i], dot[q]);
+          for (int i = 0; i < 8; ++i) dot[q] = fmaf(g[i], v[q].get(i), dot[q]);
         }
         if (drows != nullptr) {
           float o[8];
@@ -96,16 +105,17 @@ __global__ __launch_bounds__(256) void combine_rows_backward_kernel(
     }
     if (dgate == nullptr) continue;
 #pragma unroll
-    for (int q = 0; q < kSlots; ++q) {
+    for (int q = 0; q < KS; ++q) {
       float v = dot[q];
 #pragma unroll
       for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
       if (lane == 0) s_dot[q][wave] = v;
     }
     __syncthreads();
-    if (threadIdx.x < kSlots && s0 + static_cast<int>(threadIdx.x) < k) {
-      const float* p = s_dot[threadIdx.x];
-      dgate[t * k + s0 + threadIdx.x] = ((p[0] + p[1]) + p[2]) + p[3];
+    if (threadIdx.x < KS && s0 + static_cast<int>(threadIdx.x) < k) {
+      float v = 0.f;
+      for (int i = 0; i < waves; ++i) v += s_dot[threadIdx.x][i];
+      dgate[t * k + s0 + threadIdx.x] = v;
     }
     __syncthreads();
   }
@@ -130,34 +140,49 @@ hipError_t launch_gather_rows(const LinearArgs& g, void* xg, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename T>
+static hipError_t combine_t(const void* rows, const int32_t* slot_row, const float* gate,
+                            int n_rows, int T_, int k, int d, void* y, hipStream_t s) {
+  auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(T_), dim3(token_threads(d)), 0, s,
+                       static_cast<const T*>(rows), slot_row, gate, n_rows, k, d,
+                       static_cast<T*>(y));
+    return hipGetLastError();
+  };
+  if (k <= 2) return run(combine_rows_kernel<T, 2>);
+  if (k <= 4) return run(combine_rows_kernel<T, 4>);
+  return run(combine_rows_kernel<T, 8>);
+}
+
 hipError_t launch_combine_rows(int dtype, const void* rows, const int32_t* slot_row,
                                const float* gate, int n_rows, int T_, int k, int d, void* y,
                                hipStream_t s) {
-  if (dtype == 1)
-    hipLaunchKernelGGL(combine_rows_kernel<bf16_t>, dim3(T_), dim3(256), 0, s,
-                       static_cast<const bf16_t*>(rows), slot_row, gate, n_rows, k, d,
-                       static_cast<bf16_t*>(y));
-  else
-    hipLaunchKernelGGL(combine_rows_kernel<float>, dim3(T_), dim3(256), 0, s,
-                       static_cast<const float*>(rows), slot_row, gate, n_rows, k, d,
-                       static_cast<float*>(y));
-  return hipGetLastError();
+  return dtype == 1 ? combine_t<bf16_t>(rows, slot_row, gate, n_rows, T_, k, d, y, s)
+                    : combine_t<float>(rows, slot_row, gate, n_rows, T_, k, d, y, s);
+}
+
+template <typename T>
+static hipError_t combine_backward_t(const void* rows, const int32_t* slot_row, const float* gate,
+                                     const void* dy, int n_rows, int T_, int k, int d, void* drows,
+                                     float* dgate, hipStream_t s) {
+  auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(T_), dim3(token_threads(d)), 0, s,
+                       static_cast<const T*>(rows), slot_row, gate, static_cast<const T*>(dy),
+                       n_rows, k, d, static_cast<T*>(drows), dgate);
+    return hipGetLastError();
+  };
+  if (k <= 2) return run(combine_rows_backward_kernel<T, 2>);
+  if (k <= 4) return run(combine_rows_backward_kernel<T, 4>);
+  return run(combine_rows_backward_kernel<T, 8>);
 }
 
 hipError_t launch_combine_rows_backward(int dtype, const void* rows, const int32_t* slot_row,
                                         const float* gate, const void* dy, int n_rows, int T_,
                                         int k, int d, void* drows, float* dgate, hipStream_t s) {
-  if (dtype == 1)
-    hipLaunchKernelGGL(combine_rows_backward_kernel<bf16_t>, dim3(T_), dim3(256), 0, s,
-                       static_cast<const bf16_t*>(rows), slot_row, gate,
-                       static_cast<const bf16_t*>(dy), n_rows, k, d, static_cast<bf16_t*>(drows),
-                       dgate);
-  else
-    hipLaunchKernelGGL(combine_rows_backward_kernel<float>, dim3(T_), dim3(256), 0, s,
-                       static_cast<const float*>(rows), slot_row, gate,
-                       static_cast<const float*>(dy), n_rows, k, d, static_cast<float*>(drows),
-                       dgate);
-  return hipGetLastError();
+  return dtype == 1 ? combine_backward_t<bf16_t>(rows, slot_row, gate, dy, n_rows, T_, k, d, drows,
+                                                 dgate, s)
+                    : combine_backward_t<float>(rows, slot_row, gate, dy, n_rows, T_, k, d, drows,
+                                                dgate, s);
 }
 
 }  // namespace moe

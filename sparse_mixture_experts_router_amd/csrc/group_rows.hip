@@ -22,7 +22,7 @@
 namespace moe {
 namespace {
 
-constexpr int kGThreads = 512, kGWaves = kGThreads / 64;
+constexpr int kGThreads = 1024, kGWaves = kGThreads / 64;
 constexpr int kMaxBlocks = 256;
 
 // Lanes of the wavefront that hold the same key (0 <= key < 1024).
@@ -35,7 +35,7 @@ __device__ __forceinline__ unsigned long long same_key(int key, int bits) {
   return m;
 }
 
-// Range of workgroup b: whole 512-pair chunks, equally many in every range
+// Range of workgroup b: whole chunks of kGThreads pairs, equally many in every range
 // but the last.
 __device__ __forceinline__ void block_range(long n, int blocks, int b, long& lo, long& hi) {
   const long chunks = (n + kGThreads - 1) / kGThreads;
@@ -77,25 +77,40 @@ __global__ __launch_bounds__(kGThreads) void group_rows_kernel(
   __shared__ int s_off[kMaxExperts];   // offsets
   __shared__ int s_wave[kGWaves][kMaxExperts];  // counts of a chunk by wavefront
   __shared__ int s_part[kGWaves];
+  __shared__ int s_tot[kGThreads], s_bef[kGThreads];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   long lo, hi;
   block_range(n, gridDim.x, blockIdx.x, lo, hi);
 
-  // totals, and the counts of the ranges before this one; N <= 512 = threads
+  // Totals, and the counts of the ranges before this one (N <= 512 < threads):
+  // kGThreads / N threads share an expert's column of the table, 8 loads of
+  // each in flight.
   int total = 0, before = 0;
   if (TABLE) {
-    if (tid < N)
-      for (int b0 = 0; b0 < static_cast<int>(gridDim.x); b0 += 8) {
+    const int parts = kGThreads / N, nb = gridDim.x, me = blockIdx.x;
+    const int e = tid % N, part = tid / N;
+    const int per = (nb + parts - 1) / parts;
+    if (part < parts) {
+      const int b1 = min(nb, (part + 1) * per);
+      for (int b0 = part * per; b0 < b1; b0 += 8) {
         int v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          v[i] = b0 + i < static_cast<int>(gridDim.x) ? table[static_cast<size_t>(b0 + i) * N + tid]
-                                                      : 0;
+          v[i] = b0 + i < b1 ? table[static_cast<size_t>(b0 + i) * N + e] : 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           total += v[i];
-          if (b0 + i < static_cast<int>(blockIdx.x)) before += v[i];
+          if (b0 + i < me) before += v[i];
         }
+      }
+    }
+    s_tot[tid] = total;
+    s_bef[tid] = before;
+    __syncthreads();
+    if (tid < N)
+      for (int p = 1; p < parts; ++p) {
+        total += s_tot[p * N + tid];
+        before += s_bef[p * N + tid];
       }
   } else {
     count_range(idx, lo, hi, N, s_run);
@@ -161,10 +176,10 @@ __global__ __launch_bounds__(kGThreads) void group_rows_kernel(
 
 }  // namespace
 
-// One range up to 4096 pairs, then about 2048 pairs a range, at most 256 ranges.
+// One range up to 2048 pairs, then about 1024 pairs a range, at most 256 ranges.
 int group_blocks(long n) {
-  if (n <= 4096) return 1;
-  const long b = (n + 2047) / 2048;
+  if (n <= 2048) return 1;
+  const long b = (n + 1023) / 1024;
   return static_cast<int>(b < kMaxBlocks ? b : kMaxBlocks);
 }
 
