@@ -14,21 +14,24 @@
 namespace moe {
 namespace {
 
-constexpr int kUnroll = 4;  // 8-column chunks of one thread, loaded before the first is used
+// 8-column chunks of one thread, loaded before the first is used.  Packing 2 /
+// 4 / 8: 4096 x 4096 bf16 12.0 / 11.0 / 12.6 us; unpacking 8192 x 28672 112.6 /
+// 115.2 / 115.4.
+constexpr int kPackUnroll = 4, kUnpackUnroll = 2;
 
 template <typename T>
 __global__ __launch_bounds__(256) void pack_kernel(const T* __restrict__ x, long chunks,
                                                    uint8_t* __restrict__ codes,
                                                    float* __restrict__ scale) {
-  const long c0 = static_cast<long>(blockIdx.x) * (256 * kUnroll) + threadIdx.x;
-  float v[kUnroll][8];
+  const long c0 = static_cast<long>(blockIdx.x) * (256 * kPackUnroll) + threadIdx.x;
+  float v[kPackUnroll][8];
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
+  for (int i = 0; i < kPackUnroll; ++i) {
     const long c = c0 + 256 * i;
     load8<T>(x + (c < chunks ? c : 0) * 8, v[i]);
   }
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
+  for (int i = 0; i < kPackUnroll; ++i) {
     const long c = c0 + 256 * i;  // chunks is a multiple of 8: a block is whole or absent
     pack_block(v[i], c < chunks, codes + c * 8, scale + c / 8);
   }
@@ -38,22 +41,21 @@ template <typename T>
 __global__ __launch_bounds__(256) void unpack_kernel(const uint8_t* __restrict__ codes,
                                                      const float* __restrict__ scale, long chunks,
                                                      T* __restrict__ x) {
-  const long c0 = static_cast<long>(blockIdx.x) * (256 * kUnroll) + threadIdx.x;
-  uint2 q[kUnroll];
-  float s[kUnroll];
+  const long c0 = static_cast<long>(blockIdx.x) * (256 * kUnpackUnroll) + threadIdx.x;
+  uint2 q[kUnpackUnroll];
+  float s[kUnpackUnroll];
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
+  for (int i = 0; i < kUnpackUnroll; ++i) {
     const long c = c0 + 256 * i < chunks ? c0 + 256 * i : 0;
     q[i] = *reinterpret_cast<const uint2*>(codes + c * 8);
     s[i] = scale[c / 8];
   }
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
+  for (int i = 0; i < kUnpackUnroll; ++i) {
     const long c = c0 + 256 * i;
-    if (c >= chunks) return;
     float v[8];
     decode8(q[i], s[i], v);
-    store8<T>(x + c * 8, v);
+    if (c < chunks) store_once8<T>(x + c * 8, v);
   }
 }
 
@@ -185,7 +187,8 @@ constexpr long kMaxBlocks = 1L << 23;  // 2^31 threads of 256-thread workgroups
 
 hipError_t launch_checkpoint_pack(int dtype, const void* x, long rows, int cols, uint8_t* codes,
                                   float* scale, hipStream_t s) {
-  const long chunks = rows * (cols / 8), blocks = (chunks + 256 * kUnroll - 1) / (256 * kUnroll);
+  const long chunks = rows * (cols / 8);
+  const long blocks = (chunks + 256 * kPackUnroll - 1) / (256 * kPackUnroll);
   if (blocks > kMaxBlocks) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks));
   if (dtype == 1)
@@ -199,7 +202,8 @@ hipError_t launch_checkpoint_pack(int dtype, const void* x, long rows, int cols,
 
 hipError_t launch_checkpoint_unpack(int dtype, const uint8_t* codes, const float* scale,
                                     long rows, int cols, void* x, hipStream_t s) {
-  const long chunks = rows * (cols / 8), blocks = (chunks + 256 * kUnroll - 1) / (256 * kUnroll);
+  const long chunks = rows * (cols / 8);
+  const long blocks = (chunks + 256 * kUnpackUnroll - 1) / (256 * kUnpackUnroll);
   if (blocks > kMaxBlocks) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks));
   if (dtype == 1)

@@ -21,8 +21,10 @@ inline int token_threads(int d) {
   return ((chunks + passes - 1) / passes + 63) / 64 * 64;
 }
 
-// KS: slots whose rows are asked for together.  Rows are read once: past the
-// caches.
+// KS: slots whose rows are asked for together.  Rows are read once and results
+// written once, past the caches: 8192 tokens x 8 rows of 7168 219 us with plain
+// loads and stores, 4 slots; 204 with 8 slots and non-temporal loads, 188 with
+// non-temporal stores too (5.6 TB/s).
 template <typename T, int KS>
 __global__ __launch_bounds__(512) void combine_rows_kernel(const T* __restrict__ rows,
                                                            const int32_t* __restrict__ slot_row,
@@ -56,7 +58,7 @@ __global__ __launch_bounds__(512) void combine_rows_kernel(const T* __restrict__
         for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[q], v[q].get(i), acc[i]);
       }
     }
-    store8<T>(y + t * d + c, acc);
+    store_once8<T>(y + t * d + c, acc);
   }
 }
 
@@ -99,7 +101,7 @@ __global__ __launch_bounds__(512) void combine_rows_backward_kernel(
           float o[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = w[q] * g[i];
-          store8<T>(drows + static_cast<size_t>(row[q]) * d + c, o);
+          store_once8<T>(drows + static_cast<size_t>(row[q]) * d + c, o);
         }
       }
     }

@@ -141,7 +141,7 @@ moe_status check_checkpoint(int64_t rows, int32_t cols, int32_t dtype, const voi
   if (rows < 0 || cols <= 0) return fail(MOE_ERR_INVALID_ARG, "bad rows or cols");
   if (check_dtype(dtype) != MOE_OK) return MOE_ERR_INVALID_ARG;
   if (cols % kCkptBlock != 0) return fail(MOE_ERR_UNSUPPORTED, "cols must be a multiple of 64");
-  if (rows > (int64_t{1} << 36) / cols) return fail(MOE_ERR_UNSUPPORTED, "rows * cols too large");
+  if (rows > (int64_t{1} << 35) / cols) return fail(MOE_ERR_UNSUPPORTED, "rows * cols too large");
   if (rows == 0) return MOE_OK;
   if (x == nullptr || codes == nullptr || scale == nullptr)
     return fail(MOE_ERR_INVALID_ARG, "x, codes or scale is NULL");
