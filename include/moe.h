@@ -421,7 +421,7 @@ typedef enum {
 /* A linear map for each of `groups` groups of rows.  z_dim = out_dim, or
  * 2 out_dim with MOE_ACT_SWIGLU, is the number of rows of a group's weights.
  * One group is an ordinary dense product.  groups <= 512, in_dim and out_dim
- * multiples of 64 up to 2^20, rows < 2^30; MOE_WEIGHTS_FP8_E4M3 needs
+ * multiples of 64 up to 2^20, rows < 2^27; MOE_WEIGHTS_FP8_E4M3 needs
  * MOE_BF16. */
 typedef struct {
   int32_t rows;          /* rows of y (and of residual, dy, dx, the checkpoint)       */
@@ -507,7 +507,7 @@ moe_status moe_checkpoint_unpack(int64_t rows, int32_t cols, int32_t dtype,
 /* y[t] = sum_s gate[t, s] rows[slot_row[t, s]] over the slots that have a row
  * (gate NULL: 1), summed in fp32 in slot order.  rows [n_rows, d], slot_row
  * and gate [T, k], y [T, d]; a slot_row outside [0, n_rows) is a slot without
- * a row.  d a multiple of 64, k <= 16.  y must not overlap rows. */
+ * a row.  d a multiple of 64, k <= 16, T < 2^23.  y must not overlap rows. */
 moe_status moe_combine(int32_t T, int32_t k, int32_t n_rows, int32_t d, int32_t dtype,
                        const void* rows, const int32_t* slot_row, const float* gate, void* y,
                        void* stream);

@@ -181,7 +181,7 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(LinearArgs g,
   dbias[static_cast<size_t>(e) * g.z_dim + n] = acc;
 }
 
-constexpr long kMaxBlocks = 1L << 23;  // 2^31 threads of 256-thread workgroups
+constexpr long kMaxBlocks = (1L << 24) - 1;  // below 2^32 threads of 256-thread workgroups
 
 }  // namespace
 

@@ -123,21 +123,34 @@ __global__ __launch_bounds__(512) void combine_rows_backward_kernel(
   }
 }
 
-// One wavefront per row.
+// A wavefront copies kGatherRows rows, one chunk of each in flight together.
+constexpr int kGatherRows = 4;
 __global__ __launch_bounds__(256) void gather_rows_kernel(LinearArgs g, bf16_t* __restrict__ xg) {
-  const int r = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (r >= min(g.offsets[g.groups], g.rows)) return;
-  const size_t src = min(max(g.row_index[r], 0), g.x_rows - 1);
-  const bf16_t* const x = static_cast<const bf16_t*>(g.x) + src * g.in_dim;
-  bf16_t* const o = xg + static_cast<size_t>(r) * g.in_dim;
-  for (int c = lane * 8; c < g.in_dim; c += 512)
-    *reinterpret_cast<u32x4*>(o + c) = *reinterpret_cast<const u32x4*>(x + c);
+  const int r0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * kGatherRows, lane = threadIdx.x & 63;
+  const int n = min(g.offsets[g.groups], g.rows) - r0;  // rows of x left
+  if (n <= 0) return;
+  const bf16_t* x[kGatherRows];
+#pragma unroll
+  for (int i = 0; i < kGatherRows; ++i) {
+    const size_t src = min(max(g.row_index[r0 + min(i, n - 1)], 0), g.x_rows - 1);
+    x[i] = static_cast<const bf16_t*>(g.x) + src * g.in_dim;
+  }
+  bf16_t* const o = xg + static_cast<size_t>(r0) * g.in_dim;
+  for (int c = lane * 8; c < g.in_dim; c += 512) {
+    u32x4 v[kGatherRows];
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i) v[i] = *reinterpret_cast<const u32x4*>(x[i] + c);
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i)
+      if (i < n) *reinterpret_cast<u32x4*>(o + static_cast<size_t>(i) * g.in_dim + c) = v[i];
+  }
 }
 
 }  // namespace
 
 hipError_t launch_gather_rows(const LinearArgs& g, void* xg, hipStream_t s) {
-  hipLaunchKernelGGL(gather_rows_kernel, dim3((g.rows + 3) / 4), dim3(256), 0, s, g,
+  hipLaunchKernelGGL(gather_rows_kernel, dim3((g.rows + 4 * kGatherRows - 1) / (4 * kGatherRows)),
+                     dim3(256), 0, s, g,
                      static_cast<bf16_t*>(xg));
   return hipGetLastError();
 }

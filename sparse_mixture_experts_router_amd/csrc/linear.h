@@ -52,7 +52,12 @@ hipError_t launch_linear_dw_tile(int dtype, const LinearArgs& g, const void* dz,
                                  hipStream_t s);
 
 // Forward for few rows a group: 32-row tiles, W streamed through registers.
-hipError_t launch_linear_rows(int dtype, bool wfp8, const LinearArgs& g, int cus, hipStream_t s);
+// linear_rows_parts: shares of K that the launch is split into; more than one
+// takes partial [parts, rows, z_dim].
+bool linear_rows_fits(const LinearArgs& g);
+int linear_rows_parts(int elem_bytes, const LinearArgs& g, int cus);
+hipError_t launch_linear_rows(int dtype, bool wfp8, const LinearArgs& g, int cus, float* partial,
+                              hipStream_t s);
 // The same three on 256 x 256 tiles (bf16; forward: weights in bf16 or FP8):
 // dW takes x's rows in order, without row_index.
 bool linear_mfma_fits(bool wfp8, const LinearArgs& g);

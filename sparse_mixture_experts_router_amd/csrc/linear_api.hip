@@ -38,7 +38,7 @@ moe_status check_linear(const moe_linear_config* c) {
     return fail(MOE_ERR_UNSUPPORTED, "in_dim and out_dim must be multiples of 64");
   if (c->in_dim > (1 << 20) || c->out_dim > (1 << 20))
     return fail(MOE_ERR_UNSUPPORTED, "in_dim or out_dim > 2^20");
-  if (c->rows >= (1 << 30) || c->x_rows >= (1 << 30))
+  if (c->rows >= (1 << 27) || c->x_rows >= (1 << 30))
     return fail(MOE_ERR_UNSUPPORTED, "too many rows");
   // grids: at most 2^23 tiles of 128 rows by 64 columns (forward and dX), or
   // of 128 by 128 (dW)
@@ -87,6 +87,13 @@ long few_rows(const moe_linear_config& c) {
   return c.weight_format == MOE_WEIGHTS_FP8_E4M3 ? 12 : 8;
 }
 
+bool streams_rows(const moe_linear_config& c, const LinearArgs& g) {
+  return c.rows <= few_rows(c) * c.groups && linear_rows_fits(g);
+}
+int rows_parts(const moe_linear_config& c, const LinearArgs& g) {
+  return linear_rows_parts(c.dtype == MOE_BF16 ? 2 : 4, g, device_cus());
+}
+
 // Whether a bf16 product has enough 256 x 256 tiles for the large-tile kernel
 // (linear_mfma.hip): with no more than an eighth of the compute units, the 64
 // x 64 tiles of linear_tile.hip spread it over more of them.  Backward, us with
@@ -132,7 +139,7 @@ moe_status check_combine(int32_t T, int32_t k, int32_t n_rows, int32_t d, int32_
   if (check_dtype(dtype) != MOE_OK) return MOE_ERR_INVALID_ARG;
   if (k > kMaxTopK) return fail(MOE_ERR_UNSUPPORTED, "top_k > 16");
   if (d % 64 != 0) return fail(MOE_ERR_UNSUPPORTED, "d must be a multiple of 64");
-  if (T >= (1 << 24)) return fail(MOE_ERR_UNSUPPORTED, "T >= 2^24");
+  if (T >= (1 << 23)) return fail(MOE_ERR_UNSUPPORTED, "T >= 2^23");
   return MOE_OK;
 }
 
@@ -182,7 +189,9 @@ moe_status moe_group_rows(int32_t T, int32_t N, int32_t k, int32_t capacity,
 
 size_t moe_linear_workspace_size(const moe_linear_config* cfg) {
   if (check_linear(cfg) != MOE_OK) return 0;
-  return kAlign;
+  const LinearArgs g = linear_args(*cfg);
+  const int parts = streams_rows(*cfg, g) ? rows_parts(*cfg, g) : 1;
+  return parts > 1 ? align_up(static_cast<size_t>(parts) * g.rows * g.z_dim * 4) : kAlign;
 }
 
 moe_status moe_grouped_linear(const moe_linear_config* cfg, const moe_linear_args* a,
@@ -218,8 +227,8 @@ moe_status moe_grouped_linear(const moe_linear_config* cfg, const moe_linear_arg
   g.z_scale = a->z_scale;
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t err;
-  if (c.rows <= few_rows(c) * c.groups)
-    err = launch_linear_rows(c.dtype, fp8, g, device_cus(), s);
+  if (streams_rows(c, g))
+    err = launch_linear_rows(c.dtype, fp8, g, device_cus(), static_cast<float*>(workspace), s);
   else if (c.dtype == MOE_BF16 && large_tiles(row_tiles(c), g.z_dim) && linear_mfma_fits(fp8, g))
     err = launch_linear_mfma(fp8, g, s);
   else

@@ -235,6 +235,11 @@ FORWARD = [
     ([511, 1, 300], 512, 448, "swiglu", dict(gather=True, bias=True, spare=9)),
     ([260, 513], 1024, 256, "gelu", dict()),
     ([2, 300, 0, 1], 640, 320, "silu", dict(bias=True, gather=True)),
+    # few workgroups and a long K: split over K, joined by a second launch
+    ([1, 0, 3], 1024, 192, "gelu", dict(bias=True, residual=True)),
+    ([2, 5, 0, 1], 1152, 128, "swiglu", dict(gather=True, bias=True, spare=3)),
+    ([0, 30, 17], 2112, 64, "none", dict(spare=70)),
+    ([1], 4096, 64, "silu", dict(bias=True)),
     # enough 256 x 256 tiles (more than an eighth of the compute units) for the
     # large-tile kernel in every product, groups of all fillings
     (RAGGED, 448, 1088, "silu", dict(gather=True, bias=True)),
@@ -325,8 +330,8 @@ def test_offsets_are_clamped(rows, groups):
 
 def test_results_repeat_and_streams_do_not_matter():
     say("[linear] repeat, another stream")
-    for sizes, F in (([3, 17, 0, 9], 192), ([300, 40, 600], 192), (RAGGED, 576)):
-        c = Case(sizes, 256 if F == 192 else 512, F, "swiglu", gather=True, bias=True)
+    for sizes, F in (([3, 17, 0, 9], 192), ([300, 40, 600], 192), (RAGGED, 576), ([2, 1], 128)):
+        c = Case(sizes, {192: 256, 576: 512, 128: 2048}[F], F, "swiglu", gather=True, bias=True)
         y0, codes, scale = c.forward(True)
         torch.cuda.synchronize()
         side = torch.cuda.Stream()
@@ -554,7 +559,7 @@ class Mlp:
 @pytest.mark.parametrize("T,N,k,d,F,act,dtype,capacity", [
     (5, 8, 2, 128, 192, "gelu", "bf16", 0), (300, 4, 2, 256, 320, "swiglu", "bf16", 0),
     (64, 4, 2, 128, 256, "silu", "f32", 0), (900, 3, 2, 192, 256, "relu", "bf16", 500),
-    (700, 16, 2, 576, 640, "swiglu", "bf16", 0)])
+    (700, 16, 2, 576, 640, "swiglu", "bf16", 0), (3, 4, 2, 1088, 1024, "gelu", "bf16", 0)])
 def test_a_training_step(T, N, k, d, F, act, dtype, capacity):
     """Every output of the chain against float64, the saved activations being
     the only 8-bit values: the 2-norms differ by at most 2^-6 (bf16: six
@@ -619,7 +624,8 @@ def test_a_step_replays_from_a_graph():
     """Captured once, replayed with other inputs between eager work; two
     graphs with workspaces of their own; every replay equals the eager step."""
     say("[step] graph")
-    for shape in ((6, 8, 2, 128, 192), (400, 4, 2, 256, 320), (500, 16, 2, 576, 640)):
+    for shape in ((6, 8, 2, 128, 192), (400, 4, 2, 256, 320), (500, 16, 2, 576, 640),
+                  (3, 4, 2, 1024, 1152)):
         a, b = Mlp(*shape, act="swiglu", seed=1), Mlp(*shape, act="gelu", seed=2)
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())

@@ -53,10 +53,10 @@ BAD_CONFIGS = [
     (dict(in_dim=0), INVALID), (dict(out_dim=-64), INVALID), (dict(dtype=2), INVALID),
     (dict(weight_format=2), INVALID), (dict(activation=5), INVALID), (dict(activation=-1), INVALID),
     (dict(groups=513), UNSUPPORTED), (dict(in_dim=96), UNSUPPORTED), (dict(out_dim=100), UNSUPPORTED),
-    (dict(in_dim=(1 << 20) + 64), UNSUPPORTED), (dict(rows=1 << 30), UNSUPPORTED),
+    (dict(in_dim=(1 << 20) + 64), UNSUPPORTED), (dict(rows=1 << 27), UNSUPPORTED),
     (dict(x_rows=1 << 30), UNSUPPORTED),
     (dict(dtype=moe.MOE_F32, weight_format=moe.MOE_WEIGHTS_FP8_E4M3), UNSUPPORTED),
-    (dict(rows=(1 << 30) - 1, out_dim=1 << 20), UNSUPPORTED),          # too many tiles
+    (dict(rows=(1 << 27) - 1, out_dim=1 << 20), UNSUPPORTED),          # too many tiles
     (dict(groups=512, in_dim=1 << 20, out_dim=1 << 20), UNSUPPORTED),  # too many tiles of dw
 ]
 
@@ -197,7 +197,7 @@ def test_combine_refusals():
         assert call(T=-1) == INVALID and call(k=0) == INVALID and call(n=-1) == INVALID
         assert call(d=0) == INVALID and call(dt=4) == INVALID
         assert call(d=96) == UNSUPPORTED and call(k=17) == UNSUPPORTED
-        assert call(T=1 << 24) == UNSUPPORTED
+        assert call(T=1 << 23) == UNSUPPORTED
         assert call(rows=None) == INVALID and call(slot=None) == INVALID
         assert call(rows=FAKE + 8) == INVALID
         assert call(T=0) == moe.MOE_OK
