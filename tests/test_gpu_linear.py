@@ -348,6 +348,112 @@ def test_results_repeat_and_streams_do_not_matter():
             assert torch.equal(g0[n].view(torch.uint8), g1[n].view(torch.uint8))
 
 
+@pytest.mark.parametrize("sizes,K,F", [([3, 4, 2, 6, 1], 64, 64), (RAGGED, 512, 576)],
+                         ids=["few", "many"])
+def test_a_range_of_experts(sizes, K, F):
+    """A call on some of the experts: offsets that start past row 0 and end
+    before the last row.  The other rows are left as they were."""
+    say(f"[linear] experts 1 .. {len(sizes) - 2} of {len(sizes)}")
+    c = Case(sizes, K, F, "gelu", gather=True, bias=True)
+    y0, codes0, scale0 = c.forward(True)
+    g0 = c.check_backward("all", codes0, scale0)
+    G = len(sizes) - 2
+    a, b = int(c.off[1]), int(c.off[G + 1])
+    cfg = moe.make_linear_config(c.rows, G, K, F, activation="gelu", x_rows=c.x_rows)
+    off, w, bias = c.offsets[1:G + 2], c.w[1:G + 1], c.bias[1:G + 1]
+    y, codes = poison((c.rows, F), c.dt), poison((c.rows, c.zd), torch.uint8)
+    scale = poison((c.rows, c.zd // 64), torch.float32)
+    moe.moe_grouped_linear(cfg, c.x, off, w, y, row_index=c.index, bias=bias, z_codes=codes,
+                           z_scale=scale, workspace=workspace(moe.alloc_linear_workspace(cfg)))
+    out = {"dx": poison((c.rows, K), c.dt), "dw": poison((G, c.zd, K), c.dt),
+           "dbias": poison((G, c.zd), torch.float32)}
+    moe.moe_grouped_linear_backward(
+        cfg, c.x, off, w, c.dy, row_index=c.index, z_codes=codes, z_scale=scale,
+        workspace=workspace(moe.alloc_linear_backward_workspace(cfg)), **out)
+    torch.cuda.synchronize()
+    r = to_np(y[a:b]).astype(np.float64) - to_np(y0[a:b])  # another kernel may take fewer experts
+    assert np.abs(r).max(initial=0) <= 2 * V * np.abs(to_np(y0[a:b])).max(initial=0)
+    assert bool(torch.isnan(y[:a]).all()) and bool(torch.isnan(y[b:]).all())
+    assert bool((codes[:a] == 0x7F).all()) and bool((codes[b:] == 0x7F).all())
+    assert bool(torch.isnan(out["dx"][:a]).all()) and bool(torch.isnan(out["dx"][b:]).all())
+    for n, part in (("dx", slice(a, b)), ("dw", slice(1, G + 1)), ("dbias", slice(1, G + 1))):
+        got = out[n][part] if n == "dx" else out[n]
+        ref = to_np(g0[n][part]).astype(np.float64)
+        assert np.linalg.norm(to_np(got) - ref) <= 2 ** -6 * np.linalg.norm(ref), n
+
+
+@pytest.mark.parametrize("groups", [64, 65, 128, 511, 512])
+def test_many_groups(groups):
+    """As many groups as lanes, one more, and the most there may be, a third
+    of them without rows."""
+    say(f"[linear] {groups} groups")
+    sizes = [(7 * e) % 9 if e % 3 else 0 for e in range(groups)]
+    sizes[-1] = 5
+    c = Case(sizes, 128, 64, "silu", gather=True, spare=2)
+    y, codes, scale = c.check_forward(f"{groups} groups", True)
+    c.check_backward(f"{groups} groups", codes, scale)
+    Case(sizes, 64, 64, "none", "f32").check_backward(f"{groups} groups f32")
+
+
+def test_offsets_past_32_bits():
+    """Arrays of more than 2^31 elements and 4 GiB: the last rows of every
+    output, and the sums over all rows, against fp32 products on the GPU (sums
+    of 64 products; over 70000 rows (70000 / 64 + 64) u of the terms)."""
+    say("[linear] past 32 bits")
+    R, K, F = 70000, 64, 32768
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn((R, K), generator=g, device=DEV).bfloat16()
+    w = (torch.randn((1, F, K), generator=g, device=DEV) * 0.125).bfloat16()
+    off = torch.tensor([0, R], dtype=torch.int32, device=DEV)
+    cfg = moe.make_linear_config(R, 1, K, F, activation="silu")
+    y = poison((R, F), torch.bfloat16)
+    codes, scale = poison((R, F), torch.uint8), poison((R, F // 64), torch.float32)
+    moe.moe_grouped_linear(cfg, x, off, w, y, z_codes=codes, z_scale=scale,
+                           workspace=moe.alloc_linear_workspace(cfg))
+    tail = slice(R - 300, R)
+    z = x[tail].float() @ w[0].float().t()
+    h = z * torch.sigmoid(z)
+    assert bool(((y[tail].float() - h).abs() <= 1.01 * V * h.abs() + 1e-4).all())
+    back = poison((R, F), torch.bfloat16)
+    moe.moe_checkpoint_unpack(codes, scale, back)
+    m = z.abs().reshape(300, -1, 64).amax(2, keepdim=True).expand(-1, -1, 64).reshape(300, F)
+    assert bool(((back[tail].float() - z).abs() <= z.abs() * (1 / 16 + 2 * V) + m / 448 / 512).all())
+    again, ascale = poison((R, F), torch.uint8), poison((R, F // 64), torch.float32)
+    moe.moe_checkpoint_pack(back, again, ascale)
+    e4m3 = torch.float8_e4m3fn
+    zq = again[tail].view(e4m3).float()
+    zq = (zq.reshape(300, -1, 64) * ascale[tail][:, :, None]).reshape(300, F)
+    assert bool(((zq - back[tail].float()).abs() <= back[tail].float().abs() / 8 + m / 448 / 256).all())
+    del again, ascale
+    dy = back  # any values: |dy| of ordinary size
+    dx, dw = poison((R, K), torch.bfloat16), poison((1, F, K), torch.bfloat16)
+    moe.moe_grouped_linear_backward(cfg, x, off, w, dy, z_codes=codes, z_scale=scale, dx=dx, dw=dw,
+                                    workspace=moe.alloc_linear_backward_workspace(cfg))
+    acc, terms = torch.zeros((F, K), device=DEV), torch.zeros((F, K), device=DEV)
+    for i in range(0, R, 1000):
+        r = slice(i, i + 1000)
+        zz = (codes[r].view(e4m3).float().reshape(1000, -1, 64) * scale[r][:, :, None]).reshape(-1, F)
+        p = torch.sigmoid(zz)
+        dz = dy[r].float() * (p + zz * p * (1 - p))
+        acc += dz.t() @ x[r].float()
+        terms += dz.abs().t() @ x[r].float().abs()
+    bound = V * acc.abs() + terms * (2 * V)
+    assert bool(((dw[0].float() - acc).abs() <= bound).all())
+    ref = dz[-300:] @ w[0].float()
+    tx = dz[-300:].abs() @ w[0].float().abs()
+    assert bool(((dx[tail].float() - ref).abs() <= V * ref.abs() + tx * 2 * V).all())
+    # combine: the same rows, two a token
+    slot = torch.arange(R, device=DEV, dtype=torch.int32).reshape(-1, 2)
+    o = poison((R // 2, F), torch.bfloat16)
+    moe.moe_combine(y, slot, o)
+    want = y[tail].float().reshape(150, 2, F).sum(1)
+    assert bool(((o[-150:].float() - want).abs() <= V * want.abs() + 1e-6).all())
+    drows = poison((R, F), torch.bfloat16)
+    moe.moe_combine_backward(y, slot, None, o, drows, None)
+    torch.cuda.synchronize()
+    assert torch.equal(drows[tail], o[-150:].repeat_interleave(2, dim=0))
+
+
 def test_small_and_large_values():
     """Activations where the exponential over- or underflows."""
     say("[linear] extremes")
@@ -595,7 +701,8 @@ def test_a_training_step(T, N, k, d, F, act, dtype, capacity):
 def test_gradients_are_differences():
     """fp32 ReLU experts: the loss is piecewise linear in x, and 8 bits keep a
     pre-activation's sign, so a central difference that crosses no kink is the
-    gradient up to fp32: |L| 2^-20 over a step of 2^-6."""
+    gradient up to fp32: the loss's terms times 2^-20 over the step, and sums
+    of the gradient's products (2^-10 of its terms leaves room)."""
     say("[step] differences")
     m = Mlp(6, 4, 2, 128, 192, "relu", "f32", seed=5)
     v = torch.randn(m.x.shape, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
