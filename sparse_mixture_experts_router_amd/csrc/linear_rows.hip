@@ -278,11 +278,12 @@ hipError_t launch_t(const LinearArgs& g, int cus, float* partial, hipStream_t s)
                        dim3(256), 0, s, g, partial, parts);
     return hipGetLastError();
   }
-  // as many slices of K in a workgroup as give every compute unit 6 wavefronts
-  const long waves = rows_blocks(g) * 4, want = 6L * cus;
-  if (waves >= want) return launch_ks<T, TW, GATED, 1>(g, 1, nullptr, s);
-  if (waves * 2 >= want) return launch_ks<T, TW, GATED, 2>(g, 1, nullptr, s);
-  return launch_ks<T, TW, GATED, 4>(g, 1, nullptr, s);
+  // Two slices of K in a workgroup where one would give a compute unit fewer
+  // than 6 wavefronts.  One / two slices: 448 workgroups (one FP8 token's gate
+  // and up projection) 46.5 / 51.7 us, 224 (8 rows, 4096 -> 2 x 14336) 54 / 49,
+  // 170 (2 rows, 8192 -> 2 x 10880) 92 / 76; four measured as two.
+  if (rows_blocks(g) * 4 >= 6L * cus) return launch_ks<T, TW, GATED, 1>(g, 1, nullptr, s);
+  return launch_ks<T, TW, GATED, 2>(g, 1, nullptr, s);
 }
 
 }  // namespace
