@@ -13,10 +13,11 @@
 //
 // One workgroup owns a B x B tile of one group (B = 128, or 64 where the
 // larger tiles would leave compute units without work), its 4 wavefronts a
-// quarter each; a K step is 128 bytes of every row, fetched into registers while the step
-// before it is multiplied out of the other of two LDS buffers.  Rows past a
-// group's end repeat its last row (results not written); K-rows past it are
-// zeros in both operands, so that no NaN of a neighbouring group enters.
+// quarter each; a K step is 128 bytes of every row, fetched into registers one
+// or two steps before it is multiplied out of one of two LDS buffers.  Rows
+// past a group's end repeat its last row (results not written); K-rows past it
+// are zeros in both operands, so that no NaN of a neighbouring group enters.
+// fp32 reaches 75-82 of the 153 TFLOP/s of a large library product.
 #include <algorithm>
 #include <type_traits>
 
@@ -28,7 +29,8 @@ namespace {
 
 constexpr int kFwd = 0, kDx = 1, kDw = 2;
 
-// One operand tile: L x 32 rows of 128 bytes, L 16-byte chunks a thread.
+// One operand tile: L x 32 rows of 128 bytes, L 16-byte chunks a thread, held
+// for two K steps (slots P).
 template <typename T, typename TW, bool KROW, int L>
 struct Operand;
 
@@ -37,24 +39,26 @@ struct Operand;
 template <typename T, typename TW, int L>
 struct Operand<T, TW, false, L> {
   static constexpr int CB = 16 * static_cast<int>(sizeof(TW)) / static_cast<int>(sizeof(T));
+  static constexpr bool FP8 = sizeof(TW) != sizeof(T);
   const char* p[L];
-  u32x4 v[L];
-  __device__ __forceinline__ void load(int step) {
+  int steps;  // K steps there are (a load past them repeats the last)
+  u32x4 v[2][FP8 ? 1 : L];
+  uint2 c8[2][FP8 ? L : 1];  // codes, widened on their way into LDS
+  template <int P> __device__ __forceinline__ void load(int step) {
+    const size_t off = static_cast<size_t>(min(step, steps - 1)) * 8 * CB;
 #pragma unroll
     for (int i = 0; i < L; ++i) {
-      const char* q = p[i] + static_cast<size_t>(step) * 8 * CB;
-      if constexpr (sizeof(TW) == sizeof(T)) {
-        v[i] = *reinterpret_cast<const u32x4*>(q);
-      } else {
-        v[i] = e4m3x8_to_bf16(*reinterpret_cast<const uint2*>(q));
-      }
+      if constexpr (FP8) c8[P][i] = *reinterpret_cast<const uint2*>(p[i] + off);
+      else v[P][i] = *reinterpret_cast<const u32x4*>(p[i] + off);
     }
   }
-  __device__ __forceinline__ void store(char* lds) const {
+  template <int P> __device__ __forceinline__ void store(char* lds) const {
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       const int c = threadIdx.x + 256 * i;
-      *reinterpret_cast<u32x4*>(lds + lds_swz(c >> 3, c & 7)) = v[i];
+      u32x4* const d = reinterpret_cast<u32x4*>(lds + lds_swz(c >> 3, c & 7));
+      if constexpr (FP8) *d = e4m3x8_to_bf16(c8[P][i]);
+      else *d = v[P][i];
     }
   }
 };
@@ -68,25 +72,25 @@ struct Operand<T, T, true, L> {
   int cols, krows;            // columns of the operand from the tile's first; K-rows there are
   const int32_t* index;       // source row of K-row j, or null
   int index_rows;             // rows the index may name
-  u32x4 v[L];
-  __device__ __forceinline__ void load(int step) {
+  u32x4 v[2][L];
+  template <int P> __device__ __forceinline__ void load(int step) {
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       const int c = threadIdx.x + 256 * i;
       const int kk = step * KE + c % KE, col = c / KE * V;
-      v[i] = u32x4{0u, 0u, 0u, 0u};
+      v[P][i] = u32x4{0u, 0u, 0u, 0u};
       if (kk < krows && col < cols) {
         const int src = index != nullptr ? min(max(index[kk], 0), index_rows - 1) : kk;
-        v[i] = *reinterpret_cast<const u32x4*>(base + static_cast<size_t>(src) * ld + col);
+        v[P][i] = *reinterpret_cast<const u32x4*>(base + static_cast<size_t>(src) * ld + col);
       }
     }
   }
-  __device__ __forceinline__ void store(char* lds) const {
+  template <int P> __device__ __forceinline__ void store(char* lds) const {
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       const int c = threadIdx.x + 256 * i;
       const int kb = c % KE * static_cast<int>(sizeof(T)), col = c / KE * V;
-      const T* e = reinterpret_cast<const T*>(&v[i]);
+      const T* e = reinterpret_cast<const T*>(&v[P][i]);
 #pragma unroll
       for (int q = 0; q < V; ++q)
         *reinterpret_cast<T*>(lds + lds_swz(col + q, kb >> 4) + (kb & 15)) = e[q];
@@ -95,7 +99,7 @@ struct Operand<T, T, true, L> {
 };
 
 template <typename T, typename TW, int MODE, bool GATED, int B>
-__global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs g, const T* __restrict__ dz,
+__global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs g, const T* __restrict__ dz,
                                                           T* __restrict__ out) {
   constexpr int TILE = B * 128;
   constexpr int NB = B / 32;           // 16-row and 16-column blocks of a wavefront
@@ -171,7 +175,9 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs g, const T*
       opa.p[i] = src + static_cast<size_t>(srow) * k_dim * sizeof(T) + (c & 7) * 16;
     }
     nsteps = static_cast<int>(static_cast<size_t>(k_dim) * sizeof(T) / 128);
+    opa.steps = nsteps;
     if constexpr (MODE == kFwd) {
+      opb.steps = nsteps;
       const char* w = static_cast<const char*>(g.w) + e * wmat * sizeof(TW);
 #pragma unroll
       for (int i = 0; i < L; ++i) {
@@ -217,29 +223,63 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs g, const T*
         }
     }
   };
-  if (nsteps > 0) {
-    opa.load(0);
-    opb.load(0);
-    opa.store(stage(0));
-    opb.store(stage(0) + TILE);
+  // (only the forward has tiles of few rows by rule: fp32 with up to 48 rows a
+  // group does not come here; dX and dW run faster without the branches)
+  auto multiply = [&](const char* st) {
+    if (MODE != kFwd || live == NB) compute(st, std::true_type{});
+    else if (live > 0) compute(st, std::false_type{});
+  };
+  // Two steps of loads in flight, but for the 128 x 128 tiles of dX and dW,
+  // whose turned operand takes the registers (fp32 backward of 2048 rows, 4096
+  // -> 2 x 2048: 1728 us with one step, 1807 with two; forward 950 / 896, 1000
+  // bf16 rows of 4096 -> 1024 on 64 x 64 tiles 41 / 26).
+  constexpr bool DEEP = MODE == kFwd || B == 64;
+  if (!DEEP && nsteps > 0) {
+    opa.template load<0>(0);
+    opb.template load<0>(0);
+    opa.template store<0>(stage(0));
+    opb.template store<0>(stage(0) + TILE);
     lds_barrier();
     for (int s = 0; s < nsteps; ++s) {
       const bool more = s + 1 < nsteps;
       if (more) {
-        opa.load(s + 1);
-        opb.load(s + 1);
+        opa.template load<0>(s + 1);
+        opb.template load<0>(s + 1);
       }
-      const char* st = stage(s & 1);
-      // (only the forward has tiles of few rows by rule: fp32 with up to 48 rows
-      // a group does not come here; dX and dW run faster without the branches)
-      if (MODE != kFwd || live == NB) compute(st, std::true_type{});
-      else if (live > 0) compute(st, std::false_type{});
+      multiply(stage(s & 1));
       if (more) {
-        opa.store(stage((s + 1) & 1));
-        opb.store(stage((s + 1) & 1) + TILE);
+        opa.template store<0>(stage((s + 1) & 1));
+        opb.template store<0>(stage((s + 1) & 1) + TILE);
       }
       lds_barrier();
     }
+  } else if (nsteps > 0) {
+    opa.template load<0>(0);
+    opb.template load<0>(0);
+    opa.template load<1>(1);
+    opb.template load<1>(1);
+    opa.template store<0>(stage(0));
+    opb.template store<0>(stage(0) + TILE);
+    lds_barrier();
+    // two steps of loads in flight: step s + 2 is asked for while step s is
+    // multiplied out of one buffer and step s + 1 waits to go into the other
+    for (int s = 0;; s += 2) {
+      opa.template load<0>(s + 2);
+      opb.template load<0>(s + 2);
+      multiply(stage(0));
+      if (s + 1 >= nsteps) break;
+      opa.template store<1>(stage(1));
+      opb.template store<1>(stage(1) + TILE);
+      lds_barrier();
+      opa.template load<1>(s + 3);
+      opb.template load<1>(s + 3);
+      multiply(stage(1));
+      if (s + 2 >= nsteps) break;
+      opa.template store<0>(stage(0));
+      opb.template store<0>(stage(0) + TILE);
+      lds_barrier();
+    }
+    lds_barrier();
   }
 
   // the tile as fp32 rows in LDS, then 8 columns of a row per lane
