@@ -98,13 +98,14 @@ int rows_parts(const moe_linear_config& c, const LinearArgs& g) {
 }
 
 // Whether a bf16 product has enough 256 x 256 tiles for the large-tile kernel
-// (linear_mfma.hip): with no more than an eighth of the compute units, the 64
-// x 64 tiles of linear_tile.hip spread it over more of them.  Backward, us with
-// large / with small tiles: 600 rows, 4 experts, 512 -> 1024: 47 / 35; 2000
-// rows, one expert, 1024 -> 2 x 4096: 200 / 223 (dX, 32 tiles, alone on the
-// small ones 169); 1600 rows, 64 experts, 512 -> 512: 48 / 64.
+// (linear_mfma.hip): with at most a quarter of the compute units, the tiles of
+// linear_tile.hip spread it over more of them.  us with large / with small
+// tiles: forward of 1000 rows 2048 -> 4096 (64 tiles) 41 / 33, 3000 rows 4096
+// -> 2048 (96) 70 / 76; backward of 600 rows of 4 experts 512 -> 1024 (12 and
+// 32) 45 / 30, of 2000 rows of one expert 1024 -> 2 x 4096 201 / 205, and 151
+// with dX (32) on small and dW (128) on large ones.
 bool large_tiles(long row_tiles, int cols) {
-  return row_tiles * ((cols + 255) / 256) > device_cus() / 8;
+  return row_tiles * ((cols + 255) / 256) > device_cus() / 4;
 }
 // Row tiles of 256 rows that the rows of all groups can need.
 long row_tiles(const moe_linear_config& c) { return c.rows / 256 + std::min(c.groups, c.rows); }
