@@ -439,9 +439,9 @@ typedef struct {
  * rows) or r.  Rows at or past offsets[groups] are left as they were.
  *
  * offsets is read on the device; values outside [0, rows], or decreasing,
- * are clamped.  y may be residual.  With z_codes and z_scale the call also
- * writes the 8-bit checkpoint of z (below), which the backward of an
- * activation reads.  z is held in fp32 until it is rounded to y or coded. */
+ * are clamped.  y may be residual; no output may overlap another input.  With
+ * z_codes and z_scale the call also writes the 8-bit checkpoint of z (below),
+ * which the backward of an activation reads.  z is held in fp32 until it is rounded to y or coded. */
 typedef struct {
   const void* x;            /* [x_rows or rows, in_dim]                               */
   const int32_t* row_index; /* [rows], or NULL when x_rows = 0                        */
@@ -467,8 +467,8 @@ moe_status moe_grouped_linear(const moe_linear_config* cfg, const moe_linear_arg
  *                                     through row_index are summed over a
  *                                     token's slots by moe_combine
  *   dw[e]    = sum_r dz[r]^T x[src(r)],  dbias[e] = sum_r dz[r]
- * (the residual's gradient is dy).  Each output is optional, one at least
- * is required; groups without rows get zeros; rows of dx at or past
+ * (the residual's gradient is dy).  No output may overlap an input.  Each is
+ * optional, one at least is required; groups without rows get zeros; rows of dx at or past
  * offsets[groups] are left as they were.  dz is held in dtype as operand of
  * both products, dbias sums it before that rounding.  Weights in dtype only
  * (MOE_WEIGHTS_DTYPE). */
@@ -514,7 +514,8 @@ moe_status moe_combine(int32_t T, int32_t k, int32_t n_rows, int32_t d, int32_t 
 /* drows[slot_row[t, s]] = gate[t, s] dy[t],  dgate[t, s] = <dy[t], rows[...]>
  * (0 for a slot without a row).  drows and dgate are optional, one at least
  * is required; rows may be NULL when dgate is.  Rows that no slot names are
- * left as they were; no row may be named twice. */
+ * left as they were; no row may be named twice, and drows must not overlap
+ * rows. */
 moe_status moe_combine_backward(int32_t T, int32_t k, int32_t n_rows, int32_t d, int32_t dtype,
                                 const void* rows, const int32_t* slot_row, const float* gate,
                                 const void* dy, void* drows, float* dgate, void* stream);

@@ -152,9 +152,10 @@ __global__ __launch_bounds__(256) void act_backward_kernel(LinearArgs g, const T
 }
 
 // dbias of one group and 256 columns: its tiles' partial sums, in tile order.
+// cap: rows of partial (offsets that overlap could name more tiles).
 __global__ __launch_bounds__(256) void bias_grad_kernel(LinearArgs g,
                                                         const float* __restrict__ partial,
-                                                        float* __restrict__ dbias) {
+                                                        int cap, float* __restrict__ dbias) {
   const int e = blockIdx.x, n = blockIdx.y * 256 + threadIdx.x;
   // tiles of the groups before e
   int before = 0;
@@ -166,7 +167,7 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(LinearArgs g,
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) before += __shfl_xor(before, off, 64);
   const int2 r = group_range(g.offsets, e, g.rows);
-  const int tiles = (r.y - r.x + kActRows - 1) / kActRows;
+  const int tiles = min((r.y - r.x + kActRows - 1) / kActRows, cap - before);
   if (n >= g.z_dim) return;
   const float* p = partial + static_cast<size_t>(before) * g.z_dim + n;
   float acc = 0.f;
@@ -241,7 +242,8 @@ hipError_t launch_act_backward(int dtype, const LinearArgs& g, const void* dy, v
 hipError_t launch_bias_grad(const LinearArgs& g, const float* partial, float* dbias,
                             hipStream_t s) {
   const dim3 grid(g.groups, (g.z_dim + 255) / 256);
-  hipLaunchKernelGGL(bias_grad_kernel, grid, dim3(256), 0, s, g, partial, dbias);
+  hipLaunchKernelGGL(bias_grad_kernel, grid, dim3(256), 0, s, g, partial,
+                     static_cast<int>(act_tiles(g.rows, g.groups)), dbias);
   return hipGetLastError();
 }
 

@@ -156,7 +156,8 @@ __global__ __launch_bounds__(kGThreads) void group_rows_kernel(
       if (e < N) {
         int rank = s_run[e] + in_wave;
         for (int w = 0; w < wave; ++w) rank += s_wave[w][e];
-        if (capacity <= 0 || rank < capacity) {
+        // (the second bound only matters if idx changed since it was counted)
+        if ((capacity <= 0 || rank < capacity) && s_off[e] + rank < n) {
           row = s_off[e] + rank;
           row_token[row] = static_cast<int>(i / k);
         }

@@ -326,6 +326,19 @@ def test_offsets_are_clamped(rows, groups):
     if groups == 4:
         assert torch.equal(y[n:2 * n], good[n:2 * n])
     assert bool(torch.isnan(guard[:32]).all()) and bool(torch.isnan(guard[32 + c.rows:]).all())
+    # the backward writes nothing outside either, and every group's dw and dbias
+    gx = poison((c.rows + 64, c.K), c.dt)
+    gw = poison((groups + 2, c.zd, c.K), c.dt)
+    gb = poison((groups + 2, c.zd), torch.float32)
+    moe.moe_grouped_linear_backward(
+        c.cfg, c.x, torch.tensor(off, dtype=torch.int32, device=DEV), c.w, c.dy,
+        dx=gx[32:32 + c.rows], dw=gw[1:1 + groups], dbias=gb[1:1 + groups],
+        workspace=workspace(moe.alloc_linear_backward_workspace(c.cfg, DEV)))
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(gx[:32]).all()) and bool(torch.isnan(gx[32 + c.rows:]).all())
+    for t in (gw, gb):
+        assert bool(torch.isnan(t[0]).all()) and bool(torch.isnan(t[-1]).all())
+        assert not bool(torch.isnan(t[1]).any())
 
 
 def test_results_repeat_and_streams_do_not_matter():
@@ -467,6 +480,62 @@ def test_small_and_large_values():
             c.bias = vals.repeat(c.zd // 64).expand(1, c.zd).contiguous().to(DEV)
             c.hx[:], c.hw[:] = 0, 0
             c.check_forward(f"extremes {act} {dtype}")
+
+
+def test_two_streams_at_once():
+    """Two calls in flight together, each with a workspace of its own."""
+    say("[linear] two streams")
+    for sizes, K, F in (([1, 2], 4096, 128), (RAGGED, 1024, 576)):
+        cases = [Case(sizes, K, F, "swiglu", gather=True, bias=True, seed=s) for s in (1, 2)]
+        want = [c.forward(True) for c in cases]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in cases]
+        args = []
+        for c in cases:
+            args.append((poison((c.rows, F), c.dt), poison((c.rows, c.zd), torch.uint8),
+                         poison((c.rows, c.zd // 64), torch.float32),
+                         workspace(moe.alloc_linear_workspace(c.cfg, DEV))))
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for c, s, (y, codes, scale, ws) in zip(cases, streams, args):
+                moe.moe_grouped_linear(c.cfg, c.x, c.offsets, c.w, y, row_index=c.index,
+                                       bias=c.bias, z_codes=codes, z_scale=scale, workspace=ws,
+                                       stream=s)
+        torch.cuda.synchronize()
+        for w, a in zip(want, args):
+            for p, q in zip(w, a):
+                assert torch.equal(p.view(torch.uint8), q.view(torch.uint8))
+
+
+def test_binding_refuses_what_the_c_side_cannot_see():
+    say("[linear] refusals")
+    c = Case([3, 2], 64, 64, "gelu")
+    ws = moe.alloc_linear_workspace(c.cfg, DEV)
+    y = poison((5, 64), c.dt)
+    good = dict(x=c.x, offsets=c.offsets, w=c.w, y=y, workspace=ws)
+    bad = [dict(x=c.x.float()), dict(x=c.x[:4]), dict(offsets=c.offsets.long()),
+           dict(offsets=c.offsets[:2]), dict(w=c.w[:1]), dict(w=c.w.transpose(1, 2)),
+           dict(y=poison((5, 128), c.dt)[:, :64]), dict(y=y.cpu()), dict(workspace=ws.cpu()),
+           dict(bias=poison((2, 64), c.dt)), dict(residual=poison((4, 64), c.dt)),
+           dict(z_codes=poison((5, 64), torch.uint8), z_scale=poison((5, 2), torch.float32)),
+           dict(row_index=torch.zeros(4, dtype=torch.int32, device=DEV))]
+    for over in bad:
+        a = {**good, **over}
+        with pytest.raises(ValueError):
+            moe.moe_grouped_linear(c.cfg, a.pop("x"), a.pop("offsets"), a.pop("w"), a.pop("y"), **a)
+    with pytest.raises(moe.MoEError):  # a checkpoint is needed to differentiate GELU
+        moe.moe_grouped_linear_backward(c.cfg, c.x, c.offsets, c.w, c.dy, dx=poison((5, 64), c.dt),
+                                        workspace=moe.alloc_linear_backward_workspace(c.cfg, DEV))
+    with pytest.raises(moe.MoEError):  # 8 of 16-byte aligned
+        flat = torch.zeros(5 * 64 + 4, dtype=c.dt, device=DEV)
+        moe.moe_grouped_linear(c.cfg, c.x, c.offsets, c.w, flat[4:].view(5, 64), workspace=ws)
+    with pytest.raises(ValueError):
+        moe.moe_checkpoint_pack(c.x.half(), poison((5, 64), torch.uint8),
+                                poison((5, 1), torch.float32))
+    with pytest.raises(ValueError):
+        moe.moe_combine(c.x, torch.zeros((2, 2), dtype=torch.int64, device=DEV),
+                        poison((2, 64), c.dt))
+    assert bool(torch.isnan(y).all())
 
 
 # ---------------------------------------------------------------- checkpoints
