@@ -436,12 +436,14 @@ typedef struct {
 
 /* z[r] = x[src(r)] W_e^T + bias[e],  y[r] = act(z[r]) + residual[r]
  * for the rows r of every group e, src(r) = row_index[r] (clamped to x's
- * rows) or r.  Rows at or past offsets[groups] are left as they were.
+ * rows) or r.  Rows of no group (before offsets[0], at or past offsets[groups])
+ * are left as they were.
  *
  * offsets is read on the device; values outside [0, rows], or decreasing,
  * are clamped.  y may be residual; no output may overlap another input.  With
  * z_codes and z_scale the call also writes the 8-bit checkpoint of z (below),
- * which the backward of an activation reads.  z is held in fp32 until it is rounded to y or coded. */
+ * which the backward of an activation reads.  z is held in fp32 until it is
+ * rounded to y or coded. */
 typedef struct {
   const void* x;            /* [x_rows or rows, in_dim]                               */
   const int32_t* row_index; /* [rows], or NULL when x_rows = 0                        */
