@@ -439,11 +439,12 @@ typedef struct {
  * rows) or r.  Rows of no group (before offsets[0], at or past offsets[groups])
  * are left as they were.
  *
- * offsets is read on the device; values outside [0, rows], or decreasing,
- * are clamped.  y may be residual; no output may overlap another input.  With
- * z_codes and z_scale the call also writes the 8-bit checkpoint of z (below),
- * which the backward of an activation reads.  z is held in fp32 until it is
- * rounded to y or coded. */
+ * offsets is read on the device and has to rise (or stay) from 0 or more to
+ * rows or less.  Other values are clamped where they are used: no access goes
+ * out of bounds, but the results may be anything.  y may be residual; no output
+ * may overlap another input.  With z_codes and z_scale the call also writes the
+ * 8-bit checkpoint of z (below), which the backward of an activation reads.  z
+ * is held in fp32 until it is rounded to y or coded. */
 typedef struct {
   const void* x;            /* [x_rows or rows, in_dim]                               */
   const int32_t* row_index; /* [rows], or NULL when x_rows = 0                        */
@@ -470,8 +471,8 @@ moe_status moe_grouped_linear(const moe_linear_config* cfg, const moe_linear_arg
  *                                     token's slots by moe_combine
  *   dw[e]    = sum_r dz[r]^T x[src(r)],  dbias[e] = sum_r dz[r]
  * (the residual's gradient is dy).  No output may overlap an input.  Each is
- * optional, one at least is required; groups without rows get zeros; rows of dx at or past
- * offsets[groups] are left as they were.  dz is held in dtype as operand of
+ * optional, one at least is required; groups without rows get zeros; rows of
+ * dx of no group are left as they were.  dz is held in dtype as operand of
  * both products, dbias sums it before that rounding.  Weights in dtype only
  * (MOE_WEIGHTS_DTYPE). */
 typedef struct {

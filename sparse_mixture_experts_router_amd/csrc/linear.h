@@ -348,8 +348,8 @@ __device__ __forceinline__ void load_cols8(const float* p, size_t at, bool ok, f
     for (int i = 0; i < 8; ++i) v[i] = fill;
   }
 }
-// 8 values of the residual (0 where there is none), widened by unpack8 when
-// they are used, so that a caller can have many in flight.
+// 8 values as they lie in memory, widened when they are used, so that a caller
+// can have many in flight.
 template <typename T> struct Raw8;
 template <> struct Raw8<bf16_t> {
   u32x4 r;

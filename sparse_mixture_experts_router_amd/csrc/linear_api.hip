@@ -123,7 +123,8 @@ BackSpace back_space(const moe_linear_config& c) {
   b.partial = o;
   o += align_up(static_cast<size_t>(act_tiles(c.rows, c.groups)) * z * 4);
   b.xg = o;
-  if (c.dtype == MOE_BF16 && c.x_rows > 0) o += align_up(static_cast<size_t>(c.rows) * c.in_dim * eb);
+  if (c.dtype == MOE_BF16 && c.x_rows > 0)
+    o += align_up(static_cast<size_t>(c.rows) * c.in_dim * eb);
   b.total = o > 0 ? o : kAlign;
   return b;
 }
@@ -134,12 +135,14 @@ moe_status check_group(int32_t T, int32_t N, int32_t k) {
   if (T < 0 || N <= 0 || k <= 0) return fail(MOE_ERR_INVALID_ARG, "bad T, N or k");
   if (N > kMaxExperts) return fail(MOE_ERR_UNSUPPORTED, "n_experts > 512");
   if (k > kMaxTopK) return fail(MOE_ERR_UNSUPPORTED, "top_k > 16");
-  if (static_cast<long>(T) * k >= kMaxGroupPairs) return fail(MOE_ERR_UNSUPPORTED, "T * k too large");
+  if (static_cast<long>(T) * k >= kMaxGroupPairs)
+    return fail(MOE_ERR_UNSUPPORTED, "T * k too large");
   return MOE_OK;
 }
 
 moe_status check_combine(int32_t T, int32_t k, int32_t n_rows, int32_t d, int32_t dtype) {
-  if (T < 0 || k <= 0 || n_rows < 0 || d <= 0) return fail(MOE_ERR_INVALID_ARG, "bad T, k, n_rows or d");
+  if (T < 0 || k <= 0 || n_rows < 0 || d <= 0)
+    return fail(MOE_ERR_INVALID_ARG, "bad T, k, n_rows or d");
   if (check_dtype(dtype) != MOE_OK) return MOE_ERR_INVALID_ARG;
   if (k > kMaxTopK) return fail(MOE_ERR_UNSUPPORTED, "top_k > 16");
   if (d % 64 != 0) return fail(MOE_ERR_UNSUPPORTED, "d must be a multiple of 64");
@@ -298,7 +301,7 @@ moe_status moe_grouped_linear_backward(const moe_linear_config* cfg,
   if (c.rows > 0 && a->dx != nullptr) {
     const bool large = bf16 && large_tiles(row_tiles(c), c.in_dim);
     err = large ? launch_linear_mfma_dx(g, dz, a->dx, s)
-               : launch_linear_dx_tile(c.dtype, g, dz, a->dx, device_cus(), s);
+                : launch_linear_dx_tile(c.dtype, g, dz, a->dx, device_cus(), s);
     if (err != hipSuccess) return hip_fail(err, "dx");
   }
   if (a->dw != nullptr) {
@@ -311,7 +314,7 @@ moe_status moe_grouped_linear_backward(const moe_linear_config* cfg,
     }
     if (large) g.row_index = nullptr;
     err = large ? launch_linear_mfma_dw(g, dz, a->dw, s)
-               : launch_linear_dw_tile(c.dtype, g, dz, a->dw, device_cus(), s);
+                : launch_linear_dw_tile(c.dtype, g, dz, a->dw, device_cus(), s);
     if (err != hipSuccess) return hip_fail(err, "dw");
   }
   return MOE_OK;

@@ -8,11 +8,10 @@
 // bound by the matrix cores: a tile does 512 operations for each byte that it
 // stages.  One workgroup of 8 wavefronts, two on each SIMD, owns a tile and
 // the whole LDS; a wavefront accumulates a quarter of the rows and half of the
-// columns in AGPRs.  A stage is
-// 64 elements of K.  The wavefronts of a SIMD take turns: while one runs its
-// 64 MFMAs of a stage from registers, the other issues its loads (global ->
-// LDS, no registers) and reads its 24 fragments of the next stage; a barrier
-// ends every phase.  Wavefronts 0-3 load the A operand one stage ahead (2
+// columns in AGPRs.  A stage is 64 elements of K.  The wavefronts of a SIMD
+// take turns: while one runs its 64 MFMAs of a stage from registers, the other
+// issues its loads (global -> LDS, no registers) and reads its 24 fragments of
+// the next stage; a barrier ends every phase.  Wavefronts 0-3 load the A operand one stage ahead (2
 // buffers), wavefronts 4-7 the B operand two stages ahead (3 buffers, for W
 // comes from HBM while the rows of x are mostly in L2).
 //

@@ -138,8 +138,9 @@ __global__ __launch_bounds__(256 * KS) void linear_rows_kernel(LinearArgs g,
     for (; s + N <= s1; s += N) run(n_, rb_);
     for (; s < s1; ++s) run(std::integral_constant<int, 1>{}, rb_);
   };
-  if (valid > 16) loop(std::integral_constant<int, FP8W ? 4 : 2>{}, std::integral_constant<int, 2>{});
-  else loop(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+  using std::integral_constant;
+  if (valid > 16) loop(integral_constant<int, FP8W ? 4 : 2>{}, integral_constant<int, 2>{});
+  else loop(integral_constant<int, 4>{}, integral_constant<int, 1>{});
 
   // partial products [kw][row][W row of the workgroup]; SwiGLU: gate columns
   // 0 .. 63, up columns 64 .. 127
@@ -215,7 +216,8 @@ __global__ __launch_bounds__(256) void join_rows_kernel(LinearArgs g,
   int e = 0;
   for (int i0 = 0; i0 < g.groups; i0 += 64) {
     const int i = i0 + lane;
-    e += __popcll(__ballot(i < g.groups && group_range(g.offsets, min(i, g.groups - 1), g.rows).y <= row));
+    const int2 r = group_range(g.offsets, min(i, g.groups - 1), g.rows);
+    e += __popcll(__ballot(i < g.groups && r.y <= row));
   }
   if (e >= g.groups || group_range(g.offsets, e, g.rows).x > row) return;
   const int n = (blockIdx.y * 256 + threadIdx.x) * 8;
