@@ -336,29 +336,42 @@ hipError_t launch_b(const LinearArgs& g, const void* dz, void* out, hipStream_t 
                                   : item_grid(g.rows, g.groups, B, nt);
   if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks));
-  if constexpr (MODE == kFwd && B == 128) {
+  if constexpr (MODE == kFwd) {
     if (gated) {
       hipLaunchKernelGGL((linear_tile_kernel<T, TW, MODE, true, B>), grid, dim3(256), 0, s, g,
                          static_cast<const T*>(dz), static_cast<T*>(out));
       return hipGetLastError();
     }
   }
-  if (gated) return hipErrorInvalidValue;  // half a 64-column tile is no checkpoint block
   hipLaunchKernelGGL((linear_tile_kernel<T, TW, MODE, false, B>), grid, dim3(256), 0, s, g,
                      static_cast<const T*>(dz), static_cast<T*>(out));
   return hipGetLastError();
 }
 
-// 64 x 64 tiles where the 128 x 128 ones are fewer than the compute units: a
-// small product is bound by one tile's chain of steps, and theirs is a
-// quarter as long.
+// 64 x 64 tiles where the 128 x 128 ones are fewer than the compute units (a
+// small product is bound by one tile's chain of steps, and theirs is a quarter
+// as long), and for fp32, which is bound by its MFMAs with either, where the
+// larger tiles would not fill their rounds of two on each compute unit: tile
+// for tile they are 12 % faster.  fp32 us on large / small tiles:
+//   8 groups of 256 rows, 4096 -> 2 x 2048: forward 897 / 657, dX 887 / 775, dW
+//   (8192 tiles) 884 / 934; 2048 -> 2048 of 3000 rows (384) 275 / 249, of 4096
+//   (512) 268 / 295, of 5000 (640) 525 / 402, of 12000 (1504) 807 / 877
+// A group's last row tile counts half, for its rows are not known here.
 template <typename T, typename TW, int MODE>
 hipError_t launch_t(const LinearArgs& g, const void* dz, void* out, int cus, hipStream_t s) {
-  const long nt = ((MODE == kFwd ? g.out_dim : g.in_dim) + 127) / 128;
-  const long mt = MODE == kDw ? static_cast<long>(g.groups) * ((g.z_dim + 127) / 128)
-                              : g.rows / 128 + std::min(g.groups, g.rows);
-  if (mt * nt < cus && !(MODE == kFwd && g.act == kActSwiglu))
-    return launch_b<T, TW, MODE, 64>(g, dz, out, s);
+  const bool gated = MODE == kFwd && g.act == kActSwiglu;
+  auto tiles = [&](long b) {
+    const long cols = gated ? b / 2 : b;
+    const long nt = ((MODE == kFwd ? g.out_dim : g.in_dim) + cols - 1) / cols;
+    if (MODE == kDw) return g.groups * ((g.z_dim + b - 1) / b) * nt;
+    if (g.groups == 1) return (g.rows + b - 1) / b * nt;
+    return (2 * g.rows / b + std::min(g.groups, g.rows)) * nt / 2;
+  };
+  const long large = tiles(128), round = 2L * cus;
+  const bool small = large < cus || (std::is_same_v<T, float> &&
+                                     tiles(64) * 28 < (large + round - 1) / round * round * 100);
+  // (half of 64 columns is no checkpoint block)
+  if (small && !(gated && g.z_codes != nullptr)) return launch_b<T, TW, MODE, 64>(g, dz, out, s);
   return launch_b<T, TW, MODE, 128>(g, dz, out, s);
 }
 
