@@ -109,6 +109,20 @@ bool large_tiles(long row_tiles, int cols) {
 }
 // Row tiles of 256 rows that the rows of all groups can need.
 long row_tiles(const moe_linear_config& c) { return c.rows / 256 + std::min(c.groups, c.rows); }
+// The same for the forward.  Small tiles also where few rows a group leave the
+// large ones mostly empty and too few for the compute units: the forward with
+// large / with small tiles of 500 rows of 16 groups 2048 -> 2048 (at most 136
+// tiles, 16 by its rows) 41.8 / 34.5, of 200 rows of 4 groups 1024 -> 2 x 4096
+// (128, 25) 24.2 / 13.8, of 512 rows of 8 groups 4096 -> 4096 (160, 32) 76.7 /
+// 66.7; but 1000 rows of 16 groups 2048 -> 4096 in FP8 (304, 63) 39.5 / 46.0,
+// 4000 rows of 8 groups 1024 -> 2048 (184, 125) 27.1 / 39.5.  (dX: 500 rows of
+// 16 groups 2048 -> 2048, backward in all, 86.6 / 92.7.)
+bool forward_large(const moe_linear_config& c, const LinearArgs& g) {
+  const long nt = (g.z_dim + 255) / 256, cus = device_cus();
+  return c.dtype == MOE_BF16 && large_tiles(row_tiles(c), g.z_dim) &&
+         (c.rows * nt / 256 > cus / 4 || row_tiles(c) * nt > cus) &&
+         linear_mfma_fits(c.weight_format == MOE_WEIGHTS_FP8_E4M3, g);
+}
 
 // Workspace of the backward.
 struct BackSpace {
@@ -236,7 +250,7 @@ moe_status moe_grouped_linear(const moe_linear_config* cfg, const moe_linear_arg
   hipError_t err;
   if (streams_rows(c, g))
     err = launch_linear_rows(c.dtype, fp8, g, device_cus(), static_cast<float*>(workspace), s);
-  else if (c.dtype == MOE_BF16 && large_tiles(row_tiles(c), g.z_dim) && linear_mfma_fits(fp8, g))
+  else if (forward_large(c, g))
     err = launch_linear_mfma(fp8, g, s);
   else
     err = launch_linear_tile(c.dtype, fp8, g, device_cus(), s);

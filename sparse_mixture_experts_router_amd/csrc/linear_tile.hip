@@ -12,12 +12,13 @@
 // same 16-byte MFMA fragments.
 //
 // One workgroup owns a B x B tile of one group (B = 128, or 64 where the
-// larger tiles would leave compute units without work), its 4 wavefronts a
+// larger tiles would leave compute units without work: launch_t), its 4 wavefronts a
 // quarter each; a K step is 128 bytes of every row, fetched into registers one
 // or two steps before it is multiplied out of one of two LDS buffers.  Rows
 // past a group's end repeat its last row (results not written); K-rows past it
 // are zeros in both operands, so that no NaN of a neighbouring group enters.
-// fp32 reaches 75-82 of the 153 TFLOP/s of a large library product.
+// fp32 reaches 130 of the 153 TFLOP/s of a large library product (8192 rows,
+// 4096 -> 4096), 105 with 8 groups of 256 rows.
 #include <algorithm>
 #include <type_traits>
 

@@ -241,12 +241,20 @@ FORWARD = [
     ([0, 30, 17], 2112, 64, "none", dict(spare=70)),
     ([1], 4096, 64, "silu", dict(bias=True)),
     # enough 256 x 256 tiles (more than a quarter of the compute units) for the
-    # large-tile kernel in every product, groups of all fillings
+    # large-tile kernel in dX and dW, groups of all fillings
     (RAGGED, 1088, 1088, "silu", dict(gather=True, bias=True)),
     (RAGGED, 1024, 576, "swiglu", dict(gather=True, bias=True, spare=9)),
     (RAGGED, 640, 832, "none", dict(bias=True, residual=True, spare=1)),
     (RAGGED, 1152, 1088, "gelu", dict(residual=True)),
     ([0] * 20 + [160] + [0] * 9 + [96] * 2, 512, 320, "relu", dict()),
+    # and in the forward (by the rows, or with few rows a group by the groups)
+    (RAGGED, 320, 3264, "silu", dict(gather=True, bias=True)),
+    (RAGGED, 384, 1664, "swiglu", dict(gather=True, bias=True, spare=9)),
+    (RAGGED, 256, 3264, "none", dict(bias=True, residual=True, spare=1)),
+    (RAGGED[:6] + [20] * 34, 384, 1664, "gelu", dict(residual=True)),
+    # full rounds of 128 x 128 tiles in fp32: forward and dW, dX
+    ([1000], 1024, 8192, "relu", dict(bias=True)),
+    ([1010], 8192, 64, "silu", dict(spare=5)),
 ]
 IDS = [f"{len(s)}g{sum(s)}r_{K}x{F}_{a}" for s, K, F, a, _ in FORWARD]
 
@@ -277,17 +285,19 @@ def test_backward_of_some(act, want):
 
 def test_residual_in_place():
     say("[linear] y is the residual")
-    for sizes, F in (([9, 4], 192), ([300, 270], 192), (RAGGED, 1088)):
+    for sizes, F in (([9, 4], 192), ([300, 270], 192), (RAGGED, 1088),
+                     (RAGGED, 3264)):
         Case(sizes, 128, F, "gelu", residual=True, spare=3).check_forward("in place", inplace=True)
 
 
-@pytest.mark.parametrize("groups", [3, 40], ids=["small", "large"])
+@pytest.mark.parametrize("groups,K,F", [(3, 128, 192), (40, 512, 448), (40, 448, 1664)],
+                         ids=["small", "large", "wide"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_neighbours_stay_apart(dtype, groups):
+def test_neighbours_stay_apart(dtype, groups, K, F):
     """One group's NaN and infinities reach none of the others' outputs,
     whatever tiles they share."""
     say(f"[linear] neighbours {dtype}")
-    c = Case([37, 70, 5] + [9] * (groups - 3), *((128, 192) if groups == 3 else (512, 448)), "silu", dtype)
+    c = Case([37, 70, 5] + [9] * (groups - 3), K, F, "silu", dtype)
     a, b = int(c.off[1]), int(c.off[2])
     ref = c.check_backward("before")
     y0, codes, scale = c.forward(True)
