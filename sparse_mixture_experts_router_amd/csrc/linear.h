@@ -43,13 +43,21 @@ struct LinearArgs {
 // ---------------------------------------------------------------- launchers
 // Forward: y = act(x W^T + b) + residual; wfp8: E4M3 weights; cus: compute
 // units of the device.
-hipError_t launch_linear_tile(int dtype, bool wfp8, const LinearArgs& g, int cus, hipStream_t s);
+// linear_tile_parts: shares of K that the launch is split into; more than one
+// takes partial [parts, rows, z_dim].
+int linear_tile_parts(int elem_bytes, const LinearArgs& g, int cus);
+hipError_t launch_linear_tile(int dtype, bool wfp8, const LinearArgs& g, int cus, float* partial,
+                              hipStream_t s);
 // dX[r] = dz[r] W_e.  dz [rows, z_dim], dx [rows, in].
 hipError_t launch_linear_dx_tile(int dtype, const LinearArgs& g, const void* dz, void* dx, int cus,
                                  hipStream_t s);
 // dW_e = sum_r dz[r]^T x[src(r)]; groups without rows get zeros.
 hipError_t launch_linear_dw_tile(int dtype, const LinearArgs& g, const void* dz, void* dw, int cus,
                                  hipStream_t s);
+
+// The epilogue of a forward split over K: y from partial [parts, rows, z_dim].
+hipError_t launch_join_rows(int dtype, const LinearArgs& g, const float* partial, int parts,
+                            hipStream_t s);
 
 // Forward for few rows a group: 32-row tiles, W streamed through registers.
 // linear_rows_parts: shares of K that the launch is split into; more than one
@@ -60,7 +68,8 @@ hipError_t launch_linear_rows(int dtype, bool wfp8, const LinearArgs& g, int cus
                               hipStream_t s);
 // The same three on 256 x 256 tiles (bf16; forward: weights in bf16 or FP8):
 // dW takes x's rows in order, without row_index.
-bool linear_mfma_fits(bool wfp8, const LinearArgs& g);
+// (gather: x is read through row_index.)
+bool linear_mfma_fits(bool wfp8, bool gather, const LinearArgs& g);
 hipError_t launch_linear_mfma(bool wfp8, const LinearArgs& g, hipStream_t s);
 hipError_t launch_linear_mfma_dx(const LinearArgs& g, const void* dz, void* dx, hipStream_t s);
 hipError_t launch_linear_mfma_dw(const LinearArgs& g, const void* dz, void* dw, hipStream_t s);

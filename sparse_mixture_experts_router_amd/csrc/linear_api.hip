@@ -93,9 +93,6 @@ bool streams_rows(const moe_linear_config& c, const LinearArgs& g) {
                                                               : std::min(8 * G, 256L);
   return c.rows <= most && linear_rows_fits(g);
 }
-int rows_parts(const moe_linear_config& c, const LinearArgs& g) {
-  return linear_rows_parts(c.dtype == MOE_BF16 ? 2 : 4, g, device_cus());
-}
 
 // Whether a bf16 product has enough 256 x 256 tiles for the large-tile kernel
 // (linear_mfma.hip): with at most a quarter of the compute units, the tiles of
@@ -121,7 +118,13 @@ bool forward_large(const moe_linear_config& c, const LinearArgs& g) {
   const long nt = (g.z_dim + 255) / 256, cus = device_cus();
   return c.dtype == MOE_BF16 && large_tiles(row_tiles(c), g.z_dim) &&
          (c.rows * nt / 256 > cus / 4 || row_tiles(c) * nt > cus) &&
-         linear_mfma_fits(c.weight_format == MOE_WEIGHTS_FP8_E4M3, g);
+         linear_mfma_fits(c.weight_format == MOE_WEIGHTS_FP8_E4M3, c.x_rows > 0, g);
+}
+// Shares of K that the forward is split into.
+int forward_parts(const moe_linear_config& c, const LinearArgs& g) {
+  const int eb = c.dtype == MOE_BF16 ? 2 : 4;
+  if (streams_rows(c, g)) return linear_rows_parts(eb, g, device_cus());
+  return forward_large(c, g) ? 1 : linear_tile_parts(eb, g, device_cus());
 }
 
 // Workspace of the backward.
@@ -211,7 +214,7 @@ moe_status moe_group_rows(int32_t T, int32_t N, int32_t k, int32_t capacity,
 size_t moe_linear_workspace_size(const moe_linear_config* cfg) {
   if (check_linear(cfg) != MOE_OK) return 0;
   const LinearArgs g = linear_args(*cfg);
-  const int parts = streams_rows(*cfg, g) ? rows_parts(*cfg, g) : 1;
+  const int parts = forward_parts(*cfg, g);
   return parts > 1 ? align_up(static_cast<size_t>(parts) * g.rows * g.z_dim * 4) : kAlign;
 }
 
@@ -253,7 +256,7 @@ moe_status moe_grouped_linear(const moe_linear_config* cfg, const moe_linear_arg
   else if (forward_large(c, g))
     err = launch_linear_mfma(fp8, g, s);
   else
-    err = launch_linear_tile(c.dtype, fp8, g, device_cus(), s);
+    err = launch_linear_tile(c.dtype, fp8, g, device_cus(), static_cast<float*>(workspace), s);
   return err == hipSuccess ? MOE_OK : hip_fail(err, "grouped linear kernel");
 }
 

@@ -514,15 +514,14 @@ hipError_t launch_t(const LinearArgs& g, const void* dz, void* out, hipStream_t 
 
 }  // namespace
 
-bool linear_mfma_fits(bool wfp8, const LinearArgs& g) {
+bool linear_mfma_fits(bool wfp8, bool gather, const LinearArgs& g) {
   // 32-bit offsets into x when its rows are gathered; whole buffers of codes
-  return (g.row_index == nullptr ||
-          static_cast<size_t>(g.x_rows) * g.in_dim * 2 < (size_t{1} << 32)) &&
+  return (!gather || static_cast<size_t>(g.x_rows) * g.in_dim * 2 < (size_t{1} << 32)) &&
          (!wfp8 || g.in_dim % 128 == 0);
 }
 
 hipError_t launch_linear_mfma(bool wfp8, const LinearArgs& g, hipStream_t s) {
-  if (!linear_mfma_fits(wfp8, g)) return hipErrorInvalidValue;
+  if (!linear_mfma_fits(wfp8, g.row_index != nullptr, g)) return hipErrorInvalidValue;
   if (wfp8)
     return g.act == kActSwiglu ? launch_t<kFwd, true, true>(g, nullptr, nullptr, s)
                                : launch_t<kFwd, false, true>(g, nullptr, nullptr, s);

@@ -276,9 +276,7 @@ hipError_t launch_t(const LinearArgs& g, int cus, float* partial, hipStream_t s)
   if (parts > 1) {
     const hipError_t err = launch_ks<T, TW, GATED, 1>(g, parts, partial, s);
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL((join_rows_kernel<T, GATED>), dim3(g.rows, (g.out_dim + 2047) / 2048),
-                       dim3(256), 0, s, g, partial, parts);
-    return hipGetLastError();
+    return launch_join_rows(sizeof(T) == 2 ? 1 : 0, g, partial, parts, s);
   }
   // Two slices of K in a workgroup where one would give a compute unit fewer
   // than 6 wavefronts.  One / two slices: 448 workgroups (one FP8 token's gate
@@ -288,7 +286,23 @@ hipError_t launch_t(const LinearArgs& g, int cus, float* partial, hipStream_t s)
   return launch_ks<T, TW, GATED, 2>(g, 1, nullptr, s);
 }
 
+template <typename T>
+hipError_t launch_join_t(const LinearArgs& g, const float* partial, int parts, hipStream_t s) {
+  const dim3 grid(g.rows, (g.out_dim + 2047) / 2048);
+  if (g.act == kActSwiglu)
+    hipLaunchKernelGGL((join_rows_kernel<T, true>), grid, dim3(256), 0, s, g, partial, parts);
+  else
+    hipLaunchKernelGGL((join_rows_kernel<T, false>), grid, dim3(256), 0, s, g, partial, parts);
+  return hipGetLastError();
+}
+
 }  // namespace
+
+hipError_t launch_join_rows(int dtype, const LinearArgs& g, const float* partial, int parts,
+                            hipStream_t s) {
+  return dtype == 1 ? launch_join_t<bf16_t>(g, partial, parts, s)
+                    : launch_join_t<float>(g, partial, parts, s);
+}
 
 bool linear_rows_fits(const LinearArgs& g) {
   return rows_blocks(g) < (1L << 23);  // 2^32 threads, the XCDs' shares rounded up

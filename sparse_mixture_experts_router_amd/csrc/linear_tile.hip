@@ -12,11 +12,14 @@
 // same 16-byte MFMA fragments.
 //
 // One workgroup owns a B x B tile of one group (B = 128, or 64 where the
-// larger tiles would leave compute units without work: launch_t), its 4 wavefronts a
-// quarter each; a K step is 128 bytes of every row, fetched into registers one
-// or two steps before it is multiplied out of one of two LDS buffers.  Rows
-// past a group's end repeat its last row (results not written); K-rows past it
-// are zeros in both operands, so that no NaN of a neighbouring group enters.
+// larger tiles would leave compute units without work: launch_t), its 4
+// wavefronts a quarter each; a K step is 128 bytes of every row, fetched into
+// registers one or two steps before it is multiplied out of one of two LDS
+// buffers.  Rows past a group's end repeat its last row (results not written);
+// K-rows past it are zeros in both operands, so that no NaN of a neighbouring
+// group enters.  A forward of few tiles is split over K: the layers of the grid
+// write fp32 partial tiles, and a second launch adds them in order and runs the
+// epilogue (linear_tile_parts).
 // fp32 reaches 130 of the 153 TFLOP/s of a large library product (8192 rows,
 // 4096 -> 4096), 105 with 8 groups of 256 rows.
 #include <algorithm>
@@ -101,7 +104,8 @@ struct Operand<T, T, true, L> {
 
 template <typename T, typename TW, int MODE, bool GATED, int B>
 __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs g, const T* __restrict__ dz,
-                                                             T* __restrict__ out) {
+                                                             T* __restrict__ out,
+                                                             float* __restrict__ partial) {
   constexpr int TILE = B * 128;
   constexpr int NB = B / 32;           // 16-row and 16-column blocks of a wavefront
   constexpr int L = B / 32;            // 16-byte chunks of an operand tile a thread
@@ -176,6 +180,14 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs g, const
       opa.p[i] = src + static_cast<size_t>(srow) * k_dim * sizeof(T) + (c & 7) * 16;
     }
     nsteps = static_cast<int>(static_cast<size_t>(k_dim) * sizeof(T) / 128);
+    int s0 = 0;  // first step of this layer's share
+    if (MODE == kFwd && B == 64 && partial != nullptr) {
+      const int per = (nsteps + gridDim.y - 1) / gridDim.y;
+      s0 = min(static_cast<int>(blockIdx.y) * per, nsteps);
+      nsteps = min(per, nsteps - s0);
+#pragma unroll
+      for (int i = 0; i < L; ++i) opa.p[i] += static_cast<size_t>(s0) * 128;
+    }
     opa.steps = nsteps;
     if constexpr (MODE == kFwd) {
       opb.steps = nsteps;
@@ -186,7 +198,8 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs g, const
         // SwiGLU: the tile's gate rows, then the up rows of the same columns
         const bool up = GATED && r >= COLS;
         const int n = min(n0 + (up ? r - COLS : r), g.out_dim - 1) + (up ? g.out_dim : 0);
-        opb.p[i] = w + (static_cast<size_t>(n) * g.in_dim) * sizeof(TW) + (c & 7) * opb.CB;
+        opb.p[i] = w + (static_cast<size_t>(n) * g.in_dim) * sizeof(TW) + (c & 7) * opb.CB +
+                   static_cast<size_t>(s0) * 8 * opb.CB;
       }
     } else {
       opb.base = static_cast<const T*>(g.w) + e * wmat + n0;
@@ -310,7 +323,17 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs g, const
     const bool ok = row < valid && n < n_dim;
     float v[8], u[8];
     load8<float>(stg + row * PITCH + c, v);
-    if constexpr (MODE == kFwd) {
+    if (MODE == kFwd && B == 64 && partial != nullptr) {
+      if (ok) {
+        float* const p = partial +
+                         (static_cast<size_t>(blockIdx.y) * g.rows + seg + m0 + row) * g.z_dim + n;
+        store8<float>(p, v);
+        if (GATED) {
+          load8<float>(stg + row * PITCH + COLS + c, u);
+          store8<float>(p + g.out_dim, u);
+        }
+      }
+    } else if constexpr (MODE == kFwd) {
       Raw8<T> res;
       load_residual<T>(g, seg + m0 + row, n, ok, res);
       if (GATED) load8<float>(stg + row * PITCH + COLS + c, u);
@@ -329,24 +352,35 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs g, const
 }
 
 template <typename T, typename TW, int MODE, int B>
-hipError_t launch_b(const LinearArgs& g, const void* dz, void* out, hipStream_t s) {
+hipError_t launch_b(const LinearArgs& g, const void* dz, void* out, hipStream_t s, int parts = 1,
+                    float* partial = nullptr) {
   const bool gated = MODE == kFwd && g.act == kActSwiglu;
   const int cols = gated ? B / 2 : B;
   const long nt = ((MODE == kFwd ? g.out_dim : g.in_dim) + cols - 1) / cols;
   const long blocks = MODE == kDw ? static_cast<long>(g.groups) * ((g.z_dim + B - 1) / B) * nt
                                   : item_grid(g.rows, g.groups, B, nt);
   if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks));
+  const dim3 grid(static_cast<unsigned>(blocks), parts);
   if constexpr (MODE == kFwd) {
     if (gated) {
       hipLaunchKernelGGL((linear_tile_kernel<T, TW, MODE, true, B>), grid, dim3(256), 0, s, g,
-                         static_cast<const T*>(dz), static_cast<T*>(out));
+                         static_cast<const T*>(dz), static_cast<T*>(out), partial);
       return hipGetLastError();
     }
   }
   hipLaunchKernelGGL((linear_tile_kernel<T, TW, MODE, false, B>), grid, dim3(256), 0, s, g,
-                     static_cast<const T*>(dz), static_cast<T*>(out));
+                     static_cast<const T*>(dz), static_cast<T*>(out), partial);
   return hipGetLastError();
+}
+
+// Tiles of b rows that a product of the mode has; a group's last row tile
+// counts half, for its rows are not known here.
+template <int MODE> long tiles_of(const LinearArgs& g, long b) {
+  const long cols = MODE == kFwd && g.act == kActSwiglu ? b / 2 : b;
+  const long nt = ((MODE == kFwd ? g.out_dim : g.in_dim) + cols - 1) / cols;
+  if (MODE == kDw) return g.groups * ((g.z_dim + b - 1) / b) * nt;
+  if (g.groups == 1) return (g.rows + b - 1) / b * nt;
+  return (2 * g.rows / b + std::min(g.groups, g.rows)) * nt / 2;
 }
 
 // 64 x 64 tiles where the 128 x 128 ones are fewer than the compute units (a
@@ -357,20 +391,22 @@ hipError_t launch_b(const LinearArgs& g, const void* dz, void* out, hipStream_t 
 //   8 groups of 256 rows, 4096 -> 2 x 2048: forward 897 / 657, dX 887 / 775, dW
 //   (8192 tiles) 884 / 934; 2048 -> 2048 of 3000 rows (384) 275 / 249, of 4096
 //   (512) 268 / 295, of 5000 (640) 525 / 402, of 12000 (1504) 807 / 877
-// A group's last row tile counts half, for its rows are not known here.
 template <typename T, typename TW, int MODE>
-hipError_t launch_t(const LinearArgs& g, const void* dz, void* out, int cus, hipStream_t s) {
+hipError_t launch_t(const LinearArgs& g, const void* dz, void* out, int cus, hipStream_t s,
+                    float* partial = nullptr) {
+  if constexpr (MODE == kFwd) {
+    const int parts = linear_tile_parts(static_cast<int>(sizeof(T)), g, cus);
+    if (parts > 1) {
+      const hipError_t err = launch_b<T, TW, MODE, 64>(g, dz, out, s, parts, partial);
+      return err != hipSuccess ? err
+                               : launch_join_rows(sizeof(T) == 2 ? 1 : 0, g, partial, parts, s);
+    }
+  }
   const bool gated = MODE == kFwd && g.act == kActSwiglu;
-  auto tiles = [&](long b) {
-    const long cols = gated ? b / 2 : b;
-    const long nt = ((MODE == kFwd ? g.out_dim : g.in_dim) + cols - 1) / cols;
-    if (MODE == kDw) return g.groups * ((g.z_dim + b - 1) / b) * nt;
-    if (g.groups == 1) return (g.rows + b - 1) / b * nt;
-    return (2 * g.rows / b + std::min(g.groups, g.rows)) * nt / 2;
-  };
-  const long large = tiles(128), round = 2L * cus;
-  const bool small = large < cus || (std::is_same_v<T, float> &&
-                                     tiles(64) * 28 < (large + round - 1) / round * round * 100);
+  const long large = tiles_of<MODE>(g, 128), round = 2L * cus;
+  const bool small =
+      large < cus || (std::is_same_v<T, float> &&
+                      tiles_of<MODE>(g, 64) * 28 < (large + round - 1) / round * round * 100);
   // (half of 64 columns is no checkpoint block)
   if (small && !(gated && g.z_codes != nullptr)) return launch_b<T, TW, MODE, 64>(g, dz, out, s);
   return launch_b<T, TW, MODE, 128>(g, dz, out, s);
@@ -378,10 +414,23 @@ hipError_t launch_t(const LinearArgs& g, const void* dz, void* out, int cus, hip
 
 }  // namespace
 
-hipError_t launch_linear_tile(int dtype, bool wfp8, const LinearArgs& g, int cus, hipStream_t s) {
-  if (wfp8) return launch_t<bf16_t, uint8_t, kFwd>(g, nullptr, nullptr, cus, s);
-  if (dtype == 1) return launch_t<bf16_t, bf16_t, kFwd>(g, nullptr, nullptr, cus, s);
-  return launch_t<float, float, kFwd>(g, nullptr, nullptr, cus, s);
+// Fewer 64 x 64 tiles than compute units: as many parts as leave two workgroups
+// or less for each, none shorter than 16 steps.  bf16 us whole / split: 64 rows
+// of 14336 -> 4096 108 / 50, of 4096 -> 4096 25 / 15 (19 with 8 parts of 8
+// steps), of 4096 -> 14336 (224 tiles) 37.4 / 34.5; with more tiles than units
+// (1200 rows of 4 groups 4096 -> 2 x 704, 456) 32 / 34.
+int linear_tile_parts(int elem_bytes, const LinearArgs& g, int cus) {
+  const long tiles = tiles_of<kFwd>(g, 64), steps = static_cast<long>(g.in_dim) * elem_bytes / 128;
+  if (tiles <= 0 || tiles > cus) return 1;
+  const long parts = std::min(2L * cus / tiles, steps / 16);
+  return parts < 2 ? 1 : static_cast<int>(std::min(parts, 16L));
+}
+
+hipError_t launch_linear_tile(int dtype, bool wfp8, const LinearArgs& g, int cus, float* partial,
+                              hipStream_t s) {
+  if (wfp8) return launch_t<bf16_t, uint8_t, kFwd>(g, nullptr, nullptr, cus, s, partial);
+  if (dtype == 1) return launch_t<bf16_t, bf16_t, kFwd>(g, nullptr, nullptr, cus, s, partial);
+  return launch_t<float, float, kFwd>(g, nullptr, nullptr, cus, s, partial);
 }
 
 hipError_t launch_linear_dx_tile(int dtype, const LinearArgs& g, const void* dz, void* dx, int cus,

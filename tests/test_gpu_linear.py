@@ -240,6 +240,10 @@ FORWARD = [
     ([2, 5, 0, 1], 1152, 128, "swiglu", dict(gather=True, bias=True, spare=3)),
     ([0, 30, 17], 2112, 64, "none", dict(spare=70)),
     ([1], 4096, 64, "silu", dict(bias=True)),
+    # the same with more rows, on 64 x 64 tiles
+    ([200, 0, 77], 4160, 192, "swiglu", dict(gather=True, bias=True, spare=5)),
+    ([90], 2112, 320, "silu", dict(bias=True, residual=True)),
+    ([60, 0, 0, 61, 0, 200], 2304, 64, "none", dict(residual=True, spare=70)),
     # enough 256 x 256 tiles (more than a quarter of the compute units) for the
     # large-tile kernel in dX and dW, groups of all fillings
     (RAGGED, 1088, 1088, "silu", dict(gather=True, bias=True)),
