@@ -11,7 +11,7 @@ operation by operation, as the definition says.
 from __future__ import annotations
 
 import numpy as np
-from scipy.special import erf
+from scipy.special import erfc
 
 from .moe_oracle import e4m3_decode
 
@@ -58,7 +58,7 @@ def activation(act: str, z):
     if act == "relu":
         return np.where(z > 0, z, 0.0)
     if act == "gelu":
-        return z * 0.5 * (1 + erf(z / np.sqrt(2)))
+        return z * 0.5 * erfc(-z / np.sqrt(2))
     if act == "silu":
         return z * _sigmoid(z)
     assert act == "swiglu"
@@ -73,7 +73,7 @@ def activation_backward(act: str, z, dy):
     if act == "relu":
         return np.where(z > 0, dy, 0.0)
     if act == "gelu":
-        return dy * (0.5 * (1 + erf(z / np.sqrt(2))) + z * np.exp(-z * z / 2) / np.sqrt(2 * np.pi))
+        return dy * (0.5 * erfc(-z / np.sqrt(2)) + z * np.exp(-z * z / 2) / np.sqrt(2 * np.pi))
     if act == "silu":
         p = _sigmoid(z)
         return dy * (p + z * p * (1 - p))

@@ -225,16 +225,21 @@ template <> __device__ __forceinline__ float sigmoid<bf16_t>(float z) {
 }
 // The normal distribution's CDF at z, and e = exp(-z^2 / 2).
 //
+// fp32 layers: erfc(-z / sqrt 2) / 2, which keeps its relative accuracy in the
+// lower tail, where (1 + erf(z / sqrt 2)) / 2 cancels (4 % off at z = -5, 0
+// below -5.6).  2000 rows of 256 -> 8192 98.6 us, 94.0 with erff.
+//
 // bf16 layers: Abramowitz and Stegun's 7.1.26,
 //   erfc(x) = (a1 t + ... + a5 t^5) e^-x^2,  t = 1 / (1 + p x),  x >= 0,
-// which shares its exponential with the density.  Taken for the tail it is
-// within 7e-8 of the CDF, and z times it within 2^-9 of GELU for z > -5 (half
-// a bf16 step is 2^-8), where GELU is 1e-6.  4096 tokens' gate and up rows
+// which shares its exponential with the density.  Evaluated in fp32 for the
+// tail it is within 3e-7 of the CDF, and z times it within 2^-9 of GELU for
+// z > -5, where GELU is -1.4e-6, and 2^-8 (half a bf16 step) for z > -6; below
+// it is off by 1 % at -8, 2 % at -10, of values under 6e-9.  4096 tokens' gate and up rows
 // (8192 x 28672 values) cost a forward 210 us with erff, 105 this way.
 template <typename T> __device__ __forceinline__ float normal_cdf(float z, float& e);
 template <> __device__ __forceinline__ float normal_cdf<float>(float z, float& e) {
   e = expf(-0.5f * z * z);
-  return 0.5f * (1.0f + erff(z * 0.70710678118654752f));
+  return 0.5f * erfcf(z * -0.70710678118654752f);
 }
 template <> __device__ __forceinline__ float normal_cdf<bf16_t>(float z, float& e) {
   e = __expf(-0.5f * z * z);

@@ -1,0 +1,46 @@
+"""GPU tests of the calls for experts of one's own where values or sizes are
+extreme: against float64, with bounds that count roundings (u = 2^-24)."""
+import numpy as np
+import pytest
+import torch
+
+import sparse_mixture_experts_router_amd as moe
+from gpu_harness import say, to_np
+from oracle import linear_oracle as lo
+from oracle.moe_oracle import e4m3_decode
+from test_gpu_linear import DEV, U, Case, check, poison, workspace
+
+pytestmark = pytest.mark.gpu
+
+
+def test_fp32_gelu_keeps_its_lower_tail():
+    """z in [-10, -4] by the bias alone, so exact.  Forward, relative: the
+    argument z / sqrt 2 is off by 2 u, which moves erfc by 2 (z^2 + 1) u; erfcf
+    is within 16 ulp (32 u); two products.  Slope Phi + z phi: the exponential's
+    argument is rounded once, z^2 / 2 u, expf and products 10 u."""
+    say("[linear] fp32 GELU tail")
+    z = np.linspace(-10, -4, 64).astype(np.float32)
+    c = Case([1], 64, 64, "gelu", "f32")
+    c.x.zero_()
+    c.w.zero_()
+    c.bias = torch.tensor(z[None], device=DEV)
+    y, _, _ = c.forward()
+    torch.cuda.synchronize()
+    zd = z.astype(np.float64)
+    ref = lo.activation("gelu", zd)
+    check("gelu", y[0], ref, np.abs(ref) * (2 * zd * zd + 64) * U)
+    codes, scale = lo.checkpoint_pack(z[None])
+    z = (e4m3_decode(codes).astype(np.float32) * scale)[0]
+    zd = z.astype(np.float64)
+    c.dy.fill_(1.0)
+    db = poison((1, 64), torch.float32)
+    moe.moe_grouped_linear_backward(
+        c.cfg, None, c.offsets, None, c.dy, z_codes=torch.tensor(codes, device=DEV),
+        z_scale=torch.tensor(scale, device=DEV), dbias=db,
+        workspace=workspace(moe.alloc_linear_backward_workspace(c.cfg, DEV)))
+    torch.cuda.synchronize()
+    cdf = lo.activation("gelu", zd) / zd
+    pdf = np.exp(-zd * zd / 2) / np.sqrt(2 * np.pi)
+    ref = lo.activation_backward("gelu", zd, np.ones_like(zd))
+    check("gelu slope", db[0], ref,
+          (cdf * (2 * zd * zd + 64) + np.abs(zd) * pdf * (zd * zd + 64)) * U)

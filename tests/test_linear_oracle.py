@@ -47,6 +47,21 @@ def test_gradients_are_differences(act):
         assert abs((up - dn) / (2 * h) - float(np.sum(grad * v[pick]))) < 1e-6
 
 
+def test_gelu_keeps_its_lower_tail():
+    """For z < 0 the normal CDF lies between its asymptotic series' partial
+    sums phi/|z| (1 - 1/z^2) and phi/|z| (1 - 1/z^2 + 3/z^4)."""
+    z = np.linspace(-30, -4, 105)[:, None]
+    y = lo.activation("gelu", z)
+    slope = lo.activation_backward("gelu", z, np.ones_like(z))
+    phi = np.exp(-z * z / 2) / np.sqrt(2 * np.pi)
+    low = phi / -z * (1 - z ** -2)
+    high = low + phi / -z * 3 * z ** -4
+    for cdf in (y / z, slope - z * phi):
+        # the slope's difference cancels z^2 of its terms, each 2^-52 (z^2 / 2 + 4)
+        assert np.all(cdf >= low - 2.0 ** -52 * (z * z + 8) * np.abs(z) * phi)
+        assert np.all(cdf <= high + 2.0 ** -52 * (z * z + 8) * np.abs(z) * phi)
+
+
 def test_checkpoint_codes_are_the_nearest():
     """Every code against all 127 magnitudes by brute force."""
     rng = np.random.default_rng(5)
