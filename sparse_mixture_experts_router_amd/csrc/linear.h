@@ -87,7 +87,7 @@ inline long act_tiles(long rows, long groups) {
 // partial [act_tiles, z_dim].
 hipError_t launch_act_backward(int dtype, const LinearArgs& g, const void* dy, void* dz,
                                float* partial, hipStream_t s);
-// dbias[e] = the sum of group e's tiles of partial, in tile order.
+// dbias[e] = the sum of group e's tiles of partial, in a fixed order.
 hipError_t launch_bias_grad(const LinearArgs& g, const float* partial, float* dbias,
                             hipStream_t s);
 

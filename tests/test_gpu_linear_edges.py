@@ -8,7 +8,7 @@ import sparse_mixture_experts_router_amd as moe
 from gpu_harness import say, to_np
 from oracle import linear_oracle as lo
 from oracle.moe_oracle import e4m3_decode
-from test_gpu_linear import DEV, U, Case, check, poison, workspace
+from test_gpu_linear import DEV, DT, U, Case, check, poison, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +44,35 @@ def test_fp32_gelu_keeps_its_lower_tail():
     ref = lo.activation_backward("gelu", zd, np.ones_like(zd))
     check("gelu slope", db[0], ref,
           (cdf * (2 * zd * zd + 64) + np.abs(zd) * pdf * (zd * zd + 64)) * U)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bias_gradient_of_many_rows(dtype):
+    """A million equal values: every addition of a running fp32 sum would round
+    the same way.  16 rows of a tile one after another (16 u), 8 tiles at a
+    time (8 u), those in sums that keep what each addition rounds off (8 u)."""
+    say(f"[linear] bias gradient of many rows {dtype}")
+    sizes = [3, (1 << 20) + 5, 0, 40000]
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    cfg = moe.make_linear_config(int(off[-1]), 4, 64, 64, dtype=DT[dtype])
+    dy = torch.full((int(off[-1]), 64), 0.1, dtype=DT[dtype], device=DEV)
+    dy[:, 1] = -0.7
+    db = poison((4, 64), torch.float32)
+
+    def run():
+        moe.moe_grouped_linear_backward(
+            cfg, None, torch.tensor(off, dtype=torch.int32, device=DEV), None, dy, dbias=db,
+            workspace=workspace(moe.alloc_linear_backward_workspace(cfg, DEV)))
+        torch.cuda.synchronize()
+
+    run()
+    ref = np.array(sizes)[:, None] * to_np(dy[0]).astype(np.float64)
+    check("dbias", db, ref, 32 * U * np.abs(ref))
+    # what is not finite stays what it is
+    dy[5, 2], dy[6, 3], dy[6, 4], dy[70000, 4] = (float(v) for v in ("inf", "nan", "inf", "-inf"))
+    before = db.clone()
+    run()
+    assert bool(torch.isposinf(db[1, 2])) and bool(torch.isnan(db[1, 3:5]).all())
+    keep = torch.ones_like(db, dtype=torch.bool)
+    keep[1, 2:5] = False
+    assert torch.equal(db[keep], before[keep])
