@@ -421,8 +421,10 @@ typedef enum {
 /* A linear map for each of `groups` groups of rows.  z_dim = out_dim, or
  * 2 out_dim with MOE_ACT_SWIGLU, is the number of rows of a group's weights.
  * One group is an ordinary dense product.  groups <= 512, in_dim and out_dim
- * multiples of 64 up to 2^20, rows < 2^27; MOE_WEIGHTS_FP8_E4M3 needs
- * MOE_BF16. */
+ * multiples of 64 up to 2^20, rows < 2^27, x_rows < 2^30, and
+ *   (rows / 128 + groups) max(in_dim, z_dim) / 64 <= 2^23   (rows / 128 rounded down)
+ *   groups z_dim in_dim <= 2^39, in a backward that writes dw < 2^36;
+ * MOE_WEIGHTS_FP8_E4M3 needs MOE_BF16.  Other sizes are MOE_ERR_UNSUPPORTED. */
 typedef struct {
   int32_t rows;          /* rows of y (and of residual, dy, dx, the checkpoint)       */
   int32_t x_rows;        /* rows of x when row_index is given; 0: x has `rows` rows   */

@@ -18,6 +18,10 @@ int z_dim(const moe_linear_config& c) {
   return c.activation == MOE_ACT_SWIGLU ? 2 * c.out_dim : c.out_dim;
 }
 
+long weights(const moe_linear_config& c) {
+  return static_cast<long>(c.groups) * z_dim(c) * c.in_dim;
+}
+
 moe_status check_dtype(int dtype) {
   return dtype == MOE_F32 || dtype == MOE_BF16 ? MOE_OK : fail(MOE_ERR_INVALID_ARG, "bad dtype");
 }
@@ -40,12 +44,14 @@ moe_status check_linear(const moe_linear_config* c) {
     return fail(MOE_ERR_UNSUPPORTED, "in_dim or out_dim > 2^20");
   if (c->rows >= (1 << 27) || c->x_rows >= (1 << 30))
     return fail(MOE_ERR_UNSUPPORTED, "too many rows");
-  // grids: at most 2^23 tiles of 128 rows by 64 columns (forward and dX), or
-  // of 128 by 128 (dW)
+  // Grids stay below 2^32 threads: at most 2^23 tiles of 128 rows by 64 columns,
+  // forward and dX.  There are twice as many tiles of 64 x 64, but launch_t
+  // takes them only for few tiles, or where fewer than 3.6 of them make one of
+  // 128 x 128: for 7 columns of them at most, times 2^21 rows of tiles.
   const long wide = std::max(c->in_dim, z_dim(*c));
-  if ((c->rows / 128 + c->groups) * (wide / 64) > (1L << 23) ||
-      static_cast<long>(c->groups) * (z_dim(*c) / 64) * (c->in_dim / 64) > (1L << 24))
+  if ((c->rows / 128 + c->groups) * (wide / 64) > (1L << 23))
     return fail(MOE_ERR_UNSUPPORTED, "too many tiles");
+  if (weights(*c) > (1L << 39)) return fail(MOE_ERR_UNSUPPORTED, "more than 2^39 weights");
   return MOE_OK;
 }
 
@@ -279,6 +285,9 @@ moe_status moe_grouped_linear_backward(const moe_linear_config* cfg,
   if (a->dw == nullptr && a->dbias == nullptr && c.rows == 0) return MOE_OK;
   if (a->dx == nullptr && a->dw == nullptr && a->dbias == nullptr)
     return fail(MOE_ERR_INVALID_ARG, "no gradient asked for");
+  // dW's grid: below 2^24 tiles of 64 x 64
+  if (a->dw != nullptr && weights(c) >= (1L << 36))
+    return fail(MOE_ERR_UNSUPPORTED, "dw of 2^36 weights or more");
   if (a->offsets == nullptr) return fail(MOE_ERR_INVALID_ARG, "offsets is NULL");
   const bool act = c.activation != MOE_ACT_NONE;
   if (c.rows > 0) {

@@ -8,7 +8,7 @@ import sparse_mixture_experts_router_amd as moe
 from gpu_harness import say, to_np
 from oracle import linear_oracle as lo
 from oracle.moe_oracle import e4m3_decode
-from test_gpu_linear import DEV, DT, U, Case, check, poison, workspace
+from test_gpu_linear import DEV, DT, U, V, Case, check, poison, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +76,37 @@ def test_bias_gradient_of_many_rows(dtype):
     keep = torch.ones_like(db, dtype=torch.bool)
     keep[1, 2:5] = False
     assert torch.equal(db[keep], before[keep])
+
+
+def test_fp8_weights_past_the_limit_of_a_gradient():
+    """512 experts of 4096 -> 2 x 16448, 69 GB of codes, of which the first and
+    the last have rows; their weights begin past 2^35 and end past 2^36."""
+    say("[linear] 2^36 FP8 weights")
+    G, K, F = 512, 4096, 16448
+    cfg = moe.make_linear_config(3, G, K, F, activation="swiglu",
+                                 weight_format=moe.MOE_WEIGHTS_FP8_E4M3)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    w = torch.empty((G, 2 * F, K), dtype=torch.uint8, device=DEV)
+    scale = torch.full((G, 2 * F), float("nan"), device=DEV)
+    x = torch.randn((3, K), generator=g, device=DEV).bfloat16()
+    offsets = torch.full((G + 1,), 1, dtype=torch.int32, device=DEV)
+    offsets[0], offsets[G] = 0, 3
+    y = poison((3, F), torch.bfloat16)
+    for e in (0, G - 1):
+        codes = torch.randint(0, 120, (2 * F, K), generator=g, device=DEV, dtype=torch.uint8)
+        w[e] = codes ^ (torch.randint(0, 2, (2 * F, K), generator=g, device=DEV,
+                                      dtype=torch.uint8) << 7)
+        scale[e] = 1e-4 * (1 + torch.rand(2 * F, generator=g, device=DEV))
+    moe.moe_grouped_linear(cfg, x, offsets, w, y, w_scale=scale,
+                           workspace=workspace(moe.alloc_linear_workspace(cfg, DEV)))
+    torch.cuda.synchronize()
+    for e, r in ((0, slice(0, 1)), (G - 1, slice(1, 3))):
+        we = w[e].view(torch.float8_e4m3fn).float().double() * scale[e].double()[:, None]
+        z = (x[r].double() @ we.t()).cpu().numpy()
+        dz = (K + 8) * U * (x[r].double().abs() @ we.abs().t()).cpu().numpy()
+        a, b = np.split(z, 2, axis=1)
+        da, db = np.split(dz, 2, axis=1)
+        ref = lo.activation("swiglu", z)
+        err = 1.1 * da * np.abs(b) + np.abs(lo.activation("silu", a)) * db + da * db
+        err = err + 2.0 ** -17 * np.abs(a) * np.abs(b)
+        check(f"expert {e}", y[r], ref, (1 + V) * err + V * np.abs(ref))

@@ -152,6 +152,44 @@ def test_backward_refusals_by_configuration():
     assert backward(cfg(rows=0), grads(dw=None, dbias=None, dx=None)) == moe.MOE_OK
 
 
+# the last configuration inside each limit of the header, and the first outside it
+LIMITS = [
+    (dict(groups=512), dict(groups=513)),
+    (dict(in_dim=1 << 20, groups=1), dict(in_dim=(1 << 20) + 64, groups=1)),
+    (dict(out_dim=1 << 20, groups=1), dict(out_dim=(1 << 20) + 64, groups=1)),
+    (dict(rows=(1 << 27) - 1), dict(rows=1 << 27)),
+    (dict(x_rows=(1 << 30) - 1), dict(x_rows=1 << 30)),
+    (dict(rows=128 * 508 + 127, in_dim=1 << 20), dict(rows=128 * 509, in_dim=1 << 20)),
+    (dict(groups=512, in_dim=1 << 15, out_dim=1 << 15), dict(groups=512, in_dim=1 << 15, out_dim=(1 << 15) + 64)),
+    # FP8 experts of 8192 -> 2 x 14336, 120 GB of codes
+    (dict(groups=512, in_dim=8192, out_dim=14336, activation=4, weight_format=1),
+     dict(groups=512, in_dim=1 << 17, out_dim=14336, activation=4, weight_format=1)),
+]
+
+
+@pytest.mark.parametrize("inside,outside", LIMITS, ids=[str(o) for _, o in LIMITS])
+def test_limits_are_the_headers(inside, outside):
+    """Inside a limit only the missing x is refused, outside it the size."""
+    assert moe.moe_linear_workspace_size(cfg(**inside)) > 0
+    assert moe.moe_linear_backward_workspace_size(cfg(**inside)) > 0
+    a = args(x=None, w_scale=FAKE if inside.get("weight_format") else None)
+    assert forward(cfg(**inside), a) == INVALID
+    assert forward(cfg(**outside), a) == UNSUPPORTED
+    assert moe.moe_linear_workspace_size(cfg(**outside)) == 0
+    if not inside.get("weight_format"):
+        assert backward(cfg(**inside), grads(dw=None, dy=None)) == INVALID
+        assert backward(cfg(**outside), grads(dw=None, dy=None)) == UNSUPPORTED
+
+
+def test_limit_of_dw():
+    """2^36 weights have a forward and a dx, but no dw."""
+    c = cfg(groups=512, in_dim=1 << 14, out_dim=1 << 13)
+    assert backward(c, grads(dw=None, dy=None)) == INVALID
+    assert backward(c, grads(dy=None)) == UNSUPPORTED
+    c.out_dim -= 64
+    assert backward(c, grads(dy=None)) == INVALID
+
+
 def test_group_refusals():
     lib = moe.lib()
 
