@@ -110,3 +110,75 @@ def test_fp8_weights_past_the_limit_of_a_gradient():
         err = 1.1 * da * np.abs(b) + np.abs(lo.activation("silu", a)) * db + da * db
         err = err + 2.0 ** -17 * np.abs(a) * np.abs(b)
         check(f"expert {e}", y[r], ref, (1 + V) * err + V * np.abs(ref))
+
+
+@pytest.mark.parametrize("sizes,K,F,act", [
+    ([3, 2], 64, 64, "none"), ([1, 3], 1024, 192, "swiglu"), ([90, 40], 2112, 320, "silu"),
+    ([200, 130], 192, 192, "swiglu"), ([300, 270, 513], 256, 8192, "none"),
+    ([300, 270, 513], 128, 4160, "swiglu")])
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+def test_checkpoint_of_a_forward_that_is_not_finite(sizes, K, F, act, dtype):
+    """Infinities and NaN in z, by its bias: the NaN code, and no part in the
+    scale of their blocks, whose other values keep their bounds."""
+    say(f"[linear] not finite {sizes} {K}x{F} {act} {dtype}")
+    c = Case(sizes, K, F, act, "f32" if dtype == "f32" else "bf16", fp8=dtype == "fp8", bias=True)
+    _, good_codes, good_scale = c.forward(True)
+    for e in range(len(sizes)):
+        for i, v in enumerate(("inf", "nan", "-inf")):
+            c.bias[e, (17 * e + 21 * i) % c.zd] = float(v)
+    c.bias[0, c.zd - 64:] = float("-inf")  # a block without a finite value
+    y, codes, scale = c.forward(True)
+    torch.cuda.synchronize()
+    ref, z = lo.grouped_linear(c.hx, c.off, c.hw, act, None, to_np(c.bias))
+    n = c.rows
+    ok = np.isfinite(z)
+    assert np.array_equal(np.isfinite(to_np(y)), np.isfinite(ref))
+    hc = to_np(codes)
+    assert np.array_equal((hc & 0x7F) == 0x7F, ~ok)
+    dz = np.where(ok, (K + 8) * U * c.z_bound(), 0.0)
+    zf = np.where(ok, z, 0.0)
+    m = np.maximum(np.abs(zf).reshape(n, -1, 64).max(2), 1e-30)
+    dm = dz.reshape(n, -1, 64).max(2)
+    check("scale", scale, m / 448, (dm + 4 * U * m) / 448)
+    back = np.where(ok, lo.checkpoint_unpack(hc, to_np(scale)), 0.0)
+    step = np.repeat((m + dm) / 448 * 2.0 ** -10, 64, axis=1)
+    check("checkpoint", torch.tensor(back), zf,
+          dz + np.maximum((np.abs(zf) + dz) / 16, step) * (1 + 8 * U))
+    whole = ok.reshape(n, -1, 64).all(2)
+    assert np.array_equal(to_np(scale)[whole], to_np(good_scale)[whole])
+    assert np.array_equal(hc.reshape(n, -1, 64)[whole],
+                          to_np(good_codes).reshape(n, -1, 64)[whole])
+
+
+def test_rows_gathered_from_four_gigabytes():
+    """x of more than 2^32 bytes read through row_index, its last rows among
+    those read; the rows that are not read hold NaN."""
+    say("[linear] gather from 4 GiB")
+    sizes, K, F, n_x = [600, 0, 300], 1024, 8192, (1 << 21) + 5
+    rows = sum(sizes)
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    g = torch.Generator(device=DEV).manual_seed(6)
+    index = torch.randint(0, n_x, (rows,), generator=g, device=DEV, dtype=torch.int32)
+    index[::7] = n_x - 1
+    index[1::7] = torch.arange(n_x - 130, n_x - 1, device=DEV, dtype=torch.int32)[:len(index[1::7])]
+    x = poison((n_x, K), torch.bfloat16)
+    x[index.long()] = torch.randn((rows, K), generator=g, device=DEV).bfloat16()
+    w = (torch.randn((3, F, K), generator=g, device=DEV) / 32).bfloat16()
+    dy = torch.randn((rows, F), generator=g, device=DEV).bfloat16()
+    offsets = torch.tensor(off, dtype=torch.int32, device=DEV)
+    cfg = moe.make_linear_config(rows, 3, K, F, x_rows=n_x)
+    y, dw = poison((rows, F), torch.bfloat16), poison((3, F, K), torch.bfloat16)
+    moe.moe_grouped_linear(cfg, x, offsets, w, y, row_index=index,
+                           workspace=workspace(moe.alloc_linear_workspace(cfg, DEV)))
+    moe.moe_grouped_linear_backward(
+        cfg, x, offsets, None, dy, row_index=index, dw=dw,
+        workspace=workspace(moe.alloc_linear_backward_workspace(cfg, DEV)))
+    torch.cuda.synchronize()
+    for e, n in enumerate(sizes):
+        r = slice(int(off[e]), int(off[e + 1]))
+        xe, we, de = x[index[r].long()].double(), w[e].double(), dy[r].double()
+        for name, got, ref, terms, k in (
+                ("y", y[r], xe @ we.t(), xe.abs() @ we.abs().t(), K),
+                ("dw", dw[e], de.t() @ xe, de.abs().t() @ xe.abs(), n)):
+            tol = (1 + V) * (k + 8) * U * terms + V * ref.abs()
+            check(f"{name}[{e}]", got, ref.cpu().numpy(), tol.cpu().numpy())
