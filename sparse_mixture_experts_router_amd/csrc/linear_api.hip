@@ -82,21 +82,23 @@ LinearArgs linear_args(const moe_linear_config& c) {
 }
 
 // Whether the forward streams W through registers (linear_rows.hip) instead of
-// taking large tiles: few rows a group on average.  Mixtral-shaped gate and up
-// projection (8 experts, 4096 -> 14336, SwiGLU), us with few-row / with large
-// tiles:
+// taking tiles: few rows a group on average.  Mixtral-shaped gate and up
+// projection (8 experts, 4096 -> 14336, SwiGLU), us with few-row / with the
+// other kernels:
 //   bf16  8 rows a group 327 / 339, 12: 341 / 334, 16: 376 / 346, 32: 620 / 330
 //   FP8   8 rows 193 / 244, 12: 227 / 239, 16: 255 / 239, 32: 448 / 239
-//   fp32  8 rows 636 / 2069, 16: 957 / 2069, 32: 1558 / 2072, 48: 2060 / 2078
+//   fp32  1 row 656 / 649, 8: 649 / 624, 16: 695 / 634, 32: 1032 / 810; one
+//         expert 1 row 100 / 109, 8: 103 / 109, 24: 144 / 114; 1024 -> 2048 of
+//         one expert 1 row 12.3 / 15.7, 8: 13.5 / 16.3, 32: 16.6 / 16.7
 // Only the average is known here, so few rows in all as well: 256 experts of
 // 2048 -> 2 x 2048 with 2048 rows, spread evenly / all in one of them,
 //   bf16  693 / 237 against 703 / 45 (256 rows: 683 / 41 against 694 / 44)
 //   FP8   411 / 183 against 530 / 51
+//   fp32  1513 / 532 against 1546 / 314 (256 rows: 1409 / 77 against 1534 / 57)
 bool streams_rows(const moe_linear_config& c, const LinearArgs& g) {
   const long G = c.groups;
-  const long most = c.dtype == MOE_F32 ? 48 * G
-                    : c.weight_format == MOE_WEIGHTS_FP8_E4M3 ? std::min(12 * G, 2048L)
-                                                              : std::min(8 * G, 256L);
+  const long most = c.weight_format == MOE_WEIGHTS_FP8_E4M3 ? std::min(12 * G, 2048L)
+                                                            : std::min(8 * G, 256L);
   return c.rows <= most && linear_rows_fits(g);
 }
 
