@@ -399,7 +399,7 @@ moe_status moe_update_select_bias(int32_t N, const int32_t* counts, float rate,
  * The rows of an expert are in the flat order of their (token, slot) pairs.
  * capacity: 0, or the most pairs an expert keeps, its first ones (as in
  * moe_config).  A pair whose index lies outside [0, N) gets no row: -1 marks
- * the slots of padding.  1 <= N <= 512, k <= 16, T k < 2^30; T = 0 writes
+ * the slots of padding.  No output may overlap topk_idx.  1 <= N <= 512, k <= 16, T k < 2^30; T = 0 writes
  * offsets only.  workspace: moe_group_workspace_size(T, N, k) bytes, 256-byte
  * aligned (the size is 0 for sizes outside these). */
 size_t moe_group_workspace_size(int32_t T, int32_t N, int32_t k);
@@ -501,8 +501,10 @@ moe_status moe_grouped_linear_backward(const moe_linear_config* cfg,
  *   m = max(max |x| over the block, 1e-30),  scale = m / 448,
  *   code = E4M3(x * (448 / m)), to nearest even;  unpack: code * scale,
  * so an element is off by at most 2^-4 of itself, or scale 2^-10 where that
- * is more.  NaN and infinities become the NaN code and do not enter m.
- * codes [rows, cols], scale [rows, cols / 64].  rows = 0 launches nothing. */
+ * is more: one of at most scale 2^-10 becomes 0, where ReLU's slope is 0.  NaN
+ * and infinities become the NaN code and do not enter m.  codes [rows, cols],
+ * scale [rows, cols / 64].  rows = 0 launches nothing.  No output may overlap
+ * an input. */
 moe_status moe_checkpoint_pack(int64_t rows, int32_t cols, int32_t dtype, const void* x,
                                uint8_t* codes, float* scale, void* stream);
 moe_status moe_checkpoint_unpack(int64_t rows, int32_t cols, int32_t dtype,
@@ -519,8 +521,8 @@ moe_status moe_combine(int32_t T, int32_t k, int32_t n_rows, int32_t d, int32_t 
 /* drows[slot_row[t, s]] = gate[t, s] dy[t],  dgate[t, s] = <dy[t], rows[...]>
  * (0 for a slot without a row).  drows and dgate are optional, one at least
  * is required; rows may be NULL when dgate is.  Rows that no slot names are
- * left as they were; no row may be named twice, and drows must not overlap
- * rows. */
+ * left as they were; no row may be named twice, and no output may overlap an
+ * input. */
 moe_status moe_combine_backward(int32_t T, int32_t k, int32_t n_rows, int32_t d, int32_t dtype,
                                 const void* rows, const int32_t* slot_row, const float* gate,
                                 const void* dy, void* drows, float* dgate, void* stream);

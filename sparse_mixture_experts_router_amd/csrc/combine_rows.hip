@@ -22,7 +22,7 @@ inline int token_threads(int d) {
 }
 
 // KS: slots whose rows are asked for together.  Rows are read once and results
-// written once, past the caches: 8192 tokens x 8 rows of 7168 219 us with plain
+// written once, in bf16 past the caches (fp32 by plain accesses): 8192 tokens x 8 rows of 7168 219 us with plain
 // loads and stores, 4 slots; 204 with 8 slots and non-temporal loads, 188 with
 // non-temporal stores too (5.6 TB/s).
 template <typename T, int KS>

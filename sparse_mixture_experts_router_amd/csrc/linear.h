@@ -234,8 +234,8 @@ template <> __device__ __forceinline__ float sigmoid<bf16_t>(float z) {
 // which shares its exponential with the density.  Evaluated in fp32 for the
 // tail it is within 3e-7 of the CDF, and z times it within 2^-9 of GELU for
 // z > -5, where GELU is -1.4e-6, and 2^-8 (half a bf16 step) for z > -6; below
-// it is off by 1 % at -8, 2 % at -10, of values under 6e-9.  4096 tokens' gate and up rows
-// (8192 x 28672 values) cost a forward 210 us with erff, 105 this way.
+// it is off by 1 % at -8, 2 % at -10, of values under 6e-9.  4096 tokens' gate
+// and up rows (8192 x 28672 values) cost a forward 210 us with erff, 105 this way.
 template <typename T> __device__ __forceinline__ float normal_cdf(float z, float& e);
 template <> __device__ __forceinline__ float normal_cdf<float>(float z, float& e) {
   e = expf(-0.5f * z * z);
@@ -363,7 +363,7 @@ __device__ __forceinline__ void load_cols8(const float* p, size_t at, bool ok, f
   }
 }
 // 8 values as they lie in memory, widened when they are used, so that a caller
-// can have many in flight.
+// can have many in flight.  Read once: bf16 past the caches.
 template <typename T> struct Raw8;
 template <> struct Raw8<bf16_t> {
   u32x4 r;
@@ -392,8 +392,8 @@ __device__ __forceinline__ void load_residual(const LinearArgs& g, long row, int
   else
     r.zero();
 }
-// y is not read again by the launch that writes it: past the caches, where
-// the rows of x and W that other tiles use stay longer.
+// y is not read again by the launch that writes it: bf16 goes past the caches,
+// where the rows of x and W that other tiles use stay longer.
 template <typename T> __device__ __forceinline__ void store_once8(T* p, const float* v);
 template <> __device__ __forceinline__ void store_once8<bf16_t>(bf16_t* p, const float* v) {
   u32x4 w;

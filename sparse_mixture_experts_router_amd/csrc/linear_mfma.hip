@@ -5,8 +5,8 @@
 //   dX       dX[r] = dz[r] W_e
 //   dW       dW_e = sum_r dz[r]^T x[src(r)]
 //
-// bound by the matrix cores: a tile does 512 operations for each byte that it
-// stages.  One workgroup of 8 wavefronts, two on each SIMD, owns a tile and
+// bound by the matrix cores and by L2 -> LDS bytes: a tile does 128 operations
+// for each byte that it stages.  One workgroup of 8 wavefronts, two on each SIMD, owns a tile and
 // the whole LDS; a wavefront accumulates a quarter of the rows and half of the
 // columns in AGPRs.  A stage is 64 elements of K.  The wavefronts of a SIMD
 // take turns: while one runs its 64 MFMAs of a stage from registers, the other
