@@ -22,19 +22,20 @@ inline int token_threads(int d) {
 }
 
 // KS: slots whose rows are asked for together.  Rows are read once and results
-// written once, in bf16 past the caches (fp32 by plain accesses): 8192 tokens x 8 rows of 7168 219 us with plain
-// loads and stores, 4 slots; 204 with 8 slots and non-temporal loads, 188 with
-// non-temporal stores too (5.6 TB/s).
+// written once, in bf16 past the caches (fp32 by plain accesses): 8192 tokens x
+// 8 rows of 7168 219 us with plain loads and stores, 4 slots; 204 with 8 slots
+// and non-temporal loads, 188 with non-temporal stores too (5.6 TB/s).  Columns
+// are unsigned: the step past the last may pass 2^31.
 template <typename T, int KS>
 __global__ __launch_bounds__(512) void combine_rows_kernel(const T* __restrict__ rows,
                                                            const int32_t* __restrict__ slot_row,
                                                            const float* __restrict__ gate,
-                                                           int n_rows, int k, int d,
+                                                           int n_rows, int k, unsigned d,
                                                            T* __restrict__ y) {
   const size_t t = blockIdx.x;
   const int32_t* sr = slot_row + t * k;
   const float* gt = gate != nullptr ? gate + t * k : nullptr;
-  for (int c = threadIdx.x * 8; c < d; c += blockDim.x * 8) {
+  for (unsigned c = threadIdx.x * 8; c < d; c += blockDim.x * 8) {
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
@@ -65,7 +66,7 @@ __global__ __launch_bounds__(512) void combine_rows_kernel(const T* __restrict__
 template <typename T, int KS>
 __global__ __launch_bounds__(512) void combine_rows_backward_kernel(
     const T* __restrict__ rows, const int32_t* __restrict__ slot_row,
-    const float* __restrict__ gate, const T* __restrict__ dy, int n_rows, int k, int d,
+    const float* __restrict__ gate, const T* __restrict__ dy, int n_rows, int k, unsigned d,
     T* __restrict__ drows, float* __restrict__ dgate) {
   __shared__ float s_dot[KS][8];
   const size_t t = blockIdx.x;
@@ -81,7 +82,7 @@ __global__ __launch_bounds__(512) void combine_rows_backward_kernel(
       w[q] = gate != nullptr && row[q] >= 0 ? gate[t * k + s0 + q] : 1.f;
       dot[q] = 0.f;
     }
-    for (int c = threadIdx.x * 8; c < d; c += blockDim.x * 8) {
+    for (unsigned c = threadIdx.x * 8; c < d; c += blockDim.x * 8) {
       float g[8];
       Raw8<T> v[KS];
       if (dgate != nullptr) {

@@ -182,3 +182,25 @@ def test_rows_gathered_from_four_gigabytes():
                 ("dw", dw[e], de.t() @ xe, de.abs().t() @ xe.abs(), n)):
             tol = (1 + V) * (k + 8) * U * terms + V * ref.abs()
             check(f"{name}[{e}]", got, ref.cpu().numpy(), tol.cpu().numpy())
+
+
+def test_combine_of_the_widest_rows():
+    """d = 2^31 - 64: columns up to the last that 31 bits can count."""
+    say("[combine] widest rows")
+    d = (1 << 31) - 64
+    rows = torch.empty((2, d), dtype=torch.bfloat16, device=DEV)
+    rows[0].fill_(float("nan"))
+    rows[1].view(-1, 64).copy_(torch.arange(64, device=DEV, dtype=torch.bfloat16))
+    rows[1, -1] = 77
+    guard = poison((d + 8192,), torch.bfloat16)
+    y, tail = guard[:d].view(1, d), guard[d:]
+    slot = torch.tensor([[1]], dtype=torch.int32, device=DEV)
+    moe.moe_combine(rows, slot, y)
+    torch.cuda.synchronize()
+    assert torch.equal(y[0].view(torch.int16), rows[1].view(torch.int16))
+    assert bool(torch.isnan(tail).all())
+    drows = poison((2, d), torch.bfloat16)
+    moe.moe_combine_backward(rows, slot, None, y, drows, None)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(drows[0]).all())
+    assert torch.equal(drows[1].view(torch.int16), rows[1].view(torch.int16))
