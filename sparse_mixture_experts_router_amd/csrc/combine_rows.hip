@@ -128,7 +128,7 @@ __global__ __launch_bounds__(512) void combine_rows_backward_kernel(
 constexpr int kGatherRows = 4;
 __global__ __launch_bounds__(256) void gather_rows_kernel(LinearArgs g, bf16_t* __restrict__ xg) {
   const int r0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * kGatherRows, lane = threadIdx.x & 63;
-  const int n = min(g.offsets[g.groups], g.rows) - r0;  // rows of x left
+  const int n = min(max(g.offsets[g.groups], 0), g.rows) - r0;  // rows of x left
   if (n <= 0) return;
   const bf16_t* x[kGatherRows];
 #pragma unroll

@@ -204,3 +204,30 @@ def test_combine_of_the_widest_rows():
     torch.cuda.synchronize()
     assert bool(torch.isnan(drows[0]).all())
     assert torch.equal(drows[1].view(torch.int16), rows[1].view(torch.int16))
+
+
+@pytest.mark.parametrize("last", [-(1 << 31), -(1 << 31) + 5, -1, (1 << 31) - 1])
+def test_gathered_rows_stay_inside_whatever_the_offsets(last):
+    """dW of rows read through row_index, on the large tiles, with a last
+    offset far outside [0, rows]: nothing past the workspace is written."""
+    say(f"[linear] gather with last offset {last}")
+    rows, K, F = 37, 2048, 2048
+    cfg = moe.make_linear_config(rows, 2, K, F, x_rows=11)
+    n = moe.moe_linear_backward_workspace_size(cfg)
+    space = torch.full((n + (1 << 20),), 0xA5, dtype=torch.uint8, device=DEV)
+    x, dy = (torch.randn((r, c), device=DEV).bfloat16() for r, c in ((11, K), (rows, F)))
+    index = (torch.arange(rows, device=DEV) % 11).int()
+    dw = poison((2, F, K), torch.bfloat16)
+    moe.moe_grouped_linear_backward(
+        cfg, x, torch.tensor([0, 20, last], dtype=torch.int32, device=DEV), None, dy,
+        row_index=index, dw=dw, workspace=space[:n])
+    torch.cuda.synchronize()
+    assert bool((space[n:] == 0xA5).all())
+    if last > 0:
+        for e, r in ((0, slice(0, 20)), (1, slice(20, rows))):
+            de, xe = dy[r].double(), x[index[r].long()].double()
+            ref = (de.t() @ xe).cpu().numpy()
+            terms = (de.abs().t() @ xe.abs()).cpu().numpy()
+            check(f"dw[{e}]", dw[e], ref, (1 + V) * 45 * U * terms + V * np.abs(ref))
+    else:
+        assert bool((dw[1] == 0).all())  # the second group has no rows
