@@ -487,11 +487,20 @@ class _Call:
         return stream.cuda_stream
 
 
+def _int32(sizes: int) -> None:
+    """Refuses sizes, given or-ed together, that do not fit 32 bits: ctypes
+    would take their low bits without a word (the library refuses negative
+    ones)."""
+    if sizes > 0x7FFFFFFF:
+        raise ValueError("a size does not fit 32 bits")
+
+
 def _nbytes(workspace: torch.Tensor) -> int:
     return workspace.numel() * workspace.element_size()
 
 
 def moe_group_workspace_size(T: int, n_experts: int, top_k: int) -> int:
+    _int32(int(T) | int(n_experts) | int(top_k))
     return int(lib().moe_group_workspace_size(int(T), int(n_experts), int(top_k)))
 
 
@@ -512,6 +521,7 @@ def moe_group_rows(topk_idx: torch.Tensor, n_experts: int, offsets: torch.Tensor
     [T k] and ``slot_row`` [T, k] from ``topk_idx`` [T, k] (all int32); see
     ``moe_group_rows`` in include/moe.h."""
     T, k = topk_idx.shape
+    _int32(T | k | int(n_experts) | int(capacity))
     c = _Call(topk_idx)
     i32 = torch.int32
     c.run(lib().moe_group_rows, stream, T, int(n_experts), k, int(capacity),
@@ -530,6 +540,7 @@ def make_linear_config(rows: int, groups: int, in_dim: int, out_dim: int, *,
         raise ValueError(f"activation {activation!r} is none of {ACTIVATIONS}")
     if dtype not in (torch.bfloat16, torch.float32, "bf16", "f32", MOE_BF16, MOE_F32):
         raise ValueError(f"dtype {dtype}, expected bfloat16 or float32")
+    _int32(int(rows) | int(x_rows) | int(groups) | int(in_dim) | int(out_dim))
     code = MOE_BF16 if dtype in (torch.bfloat16, "bf16", MOE_BF16) else MOE_F32
     return MoELinearConfig(int(rows), int(x_rows), int(groups), int(in_dim), int(out_dim), code,
                            int(weight_format), ACTIVATIONS.index(activation))
@@ -623,6 +634,7 @@ def moe_checkpoint_pack(x: torch.Tensor, codes: torch.Tensor, scale: torch.Tenso
     """x [rows, cols] as E4M3 ``codes`` (uint8) and one fp32 ``scale`` for each
     64 columns of a row; see ``moe_checkpoint_pack`` in include/moe.h."""
     rows, cols = x.shape
+    _int32(cols)
     c = _Call(x)
     c.run(lib().moe_checkpoint_pack, stream, rows, cols, _dtype_code(x, "x"),
           c.ptr(x, x.dtype, "x", (rows, cols)), c.ptr(codes, torch.uint8, "codes", (rows, cols)),
@@ -633,6 +645,7 @@ def moe_checkpoint_unpack(codes: torch.Tensor, scale: torch.Tensor, x: torch.Ten
                           stream=None) -> None:
     """x [rows, cols] = codes * scale; see ``moe_checkpoint_unpack`` in include/moe.h."""
     rows, cols = x.shape
+    _int32(cols)
     c = _Call(x)
     c.run(lib().moe_checkpoint_unpack, stream, rows, cols, _dtype_code(x, "x"),
           c.ptr(codes, torch.uint8, "codes", (rows, cols)),
@@ -645,6 +658,7 @@ def moe_combine(rows: torch.Tensor, slot_row: torch.Tensor, y: torch.Tensor, *,
     """y[t] = sum_s gate[t, s] rows[slot_row[t, s]] (no gate: 1); see
     ``moe_combine`` in include/moe.h."""
     (n_rows, d), (T, k) = rows.shape, slot_row.shape
+    _int32(n_rows | d | T | k)
     c = _Call(y)
     c.run(lib().moe_combine, stream, T, k, n_rows, d, _dtype_code(rows, "rows"),
           c.ptr(rows, rows.dtype, "rows", (n_rows, d)),
@@ -659,6 +673,7 @@ def moe_combine_backward(rows: torch.Tensor, slot_row: torch.Tensor,
     """Gradients of moe_combine with respect to its rows and gates; see
     ``moe_combine_backward`` in include/moe.h."""
     (n_rows, d), (T, k) = rows.shape, slot_row.shape
+    _int32(n_rows | d | T | k)
     c = _Call(dy)
     c.run(lib().moe_combine_backward, stream, T, k, n_rows, d, _dtype_code(rows, "rows"),
           c.ptr(rows, rows.dtype, "rows", (n_rows, d)),

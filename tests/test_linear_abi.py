@@ -263,3 +263,34 @@ def test_binding_refuses_tensors():
         moe.alloc_linear_workspace(moe.make_linear_config(8, 2, 60, 64), "cpu")
     with pytest.raises(moe.MoEError):
         moe.alloc_group_workspace(8, 1000, 2, "cpu")
+
+
+def test_sizes_past_32_bits_are_refused():
+    """2^32 + n is not n, in shapes (of tensors that take no memory) or numbers."""
+    def wide(*shape, dtype=torch.bfloat16):
+        return torch.zeros(1, dtype=dtype).expand(*shape)
+
+    big, i32 = (1 << 32) + 64, torch.int32
+    ws = torch.zeros(256, dtype=torch.uint8)
+    calls = [
+        lambda: moe.moe_combine(wide(1, big), wide(1, 1, dtype=i32), wide(1, big)),
+        lambda: moe.moe_combine(wide(big, 64), wide(1, 1, dtype=i32), wide(1, 64)),
+        lambda: moe.moe_combine(wide(1, 64), wide(big, 1, dtype=i32), wide(big, 64)),
+        lambda: moe.moe_combine_backward(wide(1, big), wide(1, 1, dtype=i32), None, wide(1, big),
+                                         wide(1, big), None),
+        lambda: moe.moe_checkpoint_pack(wide(1, big), wide(1, big, dtype=torch.uint8),
+                                        wide(1, big // 64, dtype=torch.float32)),
+        lambda: moe.moe_checkpoint_unpack(wide(1, big, dtype=torch.uint8),
+                                          wide(1, big // 64, dtype=torch.float32), wide(1, big)),
+        lambda: moe.moe_group_rows(wide(big, 1, dtype=i32), 8, wide(9, dtype=i32),
+                                   wide(big, dtype=i32), wide(big, 1, dtype=i32), workspace=ws),
+        lambda: moe.moe_group_rows(wide(4, 1, dtype=i32), 8, wide(9, dtype=i32),
+                                   wide(4, dtype=i32), wide(4, 1, dtype=i32), workspace=ws,
+                                   capacity=(1 << 32) + 1),
+        lambda: moe.alloc_group_workspace(big, 8, 2, "cpu"),
+        lambda: moe.make_linear_config(big, 1, 64, 64),
+        lambda: moe.make_linear_config(8, 1, 64, big),
+    ]
+    for call in calls:
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
