@@ -399,9 +399,10 @@ moe_status moe_update_select_bias(int32_t N, const int32_t* counts, float rate,
  * The rows of an expert are in the flat order of their (token, slot) pairs.
  * capacity: 0, or the most pairs an expert keeps, its first ones (as in
  * moe_config).  A pair whose index lies outside [0, N) gets no row: -1 marks
- * the slots of padding.  No output may overlap topk_idx.  1 <= N <= 512, k <= 16, T k < 2^30; T = 0 writes
- * offsets only.  workspace: moe_group_workspace_size(T, N, k) bytes, 256-byte
- * aligned (the size is 0 for sizes outside these). */
+ * the slots of padding.  No output may overlap topk_idx.  1 <= N <= 512,
+ * k <= 16, T k < 2^30; T = 0 writes offsets only.  workspace:
+ * moe_group_workspace_size(T, N, k) bytes, 256-byte aligned (the size is 0 for
+ * sizes outside these). */
 size_t moe_group_workspace_size(int32_t T, int32_t N, int32_t k);
 moe_status moe_group_rows(int32_t T, int32_t N, int32_t k, int32_t capacity,
                           const int32_t* topk_idx, int32_t* offsets, int32_t* row_token,
@@ -496,7 +497,7 @@ moe_status moe_grouped_linear_backward(const moe_linear_config* cfg,
                                        size_t ws_bytes, void* stream);
 
 /* 8-bit activation checkpoints.  x [rows, cols] (dtype a moe_dtype, cols a
- * multiple of 64) is held as one OCP E4M3 code for each element and one fp32
+ * multiple of 64, rows cols <= 2^35) is held as one OCP E4M3 code for each element and one fp32
  * scale for each block of 64 columns of a row:
  *   m = max(max |x| over the block, 1e-30),  scale = m / 448,
  *   code = E4M3(x * (448 / m)), to nearest even;  unpack: code * scale,

@@ -294,3 +294,12 @@ def test_sizes_past_32_bits_are_refused():
     for call in calls:
         with pytest.raises(ValueError, match="32 bits"):
             call()
+
+
+def test_limit_of_a_checkpoint():
+    """Up to 2^35 elements only the alignment is refused."""
+    for fn in (moe.lib().moe_checkpoint_pack, moe.lib().moe_checkpoint_unpack):
+        for cols in (64, 192, 1 << 30):
+            rows = (1 << 35) // cols
+            assert fn(rows, cols, 1, FAKE + 8, FAKE, FAKE, None) == INVALID
+            assert fn(rows + 1, cols, 1, FAKE + 8, FAKE, FAKE, None) == UNSUPPORTED
