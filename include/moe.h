@@ -497,8 +497,8 @@ moe_status moe_grouped_linear_backward(const moe_linear_config* cfg,
                                        size_t ws_bytes, void* stream);
 
 /* 8-bit activation checkpoints.  x [rows, cols] (dtype a moe_dtype, cols a
- * multiple of 64, rows cols <= 2^35) is held as one OCP E4M3 code for each element and one fp32
- * scale for each block of 64 columns of a row:
+ * multiple of 64, rows cols <= 2^35) is held as one OCP E4M3 code for each
+ * element and one fp32 scale for each block of 64 columns of a row:
  *   m = max(max |x| over the block, 1e-30),  scale = m / 448,
  *   code = E4M3(x * (448 / m)), to nearest even;  unpack: code * scale,
  * so an element is off by at most 2^-4 of itself, or scale 2^-10 where that
