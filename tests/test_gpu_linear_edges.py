@@ -129,7 +129,8 @@ def test_checkpoint_of_a_forward_that_is_not_finite(sizes, K, F, act, dtype):
     c.bias[0, c.zd - 64:] = float("-inf")  # a block without a finite value
     y, codes, scale = c.forward(True)
     torch.cuda.synchronize()
-    ref, z = lo.grouped_linear(c.hx, c.off, c.hw, act, None, to_np(c.bias))
+    with np.errstate(invalid="ignore"):  # -inf * 0
+        ref, z = lo.grouped_linear(c.hx, c.off, c.hw, act, None, to_np(c.bias))
     n = c.rows
     ok = np.isfinite(z)
     assert np.array_equal(np.isfinite(to_np(y)), np.isfinite(ref))
