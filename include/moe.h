@@ -528,6 +528,214 @@ moe_status moe_combine_backward(int32_t T, int32_t k, int32_t n_rows, int32_t d,
                                 const void* rows, const int32_t* slot_row, const float* gate,
                                 const void* dy, void* drows, float* dgate, void* stream);
 
+/* ------------------------------------------- FP8 with scales of blocks of 128
+ *
+ * Experts trained and served in 8 bits on both sides of the product.  Rows
+ * (activations, gradients) hold OCP E4M3 codes and one power of two for each
+ * block of 128 columns, an E8M0 byte: 2^(byte - 127).  Weights hold codes and
+ * one scale for each block of 128 x 128, E8M0 or fp32 (checkpoints bring fp32
+ * ones).  The last block of a dimension that is an odd multiple of 64 has 64.
+ *
+ *   moe_block_pack         rows, their activation or its gradient -> codes
+ *   moe_block_pack_weights weights -> codes, both ways round
+ *   moe_block_linear       codes x codes -> y, or y packed for the next product
+ *   moe_block_weight_grad  turned codes x turned codes -> dw
+ *   moe_adamw_step         the parameters' update
+ *
+ * A training step of SwiGLU experts: pack x (through row_index; also turned),
+ * moe_block_linear -> z, pack SWIGLU(z) (also turned), moe_block_linear -> rows
+ * of y; backwards pack dy (also turned), moe_block_linear with the weights
+ * packed the other way round -> dh, moe_block_weight_grad -> dw_down, pack
+ * SwiGLU's gradient from z and dh (also turned), moe_block_linear -> dx,
+ * moe_block_weight_grad -> dw.  The conventions at the top of this file hold;
+ * the calls are deterministic. */
+typedef enum {
+  MOE_SCALE_F32 = 0,  /* fp32 scales                                           */
+  MOE_SCALE_E8M0 = 1  /* bytes, 2^(byte - 127)                                 */
+} moe_scale_format;
+
+/* Bytes of one block column of scales of `rows` rows: the scale of row r and
+ * block b lies at [b * MOE_BLOCK_SCALE_LINE(rows) + r]. */
+#define MOE_BLOCK_SCALE_LINE(rows) (((size_t)(rows) + 15) / 16 * 16)
+
+/* cols a multiple of 64 up to 2^21 (128 with the gradient of SwiGLU), rows
+ * < 2^27, x_rows < 2^30, groups <= 512, and
+ *   (rows / 128 + groups) (blocks of cols) <= 2^23     (rows / 128 rounded down).
+ * Other sizes are MOE_ERR_UNSUPPORTED. */
+typedef struct {
+  int32_t rows;       /* packed rows                                           */
+  int32_t x_rows;     /* rows of x when row_index is given; 0: x has `rows`    */
+  int32_t groups;     /* of offsets; 1 without                                 */
+  int32_t cols;       /* packed columns                                        */
+  int32_t dtype;      /* of x and dy, a moe_dtype                              */
+  int32_t activation; /* a moe_activation                                      */
+} moe_block_pack_config;
+
+/* The packed values v, computed in fp32:
+ *   dy NULL:  v[r] = act(x[src(r)])      x [.., cols], SWIGLU [.., 2 cols]
+ *   dy given: v[r] = dy[r] act'(x[src(r)])   x [.., cols]; dy [rows, cols], of
+ *             SWIGLU [rows, cols / 2] (v: the gate's gradient, then the up
+ *             projection's); MOE_ACT_NONE has none
+ * with src(r) = row_index[r] (clamped to x's rows) or r.  For a block,
+ *   e = the smallest integer >= -126 with max |v| <= 448 2^e,
+ *   byte = e + 127,  code = E4M3(v 2^-e), to nearest even:
+ * an element is off by at most 2^-4 of itself, or 2^(e - 10) where that is
+ * more.  NaN and infinities become the NaN code and do not count for e.
+ *
+ * The turned form, for the weight gradient, cuts each group's rows into blocks
+ * of 128; a column of a block has a scale of its own.  Group e's first block is
+ * offsets[e] / 128 + e (rounded down), and there is room for
+ * rows / 128 + groups blocks.  Places past a group's last row hold code 0;
+ * blocks of no group are left as they were, like rows of no group.
+ *
+ * codes (with scale) and codes_t (with scale_t) are optional, one at least is
+ * required.  offsets as in moe_linear_args, or NULL: all rows are one group.
+ * x, dy, codes and codes_t 16-byte aligned.  No output may overlap an input.
+ * rows = 0 launches nothing. */
+typedef struct {
+  const void* x;
+  const int32_t* row_index; /* [rows], or NULL when x_rows = 0                 */
+  const int32_t* offsets;   /* [groups + 1] or NULL                            */
+  const void* dy;           /* or NULL                                         */
+  uint8_t* codes;           /* [rows, cols]                                    */
+  uint8_t* scale;           /* [blocks of cols, MOE_BLOCK_SCALE_LINE(rows)]    */
+  uint8_t* codes_t;         /* [rows / 128 + groups, cols, 128]                */
+  uint8_t* scale_t;         /* [rows / 128 + groups, cols]                     */
+} moe_block_pack_args;
+
+moe_status moe_block_pack(const moe_block_pack_config* cfg, const moe_block_pack_args* a,
+                          void* stream);
+
+/* w [groups, out_dim, in_dim] (dtype a moe_dtype) in blocks of 128 x 128, by
+ * the rule above, as codes [groups, out_dim, in_dim] with scale
+ * [groups, blocks of out_dim, blocks of in_dim], and turned, for the product
+ * that gives dx, as codes_t [groups, in_dim, out_dim] with scale_t
+ * [groups, blocks of in_dim, blocks of out_dim]; each pair is optional, one is
+ * required.  Dimensions are multiples of 64 up to 2^21, and there are at most
+ * 2^23 blocks. */
+moe_status moe_block_pack_weights(int32_t groups, int32_t out_dim, int32_t in_dim, int32_t dtype,
+                                  const void* w, uint8_t* codes, uint8_t* scale, uint8_t* codes_t,
+                                  uint8_t* scale_t, void* stream);
+
+/* A linear map for each group of packed rows.  z_dim = out_dim, or 2 out_dim
+ * with MOE_ACT_SWIGLU (the gate's rows, then the up projection's).  Limits as
+ * for moe_linear_config. */
+typedef struct {
+  int32_t rows;
+  int32_t groups;
+  int32_t in_dim;
+  int32_t out_dim;
+  int32_t dtype;          /* of y (weight gradient: of dw), a moe_dtype        */
+  int32_t activation;     /* MOE_ACT_NONE or MOE_ACT_SWIGLU                    */
+  int32_t w_scale_format; /* a moe_scale_format                                */
+} moe_block_linear_config;
+
+/* z[r, n] = sum over blocks b of  x_scale[b, r] w_scale[e, n / 128, b]
+ *                                 (sum over k in b of x[r, k] w[e, n, k])
+ * y[r] = act(z[r]), for the rows r of every group e; codes and E8M0 scales
+ * stand for their values, and sums are fp32.  y is rounded once; y_codes and
+ * y_scale hold act(z) packed as moe_block_pack packs rows, from its fp32
+ * values.  The 8-bit matrix instruction drops, of each 8 products of neighbours
+ * in k, what lies under 2^-13 of the largest: about 1.4e-5 of the result's norm.
+ * With y in fp32 codes are widened to bf16 instead, at half the rate, and each
+ * product is exact (operands whose value is under 2^-126 may count as 0).  Either or both are given.  Rows of no group are left as they were.
+ * offsets as in moe_linear_args.  A NaN code gives NaN; the E8M0 byte 255 is
+ * not a scale.  x, w, y and y_codes 16-byte aligned.  No output may overlap an
+ * input. */
+typedef struct {
+  const uint8_t* x;       /* [rows, in_dim]                                    */
+  const uint8_t* x_scale; /* [blocks of in_dim, MOE_BLOCK_SCALE_LINE(rows)]    */
+  const int32_t* offsets; /* [groups + 1]                                      */
+  const uint8_t* w;       /* [groups, z_dim, in_dim]                           */
+  const void* w_scale;    /* [groups, blocks of z_dim, blocks of in_dim]       */
+  void* y;                /* [rows, out_dim] or NULL                           */
+  uint8_t* y_codes;       /* [rows, out_dim] or NULL                           */
+  uint8_t* y_scale;       /* [blocks of out_dim, MOE_BLOCK_SCALE_LINE(rows)]   */
+} moe_block_linear_args;
+
+size_t moe_block_linear_workspace_size(const moe_block_linear_config* cfg);
+moe_status moe_block_linear(const moe_block_linear_config* cfg, const moe_block_linear_args* a,
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/* dw[e, n, k] = sum over the rows r of group e of dy[r, n] x[r, k], from the
+ * turned forms of dy [rows, out_dim] and x [rows, in_dim]; groups without rows
+ * get zeros.  cfg's activation is MOE_ACT_NONE and its w_scale_format is not
+ * looked at (scales are E8M0).  Codes and dw 16-byte aligned, scales 4-byte. */
+typedef struct {
+  const uint8_t* x_t;        /* [rows / 128 + groups, in_dim, 128]             */
+  const uint8_t* x_scale_t;  /* [rows / 128 + groups, in_dim]                  */
+  const uint8_t* dy_t;       /* [rows / 128 + groups, out_dim, 128]            */
+  const uint8_t* dy_scale_t; /* [rows / 128 + groups, out_dim]                 */
+  const int32_t* offsets;    /* [groups + 1]                                   */
+  void* dw;                  /* [groups, out_dim, in_dim]                      */
+} moe_block_weight_grad_args;
+
+size_t moe_block_weight_grad_workspace_size(const moe_block_linear_config* cfg);
+moe_status moe_block_weight_grad(const moe_block_linear_config* cfg,
+                                 const moe_block_weight_grad_args* a, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------- AdamW
+ *
+ * One step over `count` tensors, in place and in fp32:
+ *   g = grad_scale grad,  m = beta1 m + (1 - beta1) g,
+ *   v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * with p the master copy where there is one (param then gets it, rounded to
+ * nearest), else param.
+ *
+ * States in 8 bits hold codes c and two scales for each 256 elements of a
+ * tensor:  m = m_scale c |c|  (int8),  sqrt(v) = v_scale c^2  (uint8), the
+ * scales being the block's largest |m| / 127^2 and sqrt(v) / 255^2.  A state is
+ * rounded up or down at random so that m and v are kept on average; bf16
+ * parameters without a master are, too.  The draws come from the seed, the
+ * tensor's place in the list and the element's: a call repeats bit for bit,
+ * and each step is to have another seed.  A gradient that is not finite spoils
+ * its element, with states in 8 bits its block.
+ *
+ * The tensors' list is read on the host before the call returns.  Tensors must
+ * not overlap; n = 0 is skipped.  Pointers need their element's alignment (16
+ * bytes, codes 8, for wide accesses).
+ *
+ * scalars: NULL, or five 32-bit words on the device that stand for lr,
+ * 1 - beta1^step, 1 - beta2^step, grad_scale (fp32) and seed (uint32) instead
+ * of cfg's: a captured graph follows a schedule through them.  grad_scale = 0
+ * leaves everything as it was (a step to be skipped). */
+typedef enum {
+  MOE_STATES_F32 = 0,
+  MOE_STATES_8BIT = 1
+} moe_state_format;
+
+typedef struct {
+  double lr;
+  double beta1;         /* 0 <= beta1, beta2 < 1                               */
+  double beta2;
+  double eps;           /* >= 0                                                */
+  double grad_scale;
+  int64_t step;         /* from 1 on (not looked at with scalars)              */
+  const void* scalars;  /* device, or NULL                                     */
+  uint32_t seed;
+  int32_t dtype;        /* of param, a moe_dtype                               */
+  int32_t grad_dtype;   /* of grad, a moe_dtype                                */
+  int32_t state_format; /* a moe_state_format                                  */
+} moe_adamw_config;
+
+typedef struct {
+  void* param;          /* [n]                                                 */
+  const void* grad;     /* [n]                                                 */
+  void* m;              /* [n] fp32, or int8 codes                             */
+  void* v;              /* [n] fp32, or uint8 codes of sqrt(v)                 */
+  float* master;        /* [n] with bf16 parameters, or NULL                   */
+  float* m_scale;       /* [n / 256, rounded up], states in 8 bits only        */
+  float* v_scale;
+  int64_t n;            /* <= 2^40                                             */
+  float weight_decay;
+} moe_adamw_tensor;
+
+moe_status moe_adamw_step(const moe_adamw_config* cfg, int32_t count,
+                          const moe_adamw_tensor* tensors, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,201 @@
+"""Plain oracle of the calls in 8-bit floating point with a scale for each
+block of 128, and of the AdamW step (test infrastructure only).
+
+Products and activations are float64, one group at a time, from the formulas
+in include/moe.h.  Codes of values that are exact in float32 are bytes that
+have to match; the AdamW step is written in float32, operation by operation,
+for its 8-bit codes are decided there.
+"""
+
+from __future__ import annotations
+
+import numpy as np
+
+from .linear_oracle import activation, activation_backward
+from .moe_oracle import e4m3_decode
+
+__all__ = ["BLOCK", "exponent", "e4m3_encode", "pack_rows", "pack_weights", "turned_blocks",
+           "unpack_rows", "unpack_weights", "unpack_turned", "block_linear", "weight_grad",
+           "packed_values", "adamw"]
+
+BLOCK = 128
+
+
+def exponent(top):
+    """The smallest integer e >= -126 with top <= 448 2^e (top finite, >= 0)."""
+    top = np.asarray(top, dtype=np.float64)
+    f, x = np.frexp(top)
+    e = np.where(f <= 0.875, x - 9, x - 8)
+    return np.where(top > 0, np.maximum(e, -126), -126).astype(np.int64)
+
+
+def e4m3_encode(v):
+    """E4M3 bytes of v (|v| <= 448 or not finite: NaN), to nearest even."""
+    v = np.asarray(v, dtype=np.float64)
+    finite = np.isfinite(v)
+    a = np.abs(np.where(finite, v, 0.0))
+    x = np.maximum(np.frexp(a)[1] - 1, -6)           # 2^x <= a, or the subnormals' -6
+    q = np.rint(np.ldexp(a, 3 - x)).astype(np.int64)  # in steps of 2^(x - 3), ties to even
+    code = np.where(a > 0, q + (x + 6) * 8, 0)
+    return (np.where(finite, code, 0x7F) | np.where(np.signbit(v), 0x80, 0)).astype(np.uint8)
+
+
+def _top(v, axis):
+    return np.max(np.where(np.isfinite(v), np.abs(v), 0.0), axis=axis)
+
+
+def _blocks(n):
+    return -(-n // BLOCK)
+
+
+def pack_rows(v):
+    """codes [rows, cols], bytes [blocks, rows]."""
+    rows, cols = v.shape
+    codes = np.zeros((rows, cols), dtype=np.uint8)
+    scale = np.zeros((_blocks(cols), rows), dtype=np.uint8)
+    for b in range(_blocks(cols)):
+        part = v[:, b * BLOCK:(b + 1) * BLOCK].astype(np.float64)
+        e = exponent(_top(part, 1))
+        scale[b] = e + 127
+        codes[:, b * BLOCK:(b + 1) * BLOCK] = e4m3_encode(part * np.exp2(-e.astype(np.float64))[:, None])
+    return codes, scale
+
+
+def pack_weights(w):
+    """[out, in] -> codes, bytes [blocks of out, blocks of in]."""
+    out, d_in = w.shape
+    codes = np.zeros((out, d_in), dtype=np.uint8)
+    scale = np.zeros((_blocks(out), _blocks(d_in)), dtype=np.uint8)
+    for i in range(_blocks(out)):
+        for j in range(_blocks(d_in)):
+            at = (slice(i * BLOCK, (i + 1) * BLOCK), slice(j * BLOCK, (j + 1) * BLOCK))
+            part = w[at].astype(np.float64)
+            e = int(exponent(_top(part, None)))
+            scale[i, j] = e + 127
+            codes[at] = e4m3_encode(part * 2.0 ** -e)
+    return codes, scale
+
+
+def turned_blocks(offsets):
+    """(block, first row, end row) of every block of 128 rows of a group."""
+    for e in range(len(offsets) - 1):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        for i in range(0, b - a, BLOCK):
+            yield a // BLOCK + e + i // BLOCK, a + i, min(b, a + i + BLOCK)
+
+
+def unpack_rows(codes, scale):
+    """Values of packed rows (NaN codes: NaN)."""
+    rows, cols = codes.shape
+    s = np.exp2(scale[:, :rows].astype(np.float64) - 127).T
+    return e4m3_decode(codes).astype(np.float64) * np.repeat(s, BLOCK, axis=1)[:, :cols]
+
+
+def unpack_weights(codes, scale):
+    out, d_in = codes.shape
+    s = np.exp2(scale.astype(np.float64) - 127) if scale.dtype == np.uint8 else scale.astype(np.float64)
+    return (e4m3_decode(codes).astype(np.float64) *
+            np.repeat(np.repeat(s, BLOCK, axis=0)[:out], BLOCK, axis=1)[:, :d_in])
+
+
+def unpack_turned(codes, scale, offsets, rows):
+    """Rows [rows, cols] that the turned form stands for (0 for rows of no group)."""
+    v = np.zeros((rows, codes.shape[1]))
+    for b, r0, r1 in turned_blocks(offsets):
+        s = np.exp2(scale[b].astype(np.float64) - 127)
+        v[r0:r1] = (e4m3_decode(codes[b]).astype(np.float64) * s[:, None]).T[:r1 - r0]
+    return v
+
+
+def packed_values(act, x, dy=None):
+    """What moe_block_pack packs, from rows already gathered."""
+    x = x.astype(np.float64)
+    if dy is None:
+        return activation(act, x)
+    return activation_backward(act, x, dy.astype(np.float64))
+
+
+def block_linear(x, w, offsets, act="none"):
+    """z, sum of |terms| of z, and act(z), from unpacked x [rows, in] and w [groups, z, in]."""
+    z = np.zeros((x.shape[0], w.shape[1]))
+    s = np.zeros_like(z)
+    for e in range(len(offsets) - 1):
+        r = slice(int(offsets[e]), int(offsets[e + 1]))
+        z[r] = x[r] @ w[e].T
+        s[r] = np.abs(x[r]) @ np.abs(w[e]).T
+    return z, s, activation(act, z)
+
+
+def weight_grad(x, dy, offsets):
+    """dw [groups, out, in] and the sums of its |terms|."""
+    n = len(offsets) - 1
+    dw = np.zeros((n, dy.shape[1], x.shape[1]))
+    s = np.zeros_like(dw)
+    for e in range(n):
+        r = slice(int(offsets[e]), int(offsets[e + 1]))
+        dw[e] = dy[r].T @ x[r]
+        s[e] = np.abs(dy[r]).T @ np.abs(x[r])
+    return dw, s
+
+
+# ---------------------------------------------------------------- AdamW
+_F = np.float32
+
+
+def _mixed(h):
+    h = h ^ (h >> np.uint32(16))
+    h = h * np.uint32(0x85EBCA6B)
+    h = h ^ (h >> np.uint32(13))
+    h = h * np.uint32(0xC2B2AE35)
+    return h ^ (h >> np.uint32(16))
+
+
+def _padded(x):
+    return np.pad(x, (0, -len(x) % 256)).reshape(-1, 256)
+
+
+def adamw(param, grad, m, v, *, lr, beta1, beta2, eps, step, grad_scale=1.0, weight_decay=0.0,
+          seed=0, index=0, m_scale=None, v_scale=None, narrow=False):
+    """One step of one tensor in float32 (param: the master copy's values where
+    there is one).  Returns param, m, v, and in 8 bits m_scale and v_scale;
+    ``narrow``: param rounded to bf16 at random."""
+    n = len(param)
+    b1, b2, o1, o2 = _F(beta1), _F(beta2), _F(1 - beta1), _F(1 - beta2)
+    bias1, root2 = _F(1 - beta1 ** step), np.sqrt(_F(1 - beta2 ** step))
+    eight = m_scale is not None
+    with np.errstate(all="ignore"):
+        g = grad.astype(_F) * _F(grad_scale)
+        if eight:
+            q = _padded(m.astype(_F))
+            m = (q * np.abs(q) * m_scale[:, None]).reshape(-1)[:n]
+            q = _padded(v.astype(_F))
+            r = (q * q * v_scale[:, None]).reshape(-1)[:n]
+            v = r * r
+        m = m * b1 + g * o1
+        v = v * b2 + g * g * o2
+        root = np.sqrt(v)
+        p = param.astype(_F) * (_F(1) - _F(lr) * _F(weight_decay))
+        p = p - (_F(lr) / bias1) * (m / (root / root2 + _F(eps)))
+        i = np.arange(n, dtype=np.uint64)
+        salt = _mixed(np.array([(seed + index * 0x9E3779B9) & 0xFFFFFFFF], dtype=np.uint32))
+        noise = _mixed((i & np.uint64(0xFFFFFFFF)).astype(np.uint32) ^
+                       _mixed((i >> np.uint64(32)).astype(np.uint32) ^ salt))
+        out = [p, m, v]
+        if eight:
+            mb, rb = _padded(m), _padded(root)
+            ms, vs = np.max(np.abs(mb), axis=1) / _F(127 * 127), np.max(rb, axis=1) / _F(255 * 255)
+            y = np.where(ms[:, None] > 0, np.abs(mb) / ms[:, None], _F(0)).reshape(-1)[:n]
+            k = np.minimum(np.floor(np.sqrt(y)), _F(127))
+            u = (noise & np.uint32(0xFFFF)).astype(_F) * _F(2.0 ** -16)
+            c = np.minimum(k + (u * (_F(2) * k + _F(1)) < y - k * k), _F(127))
+            mc = (np.sign(m) * c).astype(np.int8)
+            y = np.where(vs[:, None] > 0, rb / vs[:, None], _F(0)).reshape(-1)[:n]
+            k = np.minimum(np.floor(np.sqrt(y)), _F(255))
+            u = (noise >> np.uint32(16)).astype(_F) * _F(2.0 ** -16)
+            k4, n2 = (k * k) * (k * k), (k + _F(1)) * (k + _F(1))
+            vc = np.minimum(k + (u * (n2 * n2 - k4) < y * y - k4), _F(255)).astype(np.uint8)
+            out = [p, mc, vc, ms, vs]
+        if narrow:
+            bits = p.view(np.uint32) + (_mixed(noise ^ np.uint32(0x5BD1E995)) & np.uint32(0xFFFF))
+            out[0] = np.where(np.isfinite(p), (bits & np.uint32(0xFFFF0000)).view(_F), p)
+    return out

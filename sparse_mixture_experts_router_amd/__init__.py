@@ -30,6 +30,14 @@ __all__ = [
     "moe_grouped_linear_backward", "moe_checkpoint_pack", "moe_checkpoint_unpack",
     "moe_group_workspace_size", "alloc_group_workspace", "moe_group_rows", "moe_combine",
     "moe_combine_backward",
+    "MOE_SCALE_F32", "MOE_SCALE_E8M0", "MOE_STATES_F32", "MOE_STATES_8BIT", "FP8_BLOCK",
+    "STATE_BLOCK", "MoEBlockPackConfig", "MoEBlockPackArgs", "MoEBlockLinearConfig",
+    "MoEBlockLinearArgs", "MoEBlockWeightGradArgs", "MoEAdamWConfig", "MoEAdamWTensor",
+    "AdamWTensors", "block_scale_shape", "block_turned_shape", "moe_block_pack",
+    "moe_block_pack_weights", "make_block_linear_config", "moe_block_linear_workspace_size",
+    "alloc_block_linear_workspace", "moe_block_linear", "moe_block_weight_grad_workspace_size",
+    "alloc_block_weight_grad_workspace", "moe_block_weight_grad", "make_adamw_tensors",
+    "moe_adamw_step",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,6 +50,10 @@ NOALLOC_SCRATCH_BYTES = 64 << 20   # MOE_NOALLOC_SCRATCH_BYTES of include/moe.h
 _SCALES = ("w_gate_scale", "w_up_scale", "w_down_scale", "ws_gate_scale", "ws_up_scale",
            "ws_down_scale")
 ACTIVATIONS = ("none", "relu", "gelu", "silu", "swiglu")   # moe_activation, in its order
+MOE_SCALE_F32, MOE_SCALE_E8M0 = 0, 1
+MOE_STATES_F32, MOE_STATES_8BIT = 0, 1
+FP8_BLOCK = 128     # elements that share one scale of packed rows and weights
+STATE_BLOCK = 256   # elements of a tensor that share the scales of 8-bit optimizer states
 CHECKPOINT_BLOCK = 64   # columns of a row that share one scale of an 8-bit checkpoint
 STAGES = ("route", "permute", "expert_up", "expert_down", "combine")
 BACKWARD_STAGES = ("route", "transpose_w", "recompute", "grad_h", "grad_x", "segments", "grad_w",
@@ -115,6 +127,43 @@ class MoELinearGradArgs(ctypes.Structure):
                  "dbias")]
 
 
+class MoEBlockPackConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("rows", "x_rows", "groups", "cols", "dtype", "activation")]
+
+
+class MoEBlockPackArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("x", "row_index", "offsets", "dy", "codes", "scale", "codes_t", "scale_t")]
+
+
+class MoEBlockLinearConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("rows", "groups", "in_dim", "out_dim", "dtype", "activation", "w_scale_format")]
+
+
+class MoEBlockLinearArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("x", "x_scale", "offsets", "w", "w_scale", "y", "y_codes", "y_scale")]
+
+
+class MoEBlockWeightGradArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("x_t", "x_scale_t", "dy_t", "dy_scale_t", "offsets", "dw")]
+
+
+class MoEAdamWConfig(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "grad_scale")] +
+                [("step", ctypes.c_int64), ("scalars", ctypes.c_void_p), ("seed", ctypes.c_uint32)] +
+                [(n, ctypes.c_int32) for n in ("dtype", "grad_dtype", "state_format")])
+
+
+class MoEAdamWTensor(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in
+                 ("param", "grad", "m", "v", "master", "m_scale", "v_scale")] +
+                [("n", ctypes.c_int64), ("weight_decay", ctypes.c_float)])
+
+
 _LIB = None
 
 
@@ -173,9 +222,23 @@ def lib() -> ctypes.CDLL:
         L.moe_checkpoint_unpack.argtypes = [i64, i32, i32, vp, vp, vp, vp]
         L.moe_combine.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp]
         L.moe_combine_backward.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+        bcfg = ctypes.POINTER(MoEBlockLinearConfig)
+        L.moe_block_pack.argtypes = [ctypes.POINTER(MoEBlockPackConfig),
+                                     ctypes.POINTER(MoEBlockPackArgs), vp]
+        L.moe_block_pack_weights.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+        L.moe_block_linear_workspace_size.argtypes = [bcfg]
+        L.moe_block_linear_workspace_size.restype = sz
+        L.moe_block_linear.argtypes = [bcfg, ctypes.POINTER(MoEBlockLinearArgs), vp, sz, vp]
+        L.moe_block_weight_grad_workspace_size.argtypes = [bcfg]
+        L.moe_block_weight_grad_workspace_size.restype = sz
+        L.moe_block_weight_grad.argtypes = [bcfg, ctypes.POINTER(MoEBlockWeightGradArgs), vp, sz,
+                                            vp]
+        L.moe_adamw_step.argtypes = [ctypes.POINTER(MoEAdamWConfig), i32,
+                                     ctypes.POINTER(MoEAdamWTensor), vp]
         for fn in (L.moe_group_rows, L.moe_grouped_linear, L.moe_grouped_linear_backward,
                    L.moe_checkpoint_pack, L.moe_checkpoint_unpack, L.moe_combine,
-                   L.moe_combine_backward):
+                   L.moe_combine_backward, L.moe_block_pack, L.moe_block_pack_weights,
+                   L.moe_block_linear, L.moe_block_weight_grad, L.moe_adamw_step):
             fn.restype = ctypes.c_int
         _LIB = L
     return _LIB
@@ -681,6 +744,218 @@ def moe_combine_backward(rows: torch.Tensor, slot_row: torch.Tensor,
           c.ptr(gate, torch.float32, "gate", (T, k)), c.ptr(dy, rows.dtype, "dy", (T, d)),
           c.ptr(drows, rows.dtype, "drows", (n_rows, d)),
           c.ptr(dgate, torch.float32, "dgate", (T, k)))
+
+
+# ---------------------------------------------------------------- FP8 with scales of blocks of 128
+def _blocks(n: int) -> int:
+    return -(-n // FP8_BLOCK)
+
+
+def block_scale_shape(rows: int, cols: int):
+    """Shape of the scales (uint8) of packed rows [rows, cols]: a line for each
+    block of 128 columns, with the scale of every row."""
+    return (_blocks(cols), (rows + 15) // 16 * 16)
+
+
+def block_turned_shape(rows: int, groups: int, cols: int):
+    """Shape of the turned codes of [rows, cols]; their scales have the first
+    two dimensions."""
+    return (rows // FP8_BLOCK + groups, cols, FP8_BLOCK)
+
+
+def _activation_code(activation: str) -> int:
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation {activation!r} is none of {ACTIVATIONS}")
+    return ACTIVATIONS.index(activation)
+
+
+def moe_block_pack(x: torch.Tensor, codes: Optional[torch.Tensor], scale: Optional[torch.Tensor],
+                   *, activation: str = "none", dy: Optional[torch.Tensor] = None,
+                   row_index: Optional[torch.Tensor] = None,
+                   offsets: Optional[torch.Tensor] = None,
+                   codes_t: Optional[torch.Tensor] = None,
+                   scale_t: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rows of x, their activation, or with ``dy`` its gradient, as E4M3
+    ``codes`` [rows, cols] and E8M0 ``scale`` (``block_scale_shape``), and turned
+    by groups of ``offsets`` as ``codes_t`` (``block_turned_shape``) and
+    ``scale_t`` (all uint8); see ``moe_block_pack`` in include/moe.h."""
+    act = _activation_code(activation)
+    gated = activation == "swiglu"
+    x_rows, x_cols = x.shape
+    cols = x_cols // 2 if gated and dy is None else x_cols
+    rows = x_rows if row_index is None else row_index.shape[0]
+    groups = 1 if offsets is None else offsets.shape[0] - 1
+    _int32(x_rows | x_cols | rows | max(groups, 0))
+    u8, i32 = torch.uint8, torch.int32
+    c = _Call(x)
+    cfg = MoEBlockPackConfig(rows, 0 if row_index is None else x_rows, groups, cols,
+                             _dtype_code(x, "x"), act)
+    turned = block_turned_shape(rows, groups, cols)
+    if gated and dy is None and x_cols % 2:
+        raise ValueError("x of SwiGLU needs an even number of columns")
+    a = MoEBlockPackArgs(
+        c.ptr(x, x.dtype, "x", (x_rows, x_cols)), c.ptr(row_index, i32, "row_index", (rows,)),
+        c.ptr(offsets, i32, "offsets", (groups + 1,)),
+        c.ptr(dy, x.dtype, "dy", (rows, cols // 2 if gated else cols)),
+        c.ptr(codes, u8, "codes", (rows, cols)),
+        c.ptr(scale, u8, "scale", block_scale_shape(rows, cols)),
+        c.ptr(codes_t, u8, "codes_t", turned), c.ptr(scale_t, u8, "scale_t", turned[:2]))
+    c.run(lib().moe_block_pack, stream, ctypes.byref(cfg), ctypes.byref(a))
+
+
+def moe_block_pack_weights(w: torch.Tensor, codes: Optional[torch.Tensor],
+                           scale: Optional[torch.Tensor], *,
+                           codes_t: Optional[torch.Tensor] = None,
+                           scale_t: Optional[torch.Tensor] = None, stream=None) -> None:
+    """w [groups, out, in] as E4M3 ``codes`` with an E8M0 ``scale`` for each block
+    of 128 x 128 [groups, out / 128, in / 128], and the other way round as
+    ``codes_t`` [groups, in, out] with ``scale_t`` (all uint8); see
+    ``moe_block_pack_weights`` in include/moe.h."""
+    n, out, d_in = w.shape
+    _int32(n | out | d_in)
+    u8, ob, ib = torch.uint8, _blocks(out), _blocks(d_in)
+    c = _Call(w)
+    c.run(lib().moe_block_pack_weights, stream, n, out, d_in, _dtype_code(w, "w"),
+          c.ptr(w, w.dtype, "w", (n, out, d_in)), c.ptr(codes, u8, "codes", (n, out, d_in)),
+          c.ptr(scale, u8, "scale", (n, ob, ib)), c.ptr(codes_t, u8, "codes_t", (n, d_in, out)),
+          c.ptr(scale_t, u8, "scale_t", (n, ib, ob)))
+
+
+def make_block_linear_config(rows: int, groups: int, in_dim: int, out_dim: int, *,
+                             dtype=torch.bfloat16, activation: str = "none",
+                             w_scale_format="e8m0") -> MoEBlockLinearConfig:
+    """``dtype``: of the result.  ``activation``: "none" or "swiglu".
+    ``w_scale_format``: "e8m0" (as moe_block_pack_weights makes them) or "f32"."""
+    if dtype not in (torch.bfloat16, torch.float32, "bf16", "f32", MOE_BF16, MOE_F32):
+        raise ValueError(f"dtype {dtype}, expected bfloat16 or float32")
+    formats = {"f32": MOE_SCALE_F32, "e8m0": MOE_SCALE_E8M0}
+    if w_scale_format not in (*formats, MOE_SCALE_F32, MOE_SCALE_E8M0):
+        raise ValueError(f"w_scale_format {w_scale_format!r}, expected 'e8m0' or 'f32'")
+    _int32(int(rows) | int(groups) | int(in_dim) | int(out_dim))
+    code = MOE_BF16 if dtype in (torch.bfloat16, "bf16", MOE_BF16) else MOE_F32
+    return MoEBlockLinearConfig(int(rows), int(groups), int(in_dim), int(out_dim), code,
+                                _activation_code(activation),
+                                formats.get(w_scale_format, w_scale_format))
+
+
+def moe_block_linear_workspace_size(cfg: MoEBlockLinearConfig) -> int:
+    return int(lib().moe_block_linear_workspace_size(ctypes.byref(cfg)))
+
+
+def alloc_block_linear_workspace(cfg: MoEBlockLinearConfig, device="cuda") -> torch.Tensor:
+    return _alloc(moe_block_linear_workspace_size(cfg), device)
+
+
+def moe_block_linear(cfg: MoEBlockLinearConfig, x: torch.Tensor, x_scale: torch.Tensor,
+                     offsets: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
+                     workspace: torch.Tensor, y: Optional[torch.Tensor] = None,
+                     y_codes: Optional[torch.Tensor] = None,
+                     y_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y[r] = act(x[r] W_e^T) for the rows of every group, x and W as packed
+    codes with their scales, y in cfg's dtype, or packed as ``y_codes`` and
+    ``y_scale``, or both; see ``moe_block_linear`` in include/moe.h."""
+    u8, z = torch.uint8, _z_dim(cfg)
+    c = _Call(x)
+    a = MoEBlockLinearArgs(
+        c.ptr(x, u8, "x", (cfg.rows, cfg.in_dim)),
+        c.ptr(x_scale, u8, "x_scale", block_scale_shape(cfg.rows, cfg.in_dim)),
+        c.ptr(offsets, torch.int32, "offsets", (cfg.groups + 1,)),
+        c.ptr(w, u8, "w", (cfg.groups, z, cfg.in_dim)),
+        c.ptr(w_scale, u8 if cfg.w_scale_format == MOE_SCALE_E8M0 else torch.float32, "w_scale",
+              (cfg.groups, _blocks(z), _blocks(cfg.in_dim))),
+        c.ptr(y, _TORCH_DTYPE[cfg.dtype], "y", (cfg.rows, cfg.out_dim)),
+        c.ptr(y_codes, u8, "y_codes", (cfg.rows, cfg.out_dim)),
+        c.ptr(y_scale, u8, "y_scale", block_scale_shape(cfg.rows, cfg.out_dim)))
+    c.run(lib().moe_block_linear, stream, ctypes.byref(cfg), ctypes.byref(a),
+          c.workspace(workspace), _nbytes(workspace))
+
+
+def moe_block_weight_grad_workspace_size(cfg: MoEBlockLinearConfig) -> int:
+    return int(lib().moe_block_weight_grad_workspace_size(ctypes.byref(cfg)))
+
+
+def alloc_block_weight_grad_workspace(cfg: MoEBlockLinearConfig, device="cuda") -> torch.Tensor:
+    return _alloc(moe_block_weight_grad_workspace_size(cfg), device)
+
+
+def moe_block_weight_grad(cfg: MoEBlockLinearConfig, x_t: torch.Tensor, x_scale_t: torch.Tensor,
+                          dy_t: torch.Tensor, dy_scale_t: torch.Tensor, offsets: torch.Tensor,
+                          dw: torch.Tensor, *, workspace: torch.Tensor, stream=None) -> None:
+    """dw [groups, out, in] = dy^T x over the rows of every group, from their
+    turned forms; see ``moe_block_weight_grad`` in include/moe.h."""
+    u8 = torch.uint8
+    xs = block_turned_shape(cfg.rows, cfg.groups, cfg.in_dim)
+    ds = block_turned_shape(cfg.rows, cfg.groups, cfg.out_dim)
+    c = _Call(dw)
+    a = MoEBlockWeightGradArgs(
+        c.ptr(x_t, u8, "x_t", xs), c.ptr(x_scale_t, u8, "x_scale_t", xs[:2]),
+        c.ptr(dy_t, u8, "dy_t", ds), c.ptr(dy_scale_t, u8, "dy_scale_t", ds[:2]),
+        c.ptr(offsets, torch.int32, "offsets", (cfg.groups + 1,)),
+        c.ptr(dw, _TORCH_DTYPE[cfg.dtype], "dw", (cfg.groups, cfg.out_dim, cfg.in_dim)))
+    c.run(lib().moe_block_weight_grad, stream, ctypes.byref(cfg), ctypes.byref(a),
+          c.workspace(workspace), _nbytes(workspace))
+
+
+# ---------------------------------------------------------------- AdamW
+class AdamWTensors:
+    """The list of tensors that moe_adamw_step takes, made once (it keeps the
+    tensors): what a step then costs on the host does not grow with Python's
+    work for each of them."""
+
+    def __init__(self, call, array, dtype, grad_dtype, state_format, keep):
+        self.call, self.array, self.keep = call, array, keep
+        self.dtype, self.grad_dtype, self.state_format = dtype, grad_dtype, state_format
+
+
+def make_adamw_tensors(tensors: Sequence[Dict[str, object]]) -> AdamWTensors:
+    """A list of dicts with ``param`` and ``grad`` (bf16 or fp32), ``m`` and ``v``
+    (fp32; or int8 and uint8 codes with ``m_scale`` and ``v_scale`` [n / 256,
+    rounded up]), and optionally ``master`` (fp32, with bf16 parameters) and
+    ``weight_decay``.  The parameters share one dtype, the gradients one, and the
+    states one format; shapes are free, each tensor contiguous."""
+    if not tensors:
+        raise ValueError("no tensors")
+    first = tensors[0]
+    c = _Call(first["param"])
+    dtype, grad_dtype = (_dtype_code(first[n], n) for n in ("param", "grad"))
+    eight = first["m"].dtype == torch.int8
+    f32 = torch.float32
+    array = (MoEAdamWTensor * len(tensors))()
+    for at, t in zip(array, tensors):
+        n = t["param"].numel()
+        flat = lambda name: None if t.get(name) is None else t[name].view(-1)  # noqa: E731
+        blocks = -(-n // STATE_BLOCK)
+        if eight and n > 0 and (t.get("m_scale") is None or t.get("v_scale") is None):
+            raise ValueError("states in 8 bits need m_scale and v_scale")
+        for name, dt, size in (("param", _TORCH_DTYPE[dtype], n),
+                               ("grad", _TORCH_DTYPE[grad_dtype], n),
+                               ("m", torch.int8 if eight else f32, n),
+                               ("v", torch.uint8 if eight else f32, n), ("master", f32, n),
+                               ("m_scale", f32, blocks), ("v_scale", f32, blocks)):
+            setattr(at, name, c.ptr(flat(name), dt, name, (size,)))
+        at.n, at.weight_decay = n, float(t.get("weight_decay", 0.0))
+    return AdamWTensors(c, array, dtype, grad_dtype,
+                        MOE_STATES_8BIT if eight else MOE_STATES_F32, list(tensors))
+
+
+def moe_adamw_step(tensors: AdamWTensors, *, step: int = 0, lr: float = 1e-3, beta1: float = 0.9,
+                   beta2: float = 0.999, eps: float = 1e-8, grad_scale: float = 1.0,
+                   seed: Optional[int] = None, scalars: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """One AdamW step over every tensor, in place.  ``step`` counts from 1;
+    ``seed`` (for what is rounded at random) is the step where it is not given.
+    ``scalars``: 5 fp32 or int32 words on the device that stand for lr,
+    1 - beta1^step, 1 - beta2^step, grad_scale and the seed's bits; see
+    ``moe_adamw_step`` in include/moe.h."""
+    c = tensors.call
+    if scalars is not None and scalars.dtype not in (torch.float32, torch.int32):
+        raise ValueError("scalars must be float32 or int32 words")
+    cfg = MoEAdamWConfig(float(lr), float(beta1), float(beta2), float(eps), float(grad_scale),
+                         int(step),
+                         None if scalars is None else c.ptr(scalars, scalars.dtype, "scalars", (5,)),
+                         (int(step) if seed is None else int(seed)) & 0xFFFFFFFF, tensors.dtype,
+                         tensors.grad_dtype, tensors.state_format)
+    c.run(lib().moe_adamw_step, stream, ctypes.byref(cfg), len(tensors.array), tensors.array)
 
 
 class MoELayer:

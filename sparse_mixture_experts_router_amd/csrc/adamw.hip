@@ -1,0 +1,354 @@
+// AdamW over many tensors in one launch (up to 48; more take another launch).
+//
+//   g' = g grad_scale        m = b1 m + (1 - b1) g'      v = b2 v + (1 - b2) g'^2
+//   p  = p (1 - lr wd) - lr / bias1 * m / (sqrt(v) / sqrt(bias2) + eps)
+//
+// One pass: a workgroup takes 2048 elements of a tensor, a thread 8 of them.
+// Bound by HBM with fp32 states (30 bytes an element with bf16 parameters and
+// their fp32 copies).
+//
+// States in 8 bits, 256 elements to a pair of scales, in codes that are finest
+// near 0:  m = s c |c| (c in -127 .. 127),  sqrt(v) = s c^2 (c in 0 .. 255).
+// A step moves v by a part in a hundred or less, far under a code's width, so
+// rounding to nearest would never move it: of the two codes around the new
+// value one is drawn, with the odds that make m (and v, not its root) right on
+// average.  The draw is a hash of the seed, the tensor's place and the
+// element's, so a step can be repeated bit for bit.  bf16 parameters without
+// an fp32 copy are rounded the same way.
+//
+// Each operation on the states rounds by itself (contraction is off): a code
+// then does not hang on what the compiler fuses.
+#include "moe.h"
+#include "api_error.h"
+#include "linear.h"
+
+#include <algorithm>
+#include <cmath>
+
+namespace moe {
+namespace {
+
+constexpr int kTensors = 48;  // in one launch: their table is a kernel argument (4 KB at most)
+constexpr int kStateBlock = 256;
+constexpr int kChunk = 2048;
+
+struct Tensor {
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* master;
+  float* m_scale;
+  float* v_scale;
+  long n;
+  float weight_decay;
+  int aligned;  // every pointer allows 16-byte accesses of 8 elements
+};
+struct Step {
+  float lr, bias1, bias2, grad_scale;
+  uint32_t seed;
+};
+struct AdamArgs {
+  Tensor t[kTensors];
+  int first[kTensors + 1];  // chunks before each tensor
+  int count, base;          // tensors; the place of t[0] in the call
+  float b1, b2, omb1, omb2, eps;
+  Step step;
+  const Step* scalars;
+};
+static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments");
+
+// xor-shifts and odd multipliers: every bit of the result hangs on every bit
+// of the word
+__device__ __forceinline__ uint32_t mixed(uint32_t h) {
+  h ^= h >> 16;
+  h *= 0x85EBCA6Bu;
+  h ^= h >> 13;
+  h *= 0xC2B2AE35u;
+  return h ^ (h >> 16);
+}
+
+// |x| as an integer that orders like it, NaN on top.
+__device__ __forceinline__ uint32_t order(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+__device__ __forceinline__ uint32_t max32(uint32_t v) {  // of 32 lanes
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), d, 64)));
+  return v;
+}
+
+// x / s, correctly rounded, for an x of at most 2^16 s: with r = RN(1 / s) the
+// quotient x r is off by a unit at most, and one step with the exact remainder
+// rounds it (Markstein).  Tiny scales, whose reciprocal could overflow, divide.
+struct Divider {
+  float s, r;
+  bool plain;
+  __device__ __forceinline__ explicit Divider(float s_) : s(s_), r(1.0f / s_), plain(!(s_ > 0x1p-96f && s_ < 0x1p96f)) {}
+  __device__ __forceinline__ float operator()(float x) const {
+    if (plain) return s > 0.f ? x / s : 0.f;
+    const float q = x * r;
+    return fmaf(fmaf(-q, s, x), r, q);
+  }
+};
+
+// The integer k with k^2 <= y < (k + 1)^2, y >= 0, as a float.
+__device__ __forceinline__ float int_root(float y) {
+  float k = floorf(__builtin_amdgcn_sqrtf(y));
+  k = k * k > y ? k - 1.0f : k;
+  return (k + 1.0f) * (k + 1.0f) <= y ? k + 1.0f : k;
+}
+
+template <typename T> __device__ __forceinline__ float get1(const T* p);
+template <> __device__ __forceinline__ float get1<bf16_t>(const bf16_t* p) { return bf16_to_f32(*p); }
+template <> __device__ __forceinline__ float get1<float>(const float* p) { return *p; }
+
+// 8 elements at p: `full` with vector accesses, else the first `n` one by one.
+template <typename T>
+__device__ __forceinline__ void get8(const T* p, bool full, int n, float* v) {
+  if (full) {
+    load8<T>(p, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = i < n ? get1<T>(p + i) : 0.f;
+}
+template <typename T>
+__device__ __forceinline__ void put8(T* p, bool full, int n, const float* v) {
+  if (full) {
+    store8<T>(p, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) p[i] = from_f32<T>(v[i]);
+}
+__device__ __forceinline__ uint2 bytes8(const uint8_t* p, bool full, int n) {
+  if (full) return *reinterpret_cast<const uint2*>(p);
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) w[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void put_bytes8(uint8_t* p, bool full, int n, uint2 b) {
+  if (full) {
+    *reinterpret_cast<uint2*>(p) = b;
+    return;
+  }
+  const uint32_t w[2] = {b.x, b.y};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) p[i] = static_cast<uint8_t>(w[i / 4] >> (8 * (i % 4)));
+}
+
+template <typename P, typename G, bool EIGHT>
+__global__ __launch_bounds__(256) void adamw_kernel(AdamArgs a) {
+#pragma clang fp contract(off)
+  const Step st = a.scalars != nullptr ? *a.scalars : a.step;
+  if (st.grad_scale == 0.f) return;
+  const float rate = st.lr / st.bias1, root2 = sqrtf(st.bias2);
+  const int total = a.first[a.count];
+  for (int chunk = blockIdx.x; chunk < total; chunk += gridDim.x) {
+    int lo = 0, hi = a.count - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.first[mid] <= chunk) lo = mid;
+      else hi = mid - 1;
+    }
+    const Tensor& t = a.t[lo];
+    const long at = static_cast<long>(chunk - a.first[lo]) * kChunk + threadIdx.x * 8;
+    const int n = static_cast<int>(min(max(t.n - at, 0L), 8L));
+    const bool full = n == 8 && t.aligned != 0;
+    float g[8], m[8], v[8], p[8], root[8];
+    get8<G>(static_cast<const G*>(t.grad) + at, full, n, g);
+    if (t.master != nullptr) get8<float>(t.master + at, full, n, p);
+    else get8<P>(static_cast<const P*>(t.param) + at, full, n, p);
+    if constexpr (EIGHT) {
+      const uint2 mc = bytes8(static_cast<const uint8_t*>(t.m) + at, full, n);
+      const uint2 vc = bytes8(static_cast<const uint8_t*>(t.v) + at, full, n);
+      const uint32_t mw[2] = {mc.x, mc.y}, vw[2] = {vc.x, vc.y};
+      const float ms = n > 0 ? t.m_scale[at / kStateBlock] : 0.f;
+      const float vs = n > 0 ? t.v_scale[at / kStateBlock] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float q = static_cast<float>(static_cast<int8_t>(mw[i / 4] >> (8 * (i % 4))));
+        m[i] = q * fabsf(q) * ms;
+        const float c = static_cast<float>((vw[i / 4] >> (8 * (i % 4))) & 0xffu);
+        const float r = c * c * vs;
+        v[i] = r * r;
+      }
+    } else {
+      get8<float>(static_cast<const float*>(t.m) + at, full, n, m);
+      get8<float>(static_cast<const float*>(t.v) + at, full, n, v);
+    }
+    const float keep = 1.0f - st.lr * t.weight_decay;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = g[i] * st.grad_scale;
+      m[i] = m[i] * a.b1 + s * a.omb1;
+      v[i] = v[i] * a.b2 + s * s * a.omb2;
+      root[i] = sqrtf(v[i]);
+      p[i] = p[i] * keep - rate * (m[i] / (root[i] / root2 + a.eps));
+    }
+    uint32_t noise[8];
+    if constexpr (EIGHT || sizeof(P) == 2) {
+      const uint32_t salt = mixed(st.seed + static_cast<uint32_t>(a.base + lo) * 0x9E3779B9u);
+      const uint32_t high = mixed(static_cast<uint32_t>(at >> 32) ^ salt);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) noise[i] = mixed((static_cast<uint32_t>(at) + i) ^ high);
+    }
+    if constexpr (EIGHT) {
+      uint32_t tm = 0, tv = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) {
+          tm = max(tm, order(m[i]));
+          tv = max(tv, order(root[i]));
+        }
+      const float ms = __uint_as_float(max32(tm)) / (127.0f * 127.0f);
+      const float vs = __uint_as_float(max32(tv)) / (255.0f * 255.0f);
+      const Divider dm(ms), dv(vs);
+      uint32_t mw[2] = {0u, 0u}, vw[2] = {0u, 0u};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        {
+          const float y = dm(fabsf(m[i]));
+          const float k = fminf(int_root(y), 127.0f);
+          const float u = static_cast<float>(noise[i] & 0xffffu) * 0x1p-16f;
+          const float c = fminf(k + (u * (2.0f * k + 1.0f) < y - k * k ? 1.0f : 0.0f), 127.0f);
+          mw[i / 4] |= (static_cast<uint32_t>(static_cast<int>(copysignf(c, m[i]))) & 0xffu) << (8 * (i % 4));
+        }
+        {
+          const float y = dv(root[i]);
+          const float k = fminf(int_root(y), 255.0f);
+          const float u = static_cast<float>(noise[i] >> 16) * 0x1p-16f;
+          const float k2 = k * k, n2 = (k + 1.0f) * (k + 1.0f);
+          const float low = k2 * k2;
+          const float c = fminf(k + (u * (n2 * n2 - low) < y * y - low ? 1.0f : 0.0f), 255.0f);
+          vw[i / 4] |= static_cast<uint32_t>(c) << (8 * (i % 4));
+        }
+      }
+      put_bytes8(static_cast<uint8_t*>(t.m) + at, full, n, make_uint2(mw[0], mw[1]));
+      put_bytes8(static_cast<uint8_t*>(t.v) + at, full, n, make_uint2(vw[0], vw[1]));
+      if ((threadIdx.x & 31) == 0 && n > 0) {
+        t.m_scale[at / kStateBlock] = ms;
+        t.v_scale[at / kStateBlock] = vs;
+      }
+    } else {
+      put8<float>(static_cast<float*>(t.m) + at, full, n, m);
+      put8<float>(static_cast<float*>(t.v) + at, full, n, v);
+    }
+    if (t.master != nullptr) {
+      put8<float>(t.master + at, full, n, p);
+    } else if constexpr (sizeof(P) == 2) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t b = __float_as_uint(p[i]) + (mixed(noise[i] ^ 0x5BD1E995u) & 0xffffu);
+        if (order(p[i]) < 0x7f800000u) p[i] = __uint_as_float(b & 0xffff0000u);
+      }
+    }
+    put8<P>(static_cast<P*>(t.param) + at, full, n, p);
+  }
+}
+
+moe_status check(const moe_adamw_config* c, int32_t count, const moe_adamw_tensor* t) {
+  if (c == nullptr) return fail(MOE_ERR_INVALID_ARG, "cfg is NULL");
+  if (count < 0 || (count > 0 && t == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "bad count or tensors");
+  if ((c->dtype != MOE_F32 && c->dtype != MOE_BF16) ||
+      (c->grad_dtype != MOE_F32 && c->grad_dtype != MOE_BF16))
+    return fail(MOE_ERR_INVALID_ARG, "bad dtype or grad_dtype");
+  if (c->state_format != MOE_STATES_F32 && c->state_format != MOE_STATES_8BIT)
+    return fail(MOE_ERR_INVALID_ARG, "bad state_format");
+  if (!(c->beta1 >= 0.0 && c->beta1 < 1.0) || !(c->beta2 >= 0.0 && c->beta2 < 1.0) ||
+      !(c->eps >= 0.0) || !std::isfinite(c->lr) || !std::isfinite(c->eps))
+    return fail(MOE_ERR_INVALID_ARG, "beta1, beta2 in [0, 1), eps >= 0 and a finite lr are needed");
+  if (c->scalars == nullptr && c->step < 1) return fail(MOE_ERR_INVALID_ARG, "step counts from 1");
+  if ((reinterpret_cast<uintptr_t>(c->scalars) & 3u) != 0)
+    return fail(MOE_ERR_INVALID_ARG, "scalars not 4-byte aligned");
+  for (int32_t i = 0; i < count; ++i) {
+    if (t[i].n < 0) return fail(MOE_ERR_INVALID_ARG, "a tensor's n is negative");
+    if (t[i].n > (int64_t{1} << 40)) return fail(MOE_ERR_UNSUPPORTED, "a tensor has more than 2^40 elements");
+    if (!std::isfinite(t[i].weight_decay))
+      return fail(MOE_ERR_INVALID_ARG, "a weight_decay is not finite");
+    if (t[i].n == 0) continue;
+    if (t[i].param == nullptr || t[i].grad == nullptr || t[i].m == nullptr || t[i].v == nullptr)
+      return fail(MOE_ERR_INVALID_ARG, "a tensor's param, grad, m or v is NULL");
+    const uintptr_t es = c->dtype == MOE_BF16 ? 2 : 4, gs = c->grad_dtype == MOE_BF16 ? 2 : 4;
+    const uintptr_t ss = c->state_format == MOE_STATES_8BIT ? 1 : 4;
+    auto off = [](const void* p, uintptr_t b) { return reinterpret_cast<uintptr_t>(p) % b != 0; };
+    if (off(t[i].param, es) || off(t[i].grad, gs) || off(t[i].m, ss) || off(t[i].v, ss) ||
+        off(t[i].master, 4) || off(t[i].m_scale, 4) || off(t[i].v_scale, 4))
+      return fail(MOE_ERR_INVALID_ARG, "a tensor's pointer is not aligned to its element");
+    if (t[i].master != nullptr && c->dtype == MOE_F32)
+      return fail(MOE_ERR_INVALID_ARG, "fp32 parameters have no fp32 copy");
+    if ((c->state_format == MOE_STATES_8BIT) !=
+            (t[i].m_scale != nullptr && t[i].v_scale != nullptr) ||
+        (t[i].m_scale == nullptr) != (t[i].v_scale == nullptr))
+      return fail(MOE_ERR_INVALID_ARG, "m_scale and v_scale go with states in 8 bits");
+  }
+  return MOE_OK;
+}
+
+template <typename P, typename G>
+hipError_t launch(const AdamArgs& a, bool eight, hipStream_t s) {
+  const unsigned grid = static_cast<unsigned>(std::min(a.first[a.count], 1 << 20));
+  if (eight) hipLaunchKernelGGL((adamw_kernel<P, G, true>), dim3(grid), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((adamw_kernel<P, G, false>), dim3(grid), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_adamw_step(const moe_adamw_config* cfg, int32_t count,
+                                     const moe_adamw_tensor* tensors, void* stream) {
+  clear_error();
+  const moe_status st = check(cfg, count, tensors);
+  if (st != MOE_OK) return st;
+  AdamArgs a{};
+  a.b1 = static_cast<float>(cfg->beta1);
+  a.b2 = static_cast<float>(cfg->beta2);
+  a.omb1 = static_cast<float>(1.0 - cfg->beta1);
+  a.omb2 = static_cast<float>(1.0 - cfg->beta2);
+  a.eps = static_cast<float>(cfg->eps);
+  const double steps = static_cast<double>(cfg->step);
+  a.step = Step{static_cast<float>(cfg->lr), static_cast<float>(1.0 - std::pow(cfg->beta1, steps)),
+                static_cast<float>(1.0 - std::pow(cfg->beta2, steps)),
+                static_cast<float>(cfg->grad_scale), cfg->seed};
+  a.scalars = static_cast<const Step*>(static_cast<const void*>(cfg->scalars));
+  const bool eight = cfg->state_format == MOE_STATES_8BIT;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  // a launch takes up to kTensors tensors and 2^30 chunks
+  int32_t i = 0;
+  while (i < count) {
+    a.count = 0;
+    a.base = i;
+    long chunks = 0;
+    for (; i < count && a.count < kTensors; ++i) {
+      const moe_adamw_tensor& t = tensors[i];
+      const long mine = (t.n + kChunk - 1) / kChunk;
+      if (a.count > 0 && chunks + mine > (1L << 30)) break;
+      auto off = [](const void* p, uintptr_t b) { return reinterpret_cast<uintptr_t>(p) & (b - 1); };
+      const bool ok = off(t.param, 16) == 0 && off(t.grad, 16) == 0 && off(t.master, 16) == 0 &&
+                      off(t.m, eight ? 8 : 16) == 0 && off(t.v, eight ? 8 : 16) == 0;
+      a.t[a.count] = Tensor{t.param, t.grad, t.m, t.v, t.master, t.m_scale, t.v_scale,
+                            static_cast<long>(t.n), t.weight_decay, ok ? 1 : 0};
+      a.first[a.count++] = static_cast<int>(chunks);
+      chunks += mine;
+    }
+    a.first[a.count] = static_cast<int>(chunks);
+    if (chunks == 0) continue;
+    hipError_t err;
+    if (cfg->dtype == MOE_BF16)
+      err = cfg->grad_dtype == MOE_BF16 ? launch<bf16_t, bf16_t>(a, eight, s)
+                                        : launch<bf16_t, float>(a, eight, s);
+    else
+      err = cfg->grad_dtype == MOE_BF16 ? launch<float, bf16_t>(a, eight, s)
+                                        : launch<float, float>(a, eight, s);
+    if (err != hipSuccess) return hip_fail(err, "AdamW kernel");
+  }
+  return MOE_OK;
+}

@@ -1,0 +1,150 @@
+// Internal declarations of the 8-bit floating point path with a scale for each
+// block of 128: packing rows and weights, the grouped product, its weight
+// gradient.
+//
+// A packed row holds one E4M3 code for each element and one E8M0 byte
+// (2^(byte - 127)) for each block of 128 columns.  The bytes of a block column
+// lie together, one for each row: scale [blocks, scale_line(rows)].  Turned
+// rows (the operands of the weight gradient) are cut into blocks of 128 rows
+// of a group: codes [block, column, 128], bytes [block, column]; group e's
+// first block is offsets[e] / 128 + e, which leaves room for every group's
+// last, partial one whatever the groups are, so no table of blocks is needed.
+#pragma once
+
+#include "linear.h"
+
+namespace moe {
+
+constexpr int kBlk = 128;  // elements that share a scale
+
+typedef __attribute__((ext_vector_type(8))) int i32x8;
+
+// Scales of one block column of `rows` rows.
+inline size_t scale_line(long rows) { return static_cast<size_t>((rows + 15) / 16 * 16); }
+
+struct PackArgs {
+  const void* x;             // [x_rows or rows, cols; forward SwiGLU: 2 cols]
+  const int32_t* row_index;  // source row of x for every row, or null
+  const int32_t* offsets;    // [groups + 1], or null: one group of all rows
+  const void* dy;            // [rows, cols; SwiGLU: cols / 2] or null
+  uint8_t* codes;            // [rows, cols] or null
+  uint8_t* scale;            // [ceil(cols / 128), line]
+  uint8_t* codes_t;          // [rows / 128 + groups, cols, 128] or null
+  uint8_t* scale_t;          // [rows / 128 + groups, cols]
+  size_t line;
+  int rows, x_rows, groups, cols, act;
+};
+hipError_t launch_block_pack(int dtype, const PackArgs& g, hipStream_t s);
+
+struct PackWeightArgs {
+  const void* w;     // [groups, out, in]
+  uint8_t* codes;    // [groups, out, in] or null
+  uint8_t* scale;    // [groups, ceil(out / 128), ceil(in / 128)]
+  uint8_t* codes_t;  // [groups, in, out] or null
+  uint8_t* scale_t;  // [groups, ceil(in / 128), ceil(out / 128)]
+  int groups, out, in;
+};
+hipError_t launch_block_pack_weights(int dtype, const PackWeightArgs& g, hipStream_t s);
+
+struct BlockArgs {
+  const uint8_t* x;        // [rows, in]; weight gradient: turned x
+  const uint8_t* x_scale;  // [ceil(in / 128), line]; turned: [blocks, in]
+  const int32_t* offsets;  // [groups + 1]
+  const uint8_t* w;        // [groups, z, in]; weight gradient: turned dy [blocks, z, 128]
+  const void* w_scale;     // [groups, ceil(z / 128), ceil(in / 128)]; turned: [blocks, z]
+  void* y;                 // [rows, out] or null; weight gradient: dw [groups, z, in]
+  uint8_t* y_codes;        // [rows, out] or null
+  uint8_t* y_scale;        // [ceil(out / 128), line]
+  float* partial;          // [parts, rows, z] (weight gradient [parts, groups, z, in]) or null
+  size_t line;
+  int rows, groups, in_dim, out_dim, z_dim, act, parts;
+  int dtype;               // of y
+  bool wide;               // fp32 results: products on the bf16 instruction
+};
+
+// The product on tiles of 128 x 128 or 64 x 64.  parts > 1 or packed results:
+// sums go to partial, and launch_block_join finishes them.
+int block_tile_parts(const BlockArgs& g, int cus);
+hipError_t launch_block_tile(bool wf32, const BlockArgs& g, int cus, hipStream_t s);
+// y = act(sum of the parts), in y's type and packed.
+hipError_t launch_block_join(const BlockArgs& g, hipStream_t s);
+// The weight gradient on the same tiles.
+int block_dw_parts(const BlockArgs& g, int cus);
+hipError_t launch_block_dw_tile(const BlockArgs& g, int cus, hipStream_t s);
+hipError_t launch_block_dw_join(const BlockArgs& g, hipStream_t s);
+
+// ---------------------------------------------------------------- device helpers
+// Turned block of a group's first rows.
+__device__ __forceinline__ int turned_first(int begin, int e) { return begin / kBlk + e; }
+
+// The smallest power of two, as an E8M0 byte from 1 on, that brings m (finite,
+// >= 0) to 448 = 1.75 2^8 at most; 1 where m is 0.
+__device__ __forceinline__ int e8m0_of(float m) {
+  const uint32_t u = __float_as_uint(m);
+  const int e = static_cast<int>(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(e, 1);
+}
+// 2^(127 - byte), exact for the bytes that e8m0_of gives.
+__device__ __forceinline__ float e8m0_inverse(int byte) {
+  return __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
+}
+__device__ __forceinline__ float e8m0_value(int byte) {
+  return byte != 0 ? __uint_as_float(static_cast<uint32_t>(byte) << 23) : 0x1p-127f;
+}
+
+// Codes 8 t .. 8 t + 7 of a lane's 32, widened to bf16 times a power of two.
+__device__ __forceinline__ u32x4 widen8(const i32x8& c, int t, float scale) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w = static_cast<uint32_t>(c[2 * t + i]);
+    r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false));
+    r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true));
+  }
+  return r;
+}
+
+// The largest finite |v| of 8 values, and whether one is not finite.  NaN and
+// infinities do not count; they become the NaN code.
+__device__ __forceinline__ float finite_max8(const float* v, bool& bad) {
+  float m = 0.f;
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  if (__builtin_expect(top >= 0x7f800000u, 0)) {
+    bad = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (fabsf(v[i]) < INFINITY) m = fmaxf(m, fabsf(v[i]));
+    return m;
+  }
+  return __uint_as_float(top);
+}
+// 8 codes of v * inv; what is not finite becomes NaN.
+__device__ __forceinline__ uint2 encode8_finite(const float* v, float inv, bool bad) {
+  if (__builtin_expect(bad, 0)) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = fabsf(v[i]) < INFINITY ? v[i] : __builtin_nanf("");
+    return encode8(f, inv);
+  }
+  return encode8(v, inv);
+}
+
+// 1 / (1 + e^-z) to about 2^-23: packed values are compared with a border
+// (the next power of two, the next code), so an error here moves bytes.  The
+// exponent's product is carried in two parts and the reciprocal refined once;
+// the hardware's own exponential and reciprocal are good for one unit each.
+__device__ __forceinline__ float sigmoid_close(float z) {
+  const float kL = -1.44269504088896340736f, kLo = -1.925963033500e-8f;
+  const float zc = fminf(fmaxf(z, -87.f), 87.f);  // e^87 is still finite
+  const float t = zc * kL;
+  const float lo = fmaf(zc, kLo, fmaf(zc, kL, -t));
+  const float e0 = __builtin_amdgcn_exp2f(t);
+  const float d = 1.0f + fmaf(e0 * 0.69314718f, lo, e0);
+  const float r = __builtin_amdgcn_rcpf(d);
+  const float p = fmaf(fmaf(-d, r, 1.0f), r, r);
+  return z != z ? z : p;
+}
+
+}  // namespace moe

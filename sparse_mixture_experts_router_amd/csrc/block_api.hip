@@ -1,0 +1,258 @@
+// Host side of the calls in 8-bit floating point with a scale for each block
+// of 128 (include/moe.h): argument checks, workspace layout and launch
+// sequences.  Nothing here allocates, frees or waits on the device.
+#include "moe.h"
+#include "api_error.h"
+#include "block.h"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+long blocks_of(long n) { return (n + kBlk - 1) / kBlk; }
+
+moe_status check_dtype(int dtype) {
+  return dtype == MOE_F32 || dtype == MOE_BF16 ? MOE_OK : fail(MOE_ERR_INVALID_ARG, "bad dtype");
+}
+
+moe_status check_pack(const moe_block_pack_config* c, const moe_block_pack_args* a) {
+  if (c == nullptr || a == nullptr) return fail(MOE_ERR_INVALID_ARG, "cfg or args is NULL");
+  if (c->rows < 0 || c->x_rows < 0 || c->groups <= 0 || c->cols <= 0)
+    return fail(MOE_ERR_INVALID_ARG, "sizes must be positive (rows, x_rows >= 0)");
+  if (check_dtype(c->dtype) != MOE_OK) return MOE_ERR_INVALID_ARG;
+  if (c->activation < MOE_ACT_NONE || c->activation > MOE_ACT_SWIGLU)
+    return fail(MOE_ERR_INVALID_ARG, "bad activation");
+  if (c->groups > kMaxExperts) return fail(MOE_ERR_UNSUPPORTED, "groups > 512");
+  if (c->cols % 64 != 0) return fail(MOE_ERR_UNSUPPORTED, "cols must be a multiple of 64");
+  if (c->cols > (1 << 21)) return fail(MOE_ERR_UNSUPPORTED, "cols > 2^21");
+  if (c->rows >= (1 << 27) || c->x_rows >= (1 << 30))
+    return fail(MOE_ERR_UNSUPPORTED, "too many rows");
+  // workgroups of 256 threads, fewer than 2^24 of them: 128 rows by 128 columns
+  // each, or 16 rows of one block column or more
+  if ((c->rows / kBlk + c->groups) * blocks_of(c->cols) > (1L << 23))
+    return fail(MOE_ERR_UNSUPPORTED, "too many blocks");
+  if (a->dy != nullptr) {
+    if (c->activation == MOE_ACT_NONE)
+      return fail(MOE_ERR_INVALID_ARG, "dy needs an activation (its gradient is packed)");
+    if (c->activation == MOE_ACT_SWIGLU && c->cols % 128 != 0)
+      return fail(MOE_ERR_UNSUPPORTED, "the gradient of SwiGLU needs cols a multiple of 128");
+  }
+  if (a->offsets == nullptr && c->groups != 1)
+    return fail(MOE_ERR_INVALID_ARG, "offsets is NULL with more than one group");
+  if (c->rows == 0) return MOE_OK;
+  if (a->x == nullptr) return fail(MOE_ERR_INVALID_ARG, "x is NULL");
+  if ((c->x_rows > 0) != (a->row_index != nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "row_index and x_rows go together");
+  if (a->codes == nullptr && a->codes_t == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "codes and codes_t are both NULL");
+  if ((a->codes != nullptr) != (a->scale != nullptr) ||
+      (a->codes_t != nullptr) != (a->scale_t != nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "codes and their scales go together");
+  if (!aligned(a->x, 16) || !aligned(a->dy, 16) || !aligned(a->codes, 16) ||
+      !aligned(a->codes_t, 16) || !aligned(a->row_index, 4) || !aligned(a->offsets, 4))
+    return fail(MOE_ERR_INVALID_ARG, "x, dy, codes or codes_t not 16-byte aligned");
+  return MOE_OK;
+}
+
+int z_dim(const moe_block_linear_config& c) {
+  return c.activation == MOE_ACT_SWIGLU ? 2 * c.out_dim : c.out_dim;
+}
+
+moe_status check_linear(const moe_block_linear_config* c, bool grad) {
+  if (c == nullptr) return fail(MOE_ERR_INVALID_ARG, "cfg is NULL");
+  if (c->rows < 0 || c->groups <= 0 || c->in_dim <= 0 || c->out_dim <= 0)
+    return fail(MOE_ERR_INVALID_ARG, "sizes must be positive (rows >= 0)");
+  if (check_dtype(c->dtype) != MOE_OK) return MOE_ERR_INVALID_ARG;
+  if (c->activation != MOE_ACT_NONE && c->activation != MOE_ACT_SWIGLU)
+    return fail(MOE_ERR_INVALID_ARG, "activation must be none or SwiGLU");
+  if (c->w_scale_format != MOE_SCALE_F32 && c->w_scale_format != MOE_SCALE_E8M0)
+    return fail(MOE_ERR_INVALID_ARG, "bad w_scale_format");
+  if (grad && c->activation != MOE_ACT_NONE)
+    return fail(MOE_ERR_INVALID_ARG, "the weight gradient has no activation");
+  if (c->groups > kMaxExperts) return fail(MOE_ERR_UNSUPPORTED, "groups > 512");
+  if (c->in_dim % 64 != 0 || c->out_dim % 64 != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "in_dim and out_dim must be multiples of 64");
+  if (c->in_dim > (1 << 20) || c->out_dim > (1 << 20))
+    return fail(MOE_ERR_UNSUPPORTED, "in_dim or out_dim > 2^20");
+  if (c->rows >= (1 << 27)) return fail(MOE_ERR_UNSUPPORTED, "too many rows");
+  // grids of 256 threads a tile stay below 2^32 threads
+  const long wide = std::max(c->in_dim, z_dim(*c));
+  if ((c->rows / 128 + c->groups) * (wide / 64) > (1L << 23))
+    return fail(MOE_ERR_UNSUPPORTED, "too many tiles");
+  if (static_cast<long>(c->groups) * z_dim(*c) * c->in_dim > (grad ? 1L << 36 : 1L << 39))
+    return fail(MOE_ERR_UNSUPPORTED, "too many weights");
+  return MOE_OK;
+}
+
+BlockArgs block_args(const moe_block_linear_config& c) {
+  BlockArgs g{};
+  g.rows = c.rows;
+  g.groups = c.groups;
+  g.in_dim = c.in_dim;
+  g.out_dim = c.out_dim;
+  g.z_dim = z_dim(c);
+  g.act = c.activation;
+  g.dtype = c.dtype;
+  g.line = scale_line(c.rows);
+  g.parts = 1;
+  return g;
+}
+
+moe_status check_space(const void* ws, size_t have, size_t need) {
+  if (ws == nullptr) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+  if (!aligned(ws, kAlign)) return fail(MOE_ERR_WORKSPACE, "workspace not 256-byte aligned");
+  if (have < need) return fail(MOE_ERR_WORKSPACE, "workspace smaller than its size function says");
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_block_pack(const moe_block_pack_config* cfg, const moe_block_pack_args* a,
+                          void* stream) {
+  clear_error();
+  const moe_status st = check_pack(cfg, a);
+  if (st != MOE_OK) return st;
+  if (cfg->rows == 0) return MOE_OK;
+  PackArgs g{};
+  g.x = a->x;
+  g.row_index = a->row_index;
+  g.offsets = a->offsets;
+  g.dy = a->dy;
+  g.codes = a->codes;
+  g.scale = a->scale;
+  g.codes_t = a->codes_t;
+  g.scale_t = a->scale_t;
+  g.line = scale_line(cfg->rows);
+  g.rows = cfg->rows;
+  g.x_rows = cfg->x_rows;
+  g.groups = cfg->groups;
+  g.cols = cfg->cols;
+  g.act = cfg->activation;
+  const hipError_t err = launch_block_pack(cfg->dtype, g, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? MOE_OK : hip_fail(err, "packing kernel");
+}
+
+moe_status moe_block_pack_weights(int32_t groups, int32_t out_dim, int32_t in_dim, int32_t dtype,
+                                  const void* w, uint8_t* codes, uint8_t* scale, uint8_t* codes_t,
+                                  uint8_t* scale_t, void* stream) {
+  clear_error();
+  if (groups <= 0 || out_dim <= 0 || in_dim <= 0)
+    return fail(MOE_ERR_INVALID_ARG, "sizes must be positive");
+  if (check_dtype(dtype) != MOE_OK) return MOE_ERR_INVALID_ARG;
+  if (out_dim % 64 != 0 || in_dim % 64 != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "out_dim and in_dim must be multiples of 64");
+  if (out_dim > (1 << 21) || in_dim > (1 << 21))
+    return fail(MOE_ERR_UNSUPPORTED, "out_dim or in_dim > 2^21");
+  if (blocks_of(out_dim) * blocks_of(in_dim) > (1L << 23) / groups)
+    return fail(MOE_ERR_UNSUPPORTED, "too many blocks");
+  if (w == nullptr) return fail(MOE_ERR_INVALID_ARG, "w is NULL");
+  if (codes == nullptr && codes_t == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "codes and codes_t are both NULL");
+  if ((codes != nullptr) != (scale != nullptr) || (codes_t != nullptr) != (scale_t != nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "codes and their scales go together");
+  if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(codes_t, 16))
+    return fail(MOE_ERR_INVALID_ARG, "w, codes or codes_t not 16-byte aligned");
+  const PackWeightArgs g{w, codes, scale, codes_t, scale_t, groups, out_dim, in_dim};
+  const hipError_t err = launch_block_pack_weights(dtype, g, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? MOE_OK : hip_fail(err, "weight packing kernel");
+}
+
+size_t moe_block_linear_workspace_size(const moe_block_linear_config* cfg) {
+  if (check_linear(cfg, false) != MOE_OK) return 0;
+  const BlockArgs g = block_args(*cfg);
+  const size_t parts = block_tile_parts(g, device_cus());
+  return std::max(kAlign, align_up(parts * g.rows * g.z_dim * 4));
+}
+
+moe_status moe_block_linear(const moe_block_linear_config* cfg, const moe_block_linear_args* a,
+                            void* workspace, size_t ws_bytes, void* stream) {
+  clear_error();
+  moe_status st = check_linear(cfg, false);
+  if (st != MOE_OK) return st;
+  if (a == nullptr) return fail(MOE_ERR_INVALID_ARG, "args is NULL");
+  if (a->offsets == nullptr) return fail(MOE_ERR_INVALID_ARG, "offsets is NULL");
+  if (cfg->rows == 0) return MOE_OK;
+  if (a->x == nullptr || a->x_scale == nullptr || a->w == nullptr || a->w_scale == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "x, w or a scale is NULL");
+  if (a->y == nullptr && a->y_codes == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "y and y_codes are both NULL");
+  if ((a->y_codes != nullptr) != (a->y_scale != nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "y_codes and y_scale go together");
+  if (!aligned(a->x, 16) || !aligned(a->w, 16) || !aligned(a->y, 16) || !aligned(a->y_codes, 16))
+    return fail(MOE_ERR_INVALID_ARG, "x, w, y or y_codes not 16-byte aligned");
+  if (!aligned(a->offsets, 4) || (cfg->w_scale_format == MOE_SCALE_F32 && !aligned(a->w_scale, 4)))
+    return fail(MOE_ERR_INVALID_ARG, "offsets or w_scale not 4-byte aligned");
+  if ((st = check_space(workspace, ws_bytes, moe_block_linear_workspace_size(cfg))) != MOE_OK)
+    return st;
+  BlockArgs g = block_args(*cfg);
+  g.x = a->x;
+  g.x_scale = a->x_scale;
+  g.offsets = a->offsets;
+  g.w = a->w;
+  g.w_scale = a->w_scale;
+  g.y = a->y;
+  g.y_codes = a->y_codes;
+  g.y_scale = a->y_scale;
+  g.wide = a->y != nullptr && cfg->dtype == MOE_F32;
+  const bool wf32 = cfg->w_scale_format == MOE_SCALE_F32;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int cus = device_cus();
+  g.parts = block_tile_parts(g, cus);
+  if (g.parts > 1 || g.y_codes != nullptr) g.partial = static_cast<float*>(workspace);
+  hipError_t err = launch_block_tile(wf32, g, cus, s);
+  if (err == hipSuccess && g.partial != nullptr) err = launch_block_join(g, s);
+  return err == hipSuccess ? MOE_OK : hip_fail(err, "block product kernel");
+}
+
+size_t moe_block_weight_grad_workspace_size(const moe_block_linear_config* cfg) {
+  if (check_linear(cfg, true) != MOE_OK) return 0;
+  const BlockArgs g = block_args(*cfg);
+  const size_t parts = block_dw_parts(g, device_cus());
+  return parts > 1 ? align_up(parts * g.groups * g.z_dim * g.in_dim * 4) : kAlign;
+}
+
+moe_status moe_block_weight_grad(const moe_block_linear_config* cfg,
+                                 const moe_block_weight_grad_args* a, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+  clear_error();
+  moe_status st = check_linear(cfg, true);
+  if (st != MOE_OK) return st;
+  if (a == nullptr) return fail(MOE_ERR_INVALID_ARG, "args is NULL");
+  if (a->offsets == nullptr || a->dw == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "offsets or dw is NULL");
+  if (cfg->rows > 0 && (a->x_t == nullptr || a->x_scale_t == nullptr || a->dy_t == nullptr ||
+                        a->dy_scale_t == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "x_t, dy_t or a scale is NULL");
+  if (!aligned(a->x_t, 16) || !aligned(a->dy_t, 16) || !aligned(a->dw, 16))
+    return fail(MOE_ERR_INVALID_ARG, "x_t, dy_t or dw not 16-byte aligned");
+  if (!aligned(a->x_scale_t, 4) || !aligned(a->dy_scale_t, 4) || !aligned(a->offsets, 4))
+    return fail(MOE_ERR_INVALID_ARG, "offsets or a scale not 4-byte aligned");
+  if ((st = check_space(workspace, ws_bytes, moe_block_weight_grad_workspace_size(cfg))) != MOE_OK)
+    return st;
+  BlockArgs g = block_args(*cfg);
+  g.x = a->x_t;
+  g.x_scale = a->x_scale_t;
+  g.offsets = a->offsets;
+  g.w = a->dy_t;
+  g.w_scale = a->dy_scale_t;
+  g.y = a->dw;
+  g.wide = cfg->dtype == MOE_F32;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int cus = device_cus();
+  g.parts = block_dw_parts(g, cus);
+  if (g.parts > 1) g.partial = static_cast<float*>(workspace);
+  hipError_t err = launch_block_dw_tile(g, cus, s);
+  if (err == hipSuccess && g.parts > 1) err = launch_block_dw_join(g, s);
+  return err == hipSuccess ? MOE_OK : hip_fail(err, "weight gradient kernel");
+}
+
+}  // extern "C"

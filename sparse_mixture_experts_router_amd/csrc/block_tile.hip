@@ -1,0 +1,494 @@
+// The product in 8-bit floating point with a scale for each block of 128, on
+// tiles of 128 x 128 or 64 x 64, and its weight gradient.
+//
+//   z[r, n]  = sum_b 2^xs[b, r] ws[e, n / 128, b]  sum_{k in block b} x[r, k] w[e, n, k]
+//   dW[n, k] = sum_b 2^(ds[b, n] + xs[b, k])  sum_{r in block b} dz[r, n] x[r, k]
+//
+// One v_mfma_scale_f32_16x16x128_f8f6f4 covers a whole block, so the scales
+// that are powers of two go into the instruction and cost nothing; weights
+// with fp32 scales (WF32) leave an unscaled sum of each block, which one fma
+// an element adds up.
+//
+// The instruction aligns each 8 products to the largest of them and drops what
+// lies under 2^-13 of it, before it adds in fp32: results are off by 1.4e-5 of
+// their norm, a hundredth of a rounding to bf16 and a thousandth of one to
+// E4M3.  fp32 results are worth more (WIDE): codes are widened to bf16, which
+// holds them and their power of two exactly, and multiplied by the bf16
+// instruction at half the rate.
+//
+// Four wavefronts, two by two; a stage is one block of 128 bytes of each row,
+// loaded straight into LDS (16-byte chunks XOR-swizzled by row).  The staged
+// rows of the second operand are ordered so that a lane of the result holds NB
+// neighbouring columns: results are stored without a pass through LDS, and the
+// scales of a lane's columns in the weight gradient are one load.
+#include "block.h"
+#include "lds_ring.h"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+constexpr int kFwd = 0, kDw = 1;
+
+// What a stage reads past the end of a row (the last 64 of a block of 128).
+__device__ __align__(16) const uint32_t zero_chunk[4] = {0u, 0u, 0u, 0u};
+
+template <int BT> struct Ring { static constexpr int kDepth = BT == 128 ? 2 : 3; };
+
+template <int BT, int MODE, bool GATED, bool WF32, bool WIDE>
+__global__ __launch_bounds__(256) void block_tile_kernel(BlockArgs g) {
+  static_assert(MODE == kFwd || (!GATED && !WF32), "weight gradient: plain");
+  constexpr int WT = BT / 2, NBK = WT / 16;       // a wavefront's rows (columns), 16-row blocks
+  constexpr int NBO = GATED ? NBK / 2 : NBK;      // result columns of a lane
+  constexpr int COLS = GATED ? BT / 2 : BT;
+  constexpr int D = Ring<BT>::kDepth, kStage = 2 * BT * kLineBytes;
+  constexpr int LD = BT / 32;                     // a wavefront's loads of an operand's stage
+  __shared__ __attribute__((aligned(1024))) char smem[D * kStage];
+
+  // ------------------------------------------------------- work of this block
+  const int n_dim = MODE == kFwd ? g.out_dim : g.in_dim;
+  const int nt = (n_dim + COLS - 1) / COLS;
+  int e, m0, n0, valid, seg, nst;
+  if constexpr (MODE == kFwd) {
+    TileAt at;
+    int col;
+    if (!find_item(g.offsets, g.groups, g.rows, BT, nt, at, col)) return;
+    e = __builtin_amdgcn_readfirstlane(at.e);
+    m0 = __builtin_amdgcn_readfirstlane(at.m) * BT;
+    n0 = __builtin_amdgcn_readfirstlane(col) * COLS;
+    seg = __builtin_amdgcn_readfirstlane(at.begin);
+    valid = min(BT, __builtin_amdgcn_readfirstlane(at.end) - seg - m0);
+    nst = (g.in_dim + kBlk - 1) / kBlk;
+  } else {
+    const int mt = (g.z_dim + BT - 1) / BT;
+    const int per = mt * nt;
+    e = blockIdx.x / per;
+    const int q = blockIdx.x - e * per;
+    m0 = q % mt * BT;
+    n0 = q / mt * COLS;
+    valid = min(BT, g.z_dim - m0);
+    const int2 r = group_range(g.offsets, e, g.rows);
+    seg = __builtin_amdgcn_readfirstlane(turned_first(r.x, e));
+    nst = __builtin_amdgcn_readfirstlane((r.y - r.x + kBlk - 1) / kBlk);
+  }
+  const int part = blockIdx.y;
+  const int s0 = static_cast<int>(static_cast<long>(nst) * part / g.parts);
+  const int s1 = static_cast<int>(static_cast<long>(nst) * (part + 1) / g.parts);
+
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave >> 1, wc = wave & 1;
+
+  // --------------------------------------------------- this lane's sources
+  // Loads j of a wavefront stage 8 rows each: the row lane / 8, the chunk that
+  // the swizzle puts at the lane's place.
+  const int chunk = line_lane_chunk(lane, 0);
+  uint32_t aoff[LD], boff[LD];
+  const char *abase, *bbase;
+  size_t astep, bstep, bup = 0;
+  if constexpr (MODE == kFwd) {
+    const uint32_t row_bytes = static_cast<uint32_t>(g.in_dim);
+    abase = reinterpret_cast<const char*>(g.x) + static_cast<size_t>(seg + m0) * row_bytes;
+    bbase = reinterpret_cast<const char*>(g.w) +
+            (static_cast<size_t>(e) * g.z_dim + n0) * row_bytes;
+    bup = static_cast<size_t>(g.out_dim) * row_bytes;
+    astep = bstep = kLineBytes;
+#pragma unroll
+    for (int j = 0; j < LD; ++j) {
+      const int ar = min(wave * (BT / 4) + j * 8 + (lane >> 3), valid - 1);
+      aoff[j] = static_cast<uint32_t>(ar) * row_bytes + chunk * 16;
+    }
+  } else {
+    abase = reinterpret_cast<const char*>(g.w) + (static_cast<size_t>(seg) * g.z_dim + m0) * kBlk;
+    bbase = reinterpret_cast<const char*>(g.x) + (static_cast<size_t>(seg) * g.in_dim + n0) * kBlk;
+    astep = static_cast<size_t>(g.z_dim) * kBlk;
+    bstep = static_cast<size_t>(g.in_dim) * kBlk;
+#pragma unroll
+    for (int j = 0; j < LD; ++j) {
+      const int ar = min(wave * (BT / 4) + j * 8 + (lane >> 3), valid - 1);
+      aoff[j] = static_cast<uint32_t>(ar) * kBlk + chunk * 16;
+    }
+  }
+  // staged row of the second operand -> its column: block jb of the wavefront
+  // column c, row l holds the column NBO l + jb
+  auto col_of = [&](int p) {
+    const int c = p / WT, jb = (p % WT) / 16 % NBO, l = p % 16;
+    return c * (GATED ? WT / 2 : WT) + NBO * l + jb;
+  };
+#pragma unroll
+  for (int j = 0; j < LD; ++j) {
+    const int p = wave * (BT / 4) + j * 8 + (lane >> 3);
+    const int c = min(col_of(p), n_dim - 1 - n0);
+    boff[j] = static_cast<uint32_t>(c) * (MODE == kFwd ? static_cast<uint32_t>(g.in_dim) : kBlk) +
+              chunk * 16;
+  }
+  const bool half_last = MODE == kFwd && (g.in_dim & 64) != 0;
+  // past the last stage the last one again, into a buffer that nobody reads
+  // any more: the count of loads in flight stays the same
+  auto issue = [&](int at) {
+    char* const buf = smem + (at - s0) % D * kStage;
+    const int p = min(at, s1 - 1);
+    const char* const a = abase + p * astep;
+    const char* const b = bbase + p * bstep;
+    const bool cut = half_last && p == nst - 1 && chunk >= 4;
+#pragma unroll
+    for (int j = 0; j < LD; ++j) {
+      const int p0 = wave * (BT / 4) + j * 8;  // first staged row: a multiple of 8, one block of 16
+      const char* const bj = GATED && (p0 % WT) / 16 >= NBO ? b + bup : b;
+      load_lds16(cut ? reinterpret_cast<const char*>(zero_chunk) : a + aoff[j], buf + p0 * kLineBytes);
+      load_lds16(cut ? reinterpret_cast<const char*>(zero_chunk) : bj + boff[j],
+                 buf + (BT + p0) * kLineBytes);
+    }
+  };
+
+  // ------------------------------------------------------------------ scales
+  // a: one byte a block of rows; b: the wavefront's columns share one (the
+  // gate's and the up projection's apart), or in the weight gradient NBO bytes
+  // of neighbouring columns.
+  const uint8_t* asp[NBK];
+  const uint8_t* bsp[2] = {nullptr, nullptr};
+  const float* bsf[2] = {nullptr, nullptr};
+  const int wcol = n0 + wc * (GATED ? WT / 2 : WT);  // the wavefront's first column
+#pragma unroll
+  for (int i = 0; i < NBK; ++i) {
+    const int r = min(wr * WT + i * 16 + l16, valid - 1);
+    asp[i] = MODE == kFwd ? g.x_scale + seg + m0 + r
+                          : static_cast<const uint8_t*>(g.w_scale) +
+                                static_cast<size_t>(seg) * g.z_dim + m0 + r;
+  }
+  const size_t asstep = MODE == kFwd ? g.line : static_cast<size_t>(g.z_dim);
+  if constexpr (MODE == kFwd) {
+    const int ob = (g.z_dim + kBlk - 1) / kBlk;
+#pragma unroll
+    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+      const int zc = min(wcol, g.out_dim - 1) + h * g.out_dim;
+      const size_t at = (static_cast<size_t>(e) * ob + zc / kBlk) * nst;
+      if (WF32) bsf[h] = static_cast<const float*>(g.w_scale) + at;
+      else bsp[h] = static_cast<const uint8_t*>(g.w_scale) + at;
+    }
+  } else {
+    bsp[0] = g.x_scale + static_cast<size_t>(seg) * g.in_dim + min(wcol, g.in_dim - WT) + NBO * l16;
+  }
+  struct Scales {
+    int a[NBK];
+    uint32_t b[2];
+    float f[2];
+  };
+  auto load_scales = [&](int p, Scales& s) {
+#pragma unroll
+    for (int i = 0; i < NBK; ++i) s.a[i] = asp[i][p * asstep];
+    if constexpr (MODE == kDw) {
+      const uint8_t* const q = bsp[0] + static_cast<size_t>(p) * g.in_dim;
+      s.b[0] = NBO == 4 ? *reinterpret_cast<const uint32_t*>(q)
+                        : *reinterpret_cast<const uint16_t*>(q);
+    } else {
+#pragma unroll
+      for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+        if constexpr (WF32) s.f[h] = bsf[h][p];
+        else s.b[h] = bsp[h][p];
+      }
+    }
+  };
+
+  auto scale_b = [&](const Scales& s, int j) -> int {
+    if (MODE == kDw) return static_cast<int>(s.b[0] >> (8 * j)) & 0xff;
+    return static_cast<int>(s.b[GATED && j >= NBO ? 1 : 0]);
+  };
+
+  f32x4 acc[NBK][NBK];
+#pragma unroll
+  for (int i = 0; i < NBK; ++i)
+#pragma unroll
+    for (int j = 0; j < NBK; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // --------------------------------------------------------------- main loop
+  // Stage p + D - 1 is asked for once everybody is done with p - 1, whose
+  // buffer it takes.  Before stage p is read, at most the loads of the D - 2
+  // stages after it may be in flight (the scales' loads only make this wait
+  // longer).
+  const int key = swz128_key(l16);
+  const int fl0 = l16 * kLineBytes + (((lane >> 4) ^ key) << 4);
+  const int fl1 = l16 * kLineBytes + (((4 + (lane >> 4)) ^ key) << 4);
+  Scales cur{}, next{};
+  if (s0 < s1) {
+    load_scales(s0, cur);
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int p = 0; p < D - 1; ++p) issue(s0 + p);
+  }
+  for (int p = s0; p < s1; ++p) {
+    wait_vmem<(D - 2) * 2 * LD>();
+    stage_barrier();
+    load_scales(min(p + 1, s1 - 1), next);
+    asm volatile("" ::: "memory");
+    issue(p + D - 1);
+    const char* const buf = smem + (p - s0) % D * kStage;
+    i32x8 a[NBK], b[NBK];
+    auto frag = [&](const char* at) {
+      const u32x4 lo = *reinterpret_cast<const u32x4*>(at + fl0);
+      const u32x4 hi = *reinterpret_cast<const u32x4*>(at + fl1);
+      return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]),
+                   static_cast<int>(lo[3]), static_cast<int>(hi[0]), static_cast<int>(hi[1]),
+                   static_cast<int>(hi[2]), static_cast<int>(hi[3])};
+    };
+#pragma unroll
+    for (int i = 0; i < NBK; ++i) a[i] = frag(buf + (wr * WT + i * 16) * kLineBytes);
+#pragma unroll
+    for (int j = 0; j < NBK; ++j) b[j] = frag(buf + (BT + wc * WT + j * 16) * kLineBytes);
+    if constexpr (WIDE) {
+      f32x4 d[NBK][NBK];
+      if constexpr (WF32) {
+#pragma unroll
+        for (int i = 0; i < NBK; ++i)
+#pragma unroll
+          for (int j = 0; j < NBK; ++j) d[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        u32x4 wa[NBK], wb[NBK];
+#pragma unroll
+        for (int i = 0; i < NBK; ++i) wa[i] = widen8(a[i], t, e8m0_value(cur.a[i]));
+#pragma unroll
+        for (int j = 0; j < NBK; ++j)
+          wb[j] = widen8(b[j], t, WF32 ? 1.0f : e8m0_value(scale_b(cur, j)));
+#pragma unroll
+        for (int j = 0; j < NBK; ++j)
+#pragma unroll
+          for (int i = 0; i < NBK; ++i) {
+            if constexpr (WF32) d[i][j] = Mfma<bf16_t>::step(wa[i], wb[j], d[i][j]);
+            else acc[i][j] = Mfma<bf16_t>::step(wa[i], wb[j], acc[i][j]);
+          }
+      }
+      if constexpr (WF32) {
+#pragma unroll
+        for (int i = 0; i < NBK; ++i)
+#pragma unroll
+          for (int j = 0; j < NBK; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[i][j][r] = fmaf(d[i][j][r], cur.f[GATED && j >= NBO ? 1 : 0], acc[i][j][r]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NBK; ++j)
+#pragma unroll
+        for (int i = 0; i < NBK; ++i) {
+          if constexpr (WF32) {
+            const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+            const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                a[i], b[j], z, 0, 0, 0, cur.a[i], 0, 127);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[i][j][r] = fmaf(d[r], cur.f[GATED && j >= NBO ? 1 : 0], acc[i][j][r]);
+          } else {
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                a[i], b[j], acc[i][j], 0, 0, 0, cur.a[i], 0, scale_b(cur, j));
+          }
+        }
+    }
+    cur = next;
+  }
+  wait_vmem<0>();  // the loads past the last stage
+  // The matrix instructions work for all lanes together, but the compiler takes
+  // them for ordinary ones and could move the last into a branch of the
+  // epilogue, where some lanes' operands are not written.
+#pragma unroll
+  for (int i = 0; i < NBK; ++i)
+#pragma unroll
+    for (int j = 0; j < NBK; ++j) asm volatile("" : "+v"(acc[i][j]));
+
+  // -------------------------------------------------------------- epilogue
+  const int c = wcol + NBO * l16;
+#pragma unroll
+  for (int i = 0; i < NBK; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = wr * WT + i * 16 + 4 * (lane >> 4) + r;
+      if (row >= valid || c >= n_dim) continue;
+      float v[NBO], u[NBO];
+#pragma unroll
+      for (int j = 0; j < NBO; ++j) {
+        v[j] = acc[i][j][r];
+        u[j] = GATED ? acc[i][NBK - NBO + j][r] : 0.f;
+      }
+      auto put = [&](float* o, const float* w) {
+        if constexpr (NBO == 4) *reinterpret_cast<float4*>(o) = make_float4(w[0], w[1], w[2], w[3]);
+        else if constexpr (NBO == 2) *reinterpret_cast<float2*>(o) = make_float2(w[0], w[1]);
+        else *o = w[0];
+      };
+      if (g.partial != nullptr) {
+        const size_t at = MODE == kFwd
+            ? (static_cast<size_t>(part) * g.rows + seg + m0 + row) * g.z_dim + c
+            : ((static_cast<size_t>(part) * g.groups + e) * g.z_dim + m0 + row) * g.in_dim + c;
+        put(g.partial + at, v);
+        if (GATED) put(g.partial + at + g.out_dim, u);
+        continue;
+      }
+      if (GATED) {
+#pragma unroll
+        for (int j = 0; j < NBO; ++j) v[j] = v[j] * sigmoid_close(v[j]) * u[j];
+      }
+      const size_t at = MODE == kFwd
+          ? static_cast<size_t>(seg + m0 + row) * g.out_dim + c
+          : (static_cast<size_t>(e) * g.z_dim + m0 + row) * g.in_dim + c;
+      if (g.dtype == 1) {
+        bf16_t* const o = static_cast<bf16_t*>(g.y) + at;
+        uint32_t w[(NBO + 1) / 2];
+#pragma unroll
+        for (int j = 0; j < NBO; j += 2)
+          w[j / 2] = static_cast<uint32_t>(f32_to_bf16(v[j])) |
+                     (j + 1 < NBO ? static_cast<uint32_t>(f32_to_bf16(v[j + 1])) << 16 : 0u);
+        if constexpr (NBO == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+        else if constexpr (NBO == 2) *reinterpret_cast<uint32_t*>(o) = w[0];
+        else *o = static_cast<bf16_t>(w[0]);
+      } else {
+        put(static_cast<float*>(g.y) + at, v);
+      }
+    }
+}
+
+// y = act(sum of parts) for 16 rows, 16 lanes to 128 columns; packed as
+// block_pack.hip packs rows.
+__global__ __launch_bounds__(256) void block_join_kernel(BlockArgs g) {
+  const int tid = threadIdx.x, l16 = tid & 15;
+  const int row = blockIdx.x * 16 + (tid >> 4);
+  const int first = min(max(g.offsets[0], 0), g.rows);
+  const int last = min(max(g.offsets[g.groups], 0), g.rows);
+  const bool live = row >= first && row < last;
+  const int b = blockIdx.y, c = b * kBlk + l16 * 8;
+  const bool in = live && c < g.out_dim;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (in) {
+    const bool gated = g.act == kActSwiglu;
+    float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < g.parts; ++p) {
+      const float* const q = g.partial + (static_cast<size_t>(p) * g.rows + row) * g.z_dim + c;
+      float w[8];
+      load8<float>(q, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += w[i];
+      if (gated) {
+        load8<float>(q + g.out_dim, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] += w[i];
+      }
+    }
+    if (gated) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = v[i] * sigmoid_close(v[i]) * u[i];
+    }
+    if (g.y != nullptr) {
+      const size_t at = static_cast<size_t>(row) * g.out_dim + c;
+      if (g.dtype == 1) store8<bf16_t>(static_cast<bf16_t*>(g.y) + at, v);
+      else store8<float>(static_cast<float*>(g.y) + at, v);
+    }
+  }
+  if (g.y_codes == nullptr) return;
+  bool bad = false;
+  float m = finite_max8(v, bad);
+  m = fmaxf(m, __shfl_xor(m, 1, 64));
+  m = fmaxf(m, __shfl_xor(m, 2, 64));
+  m = fmaxf(m, __shfl_xor(m, 4, 64));
+  m = fmaxf(m, __shfl_xor(m, 8, 64));
+  const int s = e8m0_of(m);
+  if (in)
+    *reinterpret_cast<uint2*>(g.y_codes + static_cast<size_t>(row) * g.out_dim + c) =
+        encode8_finite(v, e8m0_inverse(s), bad);
+  if (live && l16 == 0) g.y_scale[b * g.line + row] = static_cast<uint8_t>(s);
+}
+
+__global__ __launch_bounds__(256) void block_dw_join_kernel(BlockArgs g, size_t n8) {
+  for (size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; i < n8;
+       i += static_cast<size_t>(gridDim.x) * 256) {
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < g.parts; ++p) {
+      float w[8];
+      load8<float>(g.partial + (static_cast<size_t>(p) * n8 + i) * 8, w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += w[k];
+    }
+    if (g.dtype == 1) store8<bf16_t>(static_cast<bf16_t*>(g.y) + i * 8, v);
+    else store8<float>(static_cast<float*>(g.y) + i * 8, v);
+  }
+}
+
+// Tiles of bt rows that the rows of all groups can need.
+long row_tiles(const BlockArgs& g, int bt) {
+  return g.rows / bt + std::min<long>(g.groups, g.rows);
+}
+bool small_tiles(const BlockArgs& g, int cus) {
+  return row_tiles(g, 128) * ((g.z_dim + 127) / 128) < cus;
+}
+
+template <int BT, bool GATED, bool WF32, bool WIDE>
+hipError_t launch_fwd_t(const BlockArgs& g, hipStream_t s) {
+  constexpr int COLS = GATED ? BT / 2 : BT;
+  const long blocks = item_grid(g.rows, g.groups, BT, (g.out_dim + COLS - 1) / COLS);
+  hipLaunchKernelGGL((block_tile_kernel<BT, kFwd, GATED, WF32, WIDE>),
+                     dim3(static_cast<unsigned>(blocks), g.parts), dim3(256), 0, s, g);
+  return hipGetLastError();
+}
+template <int BT, bool GATED, bool WF32>
+hipError_t launch_fwd(const BlockArgs& g, hipStream_t s) {
+  return g.wide ? launch_fwd_t<BT, GATED, WF32, true>(g, s)
+                : launch_fwd_t<BT, GATED, WF32, false>(g, s);
+}
+template <int BT>
+hipError_t launch_fwd_bt(bool wf32, const BlockArgs& g, hipStream_t s) {
+  if (g.act == kActSwiglu)
+    return wf32 ? launch_fwd<BT, true, true>(g, s) : launch_fwd<BT, true, false>(g, s);
+  return wf32 ? launch_fwd<BT, false, true>(g, s) : launch_fwd<BT, false, false>(g, s);
+}
+
+}  // namespace
+
+int block_tile_parts(const BlockArgs& g, int cus) {
+  const long tiles = row_tiles(g, 64) * ((g.z_dim + 63) / 64);
+  const int nst = (g.in_dim + kBlk - 1) / kBlk;
+  if (!small_tiles(g, cus) || tiles >= cus) return 1;
+  return static_cast<int>(std::max<long>(1, std::min<long>({cus / tiles, nst / 4, 16})));
+}
+
+hipError_t launch_block_tile(bool wf32, const BlockArgs& g, int cus, hipStream_t s) {
+  return small_tiles(g, cus) ? launch_fwd_bt<64>(wf32, g, s) : launch_fwd_bt<128>(wf32, g, s);
+}
+
+hipError_t launch_block_join(const BlockArgs& g, hipStream_t s) {
+  hipLaunchKernelGGL(block_join_kernel, dim3((g.rows + 15) / 16, (g.out_dim + kBlk - 1) / kBlk),
+                     dim3(256), 0, s, g);
+  return hipGetLastError();
+}
+
+int block_dw_parts(const BlockArgs& g, int cus) {
+  const long tiles = static_cast<long>(g.groups) * ((g.z_dim + 63) / 64) * ((g.in_dim + 63) / 64);
+  const long blocks = g.rows / kBlk / g.groups;  // of a group, on average
+  if (tiles >= cus) return 1;
+  return static_cast<int>(std::max<long>(1, std::min<long>({cus / tiles, blocks / 4, 16})));
+}
+
+hipError_t launch_block_dw_tile(const BlockArgs& g, int cus, hipStream_t s) {
+  auto tiles = [&](int bt) {
+    return static_cast<long>(g.groups) * ((g.z_dim + bt - 1) / bt) * ((g.in_dim + bt - 1) / bt);
+  };
+  auto go = [&](auto kernel, int bt) {
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tiles(bt)), g.parts), dim3(256), 0, s, g);
+  };
+  if (tiles(128) < cus) {
+    if (g.wide) go(block_tile_kernel<64, kDw, false, false, true>, 64);
+    else go(block_tile_kernel<64, kDw, false, false, false>, 64);
+  } else {
+    if (g.wide) go(block_tile_kernel<128, kDw, false, false, true>, 128);
+    else go(block_tile_kernel<128, kDw, false, false, false>, 128);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_block_dw_join(const BlockArgs& g, hipStream_t s) {
+  const size_t n8 = static_cast<size_t>(g.groups) * g.z_dim * g.in_dim / 8;
+  const size_t blocks = std::min<size_t>((n8 + 255) / 256, 4096);
+  hipLaunchKernelGGL(block_dw_join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, g, n8);
+  return hipGetLastError();
+}
+
+}  // namespace moe

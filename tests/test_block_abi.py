@@ -1,0 +1,253 @@
+"""The calls in 8-bit floating point with a scale for each block of 128, and
+the AdamW step, without a GPU: their structs mirror the header, sizes are
+answered, and bad arguments are refused on the host before anything is
+launched."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import sparse_mixture_experts_router_amd as moe
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "moe.h")
+
+pytestmark = pytest.mark.skipif(not os.path.exists(moe.LIB_PATH),
+                                reason="libmoe.so not built (run __graft_entry__.build())")
+
+FAKE = 1 << 20  # a 256-byte aligned non-null address; never dereferenced on these paths
+BIG = 1 << 50
+OK, INVALID, UNSUPPORTED, WORKSPACE = (moe.MOE_OK, moe.MOE_ERR_INVALID_ARG,
+                                       moe.MOE_ERR_UNSUPPORTED, moe.MOE_ERR_WORKSPACE)
+NAN = float("nan")
+
+
+def _header():
+    with open(HEADER) as fh:
+        return re.sub(r"/\*.*?\*/", "", fh.read(), flags=re.S)
+
+
+@pytest.mark.parametrize("name,struct", [
+    ("moe_block_pack_config", moe.MoEBlockPackConfig), ("moe_block_pack_args", moe.MoEBlockPackArgs),
+    ("moe_block_linear_config", moe.MoEBlockLinearConfig),
+    ("moe_block_linear_args", moe.MoEBlockLinearArgs),
+    ("moe_block_weight_grad_args", moe.MoEBlockWeightGradArgs),
+    ("moe_adamw_config", moe.MoEAdamWConfig), ("moe_adamw_tensor", moe.MoEAdamWTensor)])
+def test_structs_match_the_header(name, struct):
+    body = re.search(r"typedef struct \{([^}]*)\} " + name + ";", _header()).group(1)
+    fields = re.findall(r"([\w ]+?[ *]+)(\w+);", body)
+    assert [f for _, f in fields] == [f for f, _ in struct._fields_]
+    c = {"int32_t": ctypes.c_int32, "uint32_t": ctypes.c_uint32, "int64_t": ctypes.c_int64,
+         "double": ctypes.c_double, "float": ctypes.c_float}
+    for (t, f), (_, have) in zip(fields, struct._fields_):
+        assert have is (ctypes.c_void_p if "*" in t else c[t.strip()]), f
+
+
+def test_codes_match_the_header():
+    codes = dict(re.findall(r"(MOE_(?:SCALE|STATES)_\w+) = (\d+)", _header()))
+    assert {k: int(v) for k, v in codes.items()} == {
+        k: getattr(moe, k) for k in ("MOE_SCALE_F32", "MOE_SCALE_E8M0", "MOE_STATES_F32", "MOE_STATES_8BIT")}
+    assert [moe.block_scale_shape(r, 320)[1] for r in (0, 1, 16, 17)] == [0, 16, 16, 32]
+    assert moe.block_turned_shape(300, 4, 64) == (6, 64, 128)
+
+
+# ---------------------------------------------------------------- packing rows
+def pack(args=None, **over):
+    c = moe.MoEBlockPackConfig(100, 0, 4, 192, moe.MOE_BF16, 0)
+    for k, v in over.items():
+        setattr(c, k, v)
+    a = dict(x=FAKE, offsets=FAKE, codes=FAKE, scale=FAKE, codes_t=FAKE, scale_t=FAKE)
+    a.update(args or {})
+    a = moe.MoEBlockPackArgs(**a)
+    return moe.lib().moe_block_pack(ctypes.byref(c), ctypes.byref(a), None)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(rows=-1), INVALID), (dict(x_rows=-1), INVALID), (dict(groups=0), INVALID),
+    (dict(cols=0), INVALID), (dict(cols=-64), INVALID), (dict(dtype=2), INVALID),
+    (dict(activation=5), INVALID), (dict(activation=-1), INVALID), (dict(groups=513), UNSUPPORTED),
+    (dict(cols=100), UNSUPPORTED), (dict(cols=(1 << 21) + 64), UNSUPPORTED),
+    (dict(rows=1 << 27), UNSUPPORTED), (dict(x_rows=1 << 30), UNSUPPORTED),
+    (dict(rows=(1 << 27) - 1, cols=2048), UNSUPPORTED), (dict(x_rows=5), INVALID)], ids=str)
+def test_pack_configurations(over, status):
+    assert pack(**over) == status and moe.lib().moe_last_error()
+
+
+@pytest.mark.parametrize("args,over,status", [
+    (dict(x=None), {}, INVALID), (dict(x=FAKE + 8), {}, INVALID), (dict(codes=FAKE + 8), {}, INVALID),
+    (dict(codes_t=FAKE + 4), {}, INVALID), (dict(dy=FAKE + 2), dict(activation=1), INVALID),
+    (dict(scale=None), {}, INVALID), (dict(scale_t=None), {}, INVALID), (dict(codes=None), {}, INVALID),
+    (dict(codes=None, scale=None, codes_t=None, scale_t=None), {}, INVALID),
+    (dict(offsets=None), {}, INVALID), (dict(row_index=FAKE), {}, INVALID),
+    (dict(dy=FAKE), {}, INVALID), (dict(dy=FAKE), dict(activation=4), UNSUPPORTED),
+    (dict(row_index=FAKE + 2), dict(x_rows=9), INVALID), (dict(offsets=FAKE + 2), {}, INVALID),
+    (dict(x=None, codes=None, codes_t=None, scale=None, scale_t=None), dict(rows=0), OK)], ids=str)
+def test_pack_arguments(args, over, status):
+    assert pack(args, **over) == status
+
+
+def test_pack_null():
+    assert moe.lib().moe_block_pack(None, None, None) == INVALID
+
+
+# ---------------------------------------------------------------- packing weights
+@pytest.mark.parametrize("args,status", [
+    ((0, 64, 64, 1, FAKE, FAKE, FAKE, FAKE, FAKE), INVALID),
+    ((2, -64, 64, 1, FAKE, FAKE, FAKE, FAKE, FAKE), INVALID),
+    ((2, 64, 64, 2, FAKE, FAKE, FAKE, FAKE, FAKE), INVALID),
+    ((2, 96, 64, 1, FAKE, FAKE, FAKE, FAKE, FAKE), UNSUPPORTED),
+    ((2, 64, 100, 1, FAKE, FAKE, FAKE, FAKE, FAKE), UNSUPPORTED),
+    ((2, 64, 1 << 22, 1, FAKE, FAKE, FAKE, FAKE, FAKE), UNSUPPORTED),
+    ((1 << 20, 1024, 1024, 1, FAKE, FAKE, FAKE, FAKE, FAKE), UNSUPPORTED),
+    ((2, 64, 64, 1, None, FAKE, FAKE, FAKE, FAKE), INVALID),
+    ((2, 64, 64, 1, FAKE, None, None, None, None), INVALID),
+    ((2, 64, 64, 1, FAKE, FAKE, None, FAKE, FAKE), INVALID),
+    ((2, 64, 64, 1, FAKE, FAKE, FAKE, FAKE, None), INVALID),
+    ((2, 64, 64, 1, FAKE + 8, FAKE, FAKE, FAKE, FAKE), INVALID),
+    ((2, 64, 64, 1, FAKE, FAKE + 4, FAKE, FAKE, FAKE), INVALID)], ids=str)
+def test_pack_weights(args, status):
+    assert moe.lib().moe_block_pack_weights(*args, None) == status and moe.lib().moe_last_error()
+
+
+# ---------------------------------------------------------------- product and weight gradient
+def cfg(**over):
+    c = moe.make_block_linear_config(100, 4, 128, 192)
+    for k, v in over.items():
+        setattr(c, k, v)
+    return c
+
+
+def linear(c, ws=FAKE, nbytes=BIG, **over):
+    a = dict(x=FAKE, x_scale=FAKE, offsets=FAKE, w=FAKE, w_scale=FAKE, y=FAKE)
+    a.update(over)
+    return moe.lib().moe_block_linear(None if c is None else ctypes.byref(c),
+                                      ctypes.byref(moe.MoEBlockLinearArgs(**a)), ws, nbytes, None)
+
+
+def grad(c, ws=FAKE, nbytes=BIG, **over):
+    a = dict(x_t=FAKE, x_scale_t=FAKE, dy_t=FAKE, dy_scale_t=FAKE, offsets=FAKE, dw=FAKE)
+    a.update(over)
+    return moe.lib().moe_block_weight_grad(None if c is None else ctypes.byref(c),
+                                           ctypes.byref(moe.MoEBlockWeightGradArgs(**a)), ws, nbytes,
+                                           None)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(rows=-1), INVALID), (dict(groups=0), INVALID), (dict(in_dim=0), INVALID),
+    (dict(out_dim=-64), INVALID), (dict(dtype=2), INVALID), (dict(activation=1), INVALID),
+    (dict(activation=5), INVALID), (dict(w_scale_format=2), INVALID), (dict(groups=513), UNSUPPORTED),
+    (dict(in_dim=96), UNSUPPORTED), (dict(out_dim=100), UNSUPPORTED),
+    (dict(in_dim=(1 << 20) + 64), UNSUPPORTED), (dict(out_dim=1 << 21), UNSUPPORTED),
+    (dict(rows=1 << 27), UNSUPPORTED), (dict(rows=(1 << 27) - 1, out_dim=1 << 20), UNSUPPORTED),
+    (dict(groups=512, in_dim=1 << 20, out_dim=1 << 20), UNSUPPORTED)], ids=str)
+def test_bad_configurations(over, status):
+    c = cfg(**over)
+    assert linear(c) == status and moe.lib().moe_last_error()
+    assert grad(c) == status
+    assert moe.moe_block_linear_workspace_size(c) == 0
+    assert moe.moe_block_weight_grad_workspace_size(c) == 0
+    with pytest.raises(moe.MoEError):
+        moe.alloc_block_linear_workspace(c, "cpu")
+
+
+def test_weights_of_a_gradient():
+    c = cfg(groups=256, in_dim=1 << 14, out_dim=1 << 15)  # 2^37: a product, but no gradient
+    assert moe.moe_block_linear_workspace_size(c) > 0 and moe.moe_block_weight_grad_workspace_size(c) == 0
+    assert grad(c) == UNSUPPORTED
+    assert grad(cfg(activation=4)) == INVALID and linear(None) == INVALID and grad(None) == INVALID
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(x=None), INVALID), (dict(x_scale=None), INVALID), (dict(offsets=None), INVALID),
+    (dict(w=None), INVALID), (dict(w_scale=None), INVALID), (dict(y=None), INVALID),
+    (dict(y=FAKE + 8), INVALID), (dict(x=FAKE + 4), INVALID), (dict(w=FAKE + 8), INVALID),
+    (dict(y_codes=FAKE), INVALID), (dict(y_scale=FAKE), INVALID),
+    (dict(y_codes=FAKE + 8, y_scale=FAKE), INVALID), (dict(offsets=FAKE + 2), INVALID),
+    (dict(ws=None), WORKSPACE), (dict(ws=FAKE + 64), WORKSPACE), (dict(nbytes=0), WORKSPACE)], ids=str)
+def test_linear_arguments(over, status):
+    assert linear(cfg(), **over) == status and moe.lib().moe_last_error()
+
+
+def test_linear_scales_of_weights_and_no_rows():
+    assert linear(cfg(w_scale_format=moe.MOE_SCALE_F32), w_scale=FAKE + 2) == INVALID
+    assert linear(cfg(rows=0), x=None, x_scale=None, y=None) == OK
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(x_t=None), INVALID), (dict(x_scale_t=None), INVALID), (dict(dy_t=None), INVALID),
+    (dict(dy_scale_t=None), INVALID), (dict(offsets=None), INVALID), (dict(dw=None), INVALID),
+    (dict(x_t=FAKE + 8), INVALID), (dict(dw=FAKE + 8), INVALID), (dict(dy_t=FAKE + 4), INVALID),
+    (dict(x_scale_t=FAKE + 2), INVALID), (dict(dy_scale_t=FAKE + 1), INVALID),
+    (dict(ws=None), WORKSPACE), (dict(ws=FAKE + 64), WORKSPACE), (dict(nbytes=0), WORKSPACE)], ids=str)
+def test_weight_grad_arguments(over, status):
+    assert grad(cfg(), **over) == status and moe.lib().moe_last_error()
+
+
+def test_make_block_linear_config():
+    with pytest.raises(ValueError):
+        moe.make_block_linear_config(1, 1, 64, 64, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        moe.make_block_linear_config(1, 1, 64, 64, w_scale_format="bf16")
+    with pytest.raises(ValueError):
+        moe.make_block_linear_config(1 << 32, 1, 64, 64)
+    with pytest.raises(ValueError):
+        moe.make_block_linear_config(1, 1, 64, 64, activation="tanh")
+
+
+@pytest.mark.parametrize("call", [
+    lambda t: moe.moe_block_pack(t, t.byte(), t.byte()),
+    lambda t: moe.moe_block_pack_weights(t[None], t.byte(), t.byte()),
+    lambda t: moe.make_adamw_tensors([dict(param=t, grad=t, m=t, v=t)])])
+def test_host_tensors_are_refused(call):
+    with pytest.raises(ValueError, match="device tensor"):
+        call(torch.zeros(64, 64))
+    with pytest.raises(ValueError):
+        moe.make_adamw_tensors([])
+
+
+# ---------------------------------------------------------------- AdamW
+def adamw(tensors=None, count=None, **over):
+    c = moe.MoEAdamWConfig(1e-3, 0.9, 0.999, 1e-8, 1.0, 1, None, 0, moe.MOE_BF16, moe.MOE_BF16, 0)
+    for k, v in over.items():
+        setattr(c, k, v)
+    base = dict(param=FAKE, grad=FAKE, m=FAKE, v=FAKE, n=10)
+    tensors = [dict(base, **t) for t in tensors or [{}]]
+    arr = (moe.MoEAdamWTensor * len(tensors))(*[moe.MoEAdamWTensor(**t) for t in tensors])
+    return moe.lib().moe_adamw_step(ctypes.byref(c), len(arr) if count is None else count, arr, None)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(beta1=1.0), INVALID), (dict(beta1=-0.1), INVALID), (dict(beta2=1.0), INVALID),
+    (dict(beta2=NAN), INVALID), (dict(eps=-1e-8), INVALID), (dict(eps=NAN), INVALID),
+    (dict(lr=NAN), INVALID), (dict(lr=float("inf")), INVALID), (dict(step=0), INVALID),
+    (dict(step=-3), INVALID), (dict(dtype=2), INVALID), (dict(grad_dtype=-1), INVALID),
+    (dict(state_format=2), INVALID), (dict(scalars=FAKE + 2), INVALID), (dict(count=-1), INVALID)], ids=str)
+def test_adamw_configurations(over, status):
+    assert adamw(**over) == status and moe.lib().moe_last_error()
+
+
+S8 = dict(m_scale=FAKE, v_scale=FAKE)
+
+
+@pytest.mark.parametrize("tensor,over,status", [
+    (dict(n=-1), {}, INVALID), (dict(n=(1 << 40) + 1), {}, UNSUPPORTED), (dict(param=None), {}, INVALID),
+    (dict(grad=None), {}, INVALID), (dict(m=None), {}, INVALID), (dict(v=None), {}, INVALID),
+    (S8, {}, INVALID), ({}, dict(state_format=1), INVALID), (dict(m_scale=FAKE), dict(state_format=1), INVALID),
+    (dict(m_scale=FAKE), {}, INVALID), (dict(v_scale=FAKE), {}, INVALID),
+    (dict(master=FAKE), dict(dtype=0), INVALID), (dict(weight_decay=NAN), {}, INVALID),
+    (dict(param=FAKE + 1), {}, INVALID), (dict(grad=FAKE + 2), dict(grad_dtype=0), INVALID),
+    (dict(m=FAKE + 2), {}, INVALID), (dict(master=FAKE + 2), {}, INVALID),
+    (dict(S8, v_scale=FAKE + 1), dict(state_format=1), INVALID),
+    (dict(n=0, param=None, grad=None, m=None, v=None), {}, OK)], ids=str)
+def test_adamw_tensors(tensor, over, status):
+    # a bad tensor is found wherever it stands, before anything is launched
+    assert adamw([tensor], **over) == status
+    if status != OK:
+        assert adamw([dict(n=0)] * 60 + [tensor], **over) == status
+
+
+def test_adamw_nothing():
+    assert adamw(count=0) == OK
+    assert moe.lib().moe_adamw_step(None, 0, None, None) == INVALID
