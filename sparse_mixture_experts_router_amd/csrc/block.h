@@ -73,6 +73,10 @@ int block_dw_parts(const BlockArgs& g, int cus);
 hipError_t launch_block_dw_tile(const BlockArgs& g, int cus, hipStream_t s);
 hipError_t launch_block_dw_join(const BlockArgs& g, hipStream_t s);
 
+// Both on 256 x 256 tiles: results in bf16 or packed (not wide), unsplit.
+hipError_t launch_block_mfma(bool wf32, const BlockArgs& g, hipStream_t s);
+hipError_t launch_block_dw_mfma(const BlockArgs& g, hipStream_t s);
+
 // ---------------------------------------------------------------- device helpers
 // Turned block of a group's first rows.
 __device__ __forceinline__ int turned_first(int begin, int e) { return begin / kBlk + e; }

@@ -102,6 +102,19 @@ BlockArgs block_args(const moe_block_linear_config& c) {
   return g;
 }
 
+// Whether a product has enough 256 x 256 tiles for the large-tile kernel.
+bool large_tiles(long row_tiles, int cols) {
+  return row_tiles * ((cols + 255) / 256) > device_cus() / 4;
+}
+bool forward_large(const BlockArgs& g) {
+  const long tiles = g.rows / 256 + std::min(g.groups, g.rows), nt = (g.z_dim + 255) / 256;
+  const long cus = device_cus();
+  return !g.wide && large_tiles(tiles, g.z_dim) && (g.rows * nt / 256 > cus / 4 || tiles * nt > cus);
+}
+bool grad_large(const BlockArgs& g) {
+  return !g.wide && large_tiles(static_cast<long>(g.groups) * ((g.z_dim + 255) / 256), g.in_dim);
+}
+
 moe_status check_space(const void* ws, size_t have, size_t need) {
   if (ws == nullptr) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
   if (!aligned(ws, kAlign)) return fail(MOE_ERR_WORKSPACE, "workspace not 256-byte aligned");
@@ -168,7 +181,9 @@ moe_status moe_block_pack_weights(int32_t groups, int32_t out_dim, int32_t in_di
 
 size_t moe_block_linear_workspace_size(const moe_block_linear_config* cfg) {
   if (check_linear(cfg, false) != MOE_OK) return 0;
-  const BlockArgs g = block_args(*cfg);
+  BlockArgs g = block_args(*cfg);
+  g.wide = cfg->dtype == MOE_F32;
+  if (forward_large(g)) return kAlign;
   const size_t parts = block_tile_parts(g, device_cus());
   return std::max(kAlign, align_up(parts * g.rows * g.z_dim * 4));
 }
@@ -206,6 +221,10 @@ moe_status moe_block_linear(const moe_block_linear_config* cfg, const moe_block_
   const bool wf32 = cfg->w_scale_format == MOE_SCALE_F32;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int cus = device_cus();
+  if (forward_large(g)) {
+    const hipError_t err = launch_block_mfma(wf32, g, s);
+    return err == hipSuccess ? MOE_OK : hip_fail(err, "block product kernel");
+  }
   g.parts = block_tile_parts(g, cus);
   if (g.parts > 1 || g.y_codes != nullptr) g.partial = static_cast<float*>(workspace);
   hipError_t err = launch_block_tile(wf32, g, cus, s);
@@ -215,7 +234,9 @@ moe_status moe_block_linear(const moe_block_linear_config* cfg, const moe_block_
 
 size_t moe_block_weight_grad_workspace_size(const moe_block_linear_config* cfg) {
   if (check_linear(cfg, true) != MOE_OK) return 0;
-  const BlockArgs g = block_args(*cfg);
+  BlockArgs g = block_args(*cfg);
+  g.wide = cfg->dtype == MOE_F32;
+  if (grad_large(g)) return kAlign;
   const size_t parts = block_dw_parts(g, device_cus());
   return parts > 1 ? align_up(parts * g.groups * g.z_dim * g.in_dim * 4) : kAlign;
 }
@@ -248,6 +269,10 @@ moe_status moe_block_weight_grad(const moe_block_linear_config* cfg,
   g.wide = cfg->dtype == MOE_F32;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int cus = device_cus();
+  if (grad_large(g)) {
+    const hipError_t err = launch_block_dw_mfma(g, s);
+    return err == hipSuccess ? MOE_OK : hip_fail(err, "weight gradient kernel");
+  }
   g.parts = block_dw_parts(g, cus);
   if (g.parts > 1) g.partial = static_cast<float*>(workspace);
   hipError_t err = launch_block_dw_tile(g, cus, s);

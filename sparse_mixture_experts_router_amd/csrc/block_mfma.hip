@@ -1,0 +1,566 @@
+// The product in 8-bit floating point with a scale for each block of 128, and
+// its weight gradient, on 256 x 256 tiles: the shapes with many rows a group.
+// Same products as block_tile.hip, for results in bf16 or packed.
+//
+// Bound by the matrix cores and by L2 -> LDS bytes: a tile does 256 operations
+// for each byte that it stages.  One workgroup of 8 wavefronts, two on each
+// SIMD, owns a tile and the whole LDS; a wavefront accumulates a quarter of the
+// rows and half of the columns.  A stage is 128 bytes of K, one block of the
+// scales: 32 v_mfma_scale_f32_16x16x128_f8f6f4 a wavefront.  The wavefronts of a
+// SIMD take turns: while one runs the MFMAs of a stage from registers, the other
+// issues its loads (global -> LDS, no registers) and reads its 12 fragments of
+// the next stage; a barrier ends every phase.  Wavefronts 0-3 load the first
+// operand one stage ahead (2 buffers), wavefronts 4-7 the second one two stages
+// ahead (3 buffers, for W comes from HBM while the rows of x are mostly in L2).
+//
+// Scales that are powers of two go into the instruction: one register holds the
+// bytes of a lane's four row blocks, picked by op_sel.  Rows of a staged operand
+// are ordered so that what a lane holds for neighbouring blocks are neighbouring
+// columns (weight gradient: rows, too): a lane's scales come in one load, and
+// results go out in whole lines without a pass through LDS.
+//
+// Weights with fp32 scales (WF32): an unscaled sum of each block is multiplied
+// in by one fma an element, which needs the accumulators in VGPRs.  To leave
+// room for all this, half of the second operand's fragments are read while the
+// first half is multiplied.
+#include "block.h"
+#include "lds_ring.h"
+
+#include <algorithm>
+#include <utility>
+
+namespace moe {
+namespace {
+
+constexpr int kFwd = 0, kDw = 1;
+constexpr int kT = 256;                 // rows and (effective) columns of a tile
+constexpr int kBuf = kT * kLineBytes;   // bytes of a staged operand
+constexpr int kABufs = 2, kBBufs = 3;
+constexpr int kLds = (kABufs + kBBufs) * kBuf;  // 160 KB
+constexpr int kMB = 4, kNB = 8;         // a wavefront's 16-row and 16-column blocks
+
+template <int N> struct CInt { static constexpr int value = N; };
+template <class F, int... I>
+__device__ __forceinline__ void unroll_(F&& f, std::integer_sequence<int, I...>) {
+  (f(CInt<I>{}), ...);
+}
+template <int N, class F> __device__ __forceinline__ void unroll(F&& f) {
+  unroll_(f, std::make_integer_sequence<int, N>{});
+}
+
+// The scaled MFMA with the accumulator pinned to AGPRs (as mfma_bf16_agpr);
+// SA, SB: which byte of sa and sb scales the operands.
+template <int SA, int SB>
+__device__ __forceinline__ void mfma_f8_agpr(f32x4& c, const i32x8& a, const i32x8& b, int sa, int sb) {
+  asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%6,0] op_sel_hi:[%7,%8,0]"
+               : "+a"(c)
+               : "v"(a), "v"(b), "v"(sa), "v"(sb), "n"(SA & 1), "n"(SB & 1), "n"(SA >> 1), "n"(SB >> 1));
+}
+
+// HALF: the last block of a row has 64 elements.  Its other half reads the
+// first again, and is zeroed on its way into the registers.
+template <int MODE, bool GATED, bool WF32, bool HALF>
+__global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
+  static_assert(MODE == kFwd || (!GATED && !WF32 && !HALF), "weight gradient: plain");
+  constexpr int COLS = GATED ? kT / 2 : kT;
+  __shared__ __attribute__((aligned(1024))) char smem[kLds];
+  auto abuf = [&](int i) -> char* { return smem + i * kBuf; };
+  auto bbuf = [&](int i) -> char* { return smem + (kABufs + i) * kBuf; };
+
+  // ------------------------------------------------------- work of this block
+  const int n_dim = MODE == kFwd ? g.out_dim : g.in_dim;
+  const int nt = (n_dim + COLS - 1) / COLS;
+  int e, m0, n0, valid, seg, count, nst;
+  if constexpr (MODE == kDw) {
+    // Tiles of a group in bands of 4 row tiles, column by column, and the
+    // list dealt to the XCDs in chunks of 16 (4 x 4 tiles): a chunk fetches
+    // 4 + 4 operand tiles into one L2 for its 16 tiles, and a group with many
+    // rows spreads over all XCDs.
+    constexpr int BAND = 4, CHUNK = 16;
+    const int mt = (g.z_dim + kT - 1) / kT;
+    const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
+    const long per = static_cast<long>(mt) * nt;
+    const long w = (static_cast<long>(idx / CHUNK) * 8 + xcd) * CHUNK + idx % CHUNK;
+    if (w >= per * g.groups) return;
+    e = static_cast<int>(w / per);
+    const int q = static_cast<int>(w - e * per);
+    const int band = q / (BAND * nt), h = min(BAND, mt - band * BAND), r = q - band * BAND * nt;
+    m0 = (band * BAND + r % h) * kT;
+    n0 = r / h * COLS;
+    const int2 range = group_range(g.offsets, e, g.rows);
+    seg = __builtin_amdgcn_readfirstlane(turned_first(range.x, e));
+    count = 0;
+    nst = __builtin_amdgcn_readfirstlane((range.y - range.x + kBlk - 1) / kBlk);
+    valid = min(kT, g.z_dim - m0);
+  } else {
+    TileAt at;
+    int col;
+    if (!find_item(g.offsets, g.groups, g.rows, kT, nt, at, col)) return;
+    e = __builtin_amdgcn_readfirstlane(at.e);
+    m0 = __builtin_amdgcn_readfirstlane(at.m) * kT;
+    n0 = __builtin_amdgcn_readfirstlane(col) * COLS;
+    seg = __builtin_amdgcn_readfirstlane(at.begin);
+    count = __builtin_amdgcn_readfirstlane(at.end) - seg;
+    valid = min(kT, count - m0);
+    nst = (g.in_dim + kBlk - 1) / kBlk;
+  }
+
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // Wavefront (grp, q): the row blocks q, q + 4, q + 8, q + 12 of the tile, so
+  // that the four share the rows of a partly filled one (`mlive` live blocks);
+  // in the weight gradient the rows 64 q .. + 63, block i holding 4 l + i.
+  const int grp = wave >> 2, q = wave & 3;
+  const int mlive = __builtin_amdgcn_readfirstlane(
+      MODE == kDw ? (q * 64 < valid ? kMB : 0) : min(max((valid - q * 16 + 63) / 64, 0), kMB));
+
+  // --------------------------------------------------- this lane's sources
+  // Load j of wavefront q stages 8 rows of LDS, 64 q + 8 j ..: lane l the chunk
+  // of row l / 8 that the swizzle puts at its place.  Staged row 16 k + l of a
+  // chunk of 64 columns is column 4 l + k.  The source is off0 + j-th step,
+  // clamped to the last row there is: what rows and columns past the end give
+  // is not written.
+  const int chunk = line_lane_chunk(lane, 0) * 16, l8 = lane >> 3;
+  const char* base;
+  size_t step;
+  uint32_t off0, top, s8, s16;  // offset of load 0, the largest, steps of loads 1 and 2
+  {
+    const uint32_t row_bytes = MODE == kDw ? kBlk : static_cast<uint32_t>(g.in_dim);
+    int first, last;
+    if (grp == 0) {
+      if constexpr (MODE == kDw) {
+        base = reinterpret_cast<const char*>(g.w) +
+               (static_cast<size_t>(seg) * g.z_dim + m0) * kBlk;
+        step = static_cast<size_t>(g.z_dim) * kBlk;
+        first = 4 * l8 + q;                     // row 64 k + 4 l + i at LDS row 64 i + 16 k + l
+        s8 = 32 * row_bytes;
+        s16 = 64 * row_bytes;
+      } else {
+        base = reinterpret_cast<const char*>(g.x) + static_cast<size_t>(seg + m0) * row_bytes;
+        step = kLineBytes;
+        first = 64 * q + l8;
+        s8 = 8 * row_bytes;
+        s16 = 16 * row_bytes;
+      }
+      last = valid - 1;
+    } else {
+      s8 = 32 * row_bytes;
+      s16 = row_bytes;
+      if constexpr (MODE == kDw) {
+        base = reinterpret_cast<const char*>(g.x) +
+               (static_cast<size_t>(seg) * g.in_dim + n0) * kBlk;
+        step = static_cast<size_t>(g.in_dim) * kBlk;
+        first = 64 * q + 4 * l8;
+        last = n_dim - 1 - n0;
+      } else {
+        // SwiGLU: staged rows 0 .. 127 are gate rows, 128 .. 255 the up rows of
+        // the same columns
+        const bool up = GATED && q >= 2;
+        base = reinterpret_cast<const char*>(g.w) +
+               (static_cast<size_t>(e) * g.z_dim + n0 + (up ? g.out_dim : 0)) * row_bytes;
+        step = kLineBytes;
+        first = 64 * q - (up ? COLS : 0) + 4 * l8;
+        last = n_dim - 1 - n0;
+      }
+    }
+    off0 = static_cast<uint32_t>(first) * row_bytes + chunk;
+    top = static_cast<uint32_t>(last) * row_bytes + chunk;
+    const uint64_t b = reinterpret_cast<uint64_t>(base);  // the same in every lane
+    const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(b)));
+    const uint64_t hi =
+        static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(b >> 32)));
+    base = reinterpret_cast<const char*>(lo | (hi << 32));
+  }
+  // The loads of stage p into `ring`; past the end the last one again, into a
+  // buffer that nobody reads any more.  nt_: with the non-temporal policy.
+  auto issue = [&](int p, char* ring, auto nt_) {
+    const int pc = min(p, nst - 1);
+    const char* const src = base + pc * step;
+    char* const dst = ring + q * 8192;
+    // opaque, so that the offsets are made here and the loads take the scalar
+    // base and 32 bits; hoisted, each would hold a register through the loop
+    uint32_t o0 = off0;
+    asm volatile("" : "+v"(o0));
+    uint32_t most = top;
+    if (HALF && pc == nst - 1) {
+      o0 -= chunk & 64;
+      most -= chunk & 64;
+    }
+    unroll<8>([&](auto j_) {
+      constexpr int j = decltype(j_)::value;
+      const uint32_t o = min(o0 + (j & 1) * s8 + (j >> 1) * s16, most);
+      if constexpr (decltype(nt_)::value != 0) load_lds16_nt(src + o, dst + j * 1024);
+      else load_lds16(src + o, dst + j * 1024);
+    });
+  };
+
+  // ------------------------------------------------------------------ scales
+  const int wcol = n0 + grp * (GATED ? 64 : 128);  // the wavefront's first column
+  const uint8_t* as;       // one byte a row
+  uint32_t ao[MODE == kFwd ? kMB : 1];
+  size_t astep;
+  const uint8_t* bs[2] = {nullptr, nullptr};
+  const float* bf[2] = {nullptr, nullptr};
+  uint32_t bo = 0;
+  if constexpr (MODE == kFwd) {
+    as = g.x_scale + seg + m0;
+    astep = g.line;
+#pragma unroll
+    for (int i = 0; i < kMB; ++i) ao[i] = min(i * 64 + q * 16 + l16, valid - 1);
+    const int ob = (g.z_dim + kBlk - 1) / kBlk;
+#pragma unroll
+    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+      const int zc = min(wcol, g.out_dim - 1) + h * g.out_dim;
+      const size_t at = (static_cast<size_t>(e) * ob + zc / kBlk) * nst;
+      if (WF32) bf[h] = static_cast<const float*>(g.w_scale) + at;
+      else bs[h] = static_cast<const uint8_t*>(g.w_scale) + at;
+    }
+  } else {
+    as = static_cast<const uint8_t*>(g.w_scale) + static_cast<size_t>(seg) * g.z_dim + m0;
+    astep = g.z_dim;
+    ao[0] = min(q * 64, valid - 64) + 4 * l16;
+    bs[0] = g.x_scale + static_cast<size_t>(seg) * g.in_dim + n0;
+    bo = 4 * l16;
+  }
+  // As loaded: widened where they are loaded, they would be waited for there.
+  struct Raw {
+    uint8_t a8[kMB], b8[2];
+    uint32_t a, b[2];
+    float f[2];
+  } raw{};
+  const int bc0 = MODE == kDw ? min(grp * 128, n_dim - n0 - 64) : 0;
+  const int bc1 = MODE == kDw ? min(grp * 128 + 64, n_dim - n0 - 64) : 0;
+  auto load_scales = [&](int p) {
+    const int pc = min(p, nst - 1);
+    const uint8_t* const a = as + pc * astep;
+    if constexpr (MODE == kFwd) {
+#pragma unroll
+      for (int i = 0; i < kMB; ++i) raw.a8[i] = a[ao[i]];
+#pragma unroll
+      for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+        if constexpr (WF32) raw.f[h] = bf[h][pc];
+        else raw.b8[h] = bs[h][pc];
+      }
+    } else {
+      raw.a = *reinterpret_cast<const uint32_t*>(a + ao[0]);
+      const uint8_t* const b = bs[0] + static_cast<size_t>(pc) * g.in_dim;
+      raw.b[0] = *reinterpret_cast<const uint32_t*>(b + bc0 + bo);
+      raw.b[1] = *reinterpret_cast<const uint32_t*>(b + bc1 + bo);
+    }
+    asm volatile("" ::: "memory");
+  };
+  struct Scale {
+    int a, b0, b1;
+    float f0, f1;
+  } now{};  // of the stage that is multiplied
+  auto take_scales = [&]() {
+    if constexpr (MODE == kFwd) {
+      now.a = raw.a8[0] | (raw.a8[1] << 8) | (raw.a8[2] << 16) | (raw.a8[3] << 24);
+      now.b0 = raw.b8[0];
+      now.b1 = GATED ? raw.b8[1] : raw.b8[0];
+      now.f0 = raw.f[0];
+      now.f1 = GATED ? raw.f[1] : raw.f[0];
+    } else {
+      now.a = static_cast<int>(raw.a);
+      now.b0 = static_cast<int>(raw.b[0]);
+      now.b1 = static_cast<int>(raw.b[1]);
+    }
+    if constexpr (WF32) asm volatile("" : "+v"(now.a), "+v"(now.f0), "+v"(now.f1));
+    else asm volatile("" : "+v"(now.a), "+v"(now.b0), "+v"(now.b1));
+  };
+
+  // ------------------------------------------------------- fragment addresses
+  const int fkey = swz128_key(l16);
+  const int fl0 = l16 * kLineBytes + (((lane >> 4) ^ fkey) << 4);
+  const int fl1 = l16 * kLineBytes + (((4 + (lane >> 4)) ^ fkey) << 4);
+  auto b_row = [&](int j) {  // first staged row of block j
+    if (GATED) return (j < kNB / 2 ? 0 : COLS) + grp * 64 + (j % (kNB / 2)) * 16;
+    return grp * 128 + j * 16;
+  };
+  uint32_t there = ~0u;  // HALF: 0 in the last stage
+  auto frag = [&](const char* at) {
+    const u32x4 lo = *reinterpret_cast<const u32x4*>(at + fl0);
+    u32x4 hi = *reinterpret_cast<const u32x4*>(at + fl1);
+    if constexpr (HALF) hi &= there;
+    return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]),
+                 static_cast<int>(lo[3]), static_cast<int>(hi[0]), static_cast<int>(hi[1]),
+                 static_cast<int>(hi[2]), static_cast<int>(hi[3])};
+  };
+
+  f32x4 acc[kMB][kNB];
+#pragma unroll
+  for (int i = 0; i < kMB; ++i)
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  if (nst > 0) {  // the same for the whole workgroup
+    // W of a group whose rows fit one tile is read by this tile alone: past
+    // L2, where the rows of x stay longer
+    const bool once = MODE == kFwd && count <= kT;
+    load_scales(0);
+    if (grp == 0) {
+      issue(0, abuf(0), CInt<0>{});
+      wait_vmem<0>();
+    } else {
+      if (once) {
+        issue(0, bbuf(0), CInt<1>{});
+        issue(1, bbuf(1), CInt<1>{});
+      } else {
+        issue(0, bbuf(0), CInt<0>{});
+        issue(1, bbuf(1), CInt<0>{});
+      }
+      wait_vmem<8>();
+    }
+    stage_barrier();
+
+    // A straight loop for each of the two halves: a shared one that branches
+    // every phase makes the compiler move the accumulators out of the AGPRs.
+    // Phases h = 0 .. 2 nst: half 0 reads in h = 2p and computes in 2p + 1,
+    // half 1 reads in 2p + 1 and computes in 2p + 2.
+    auto run = [&](auto live_, auto grp_, auto nt_) {
+      constexpr int LIVE = decltype(live_)::value, G = decltype(grp_)::value;
+      i32x8 fa[kMB], fb[kNB / 2];
+      const char* bnow = nullptr;
+      auto read = [&](int p) {
+        const char* const a = abuf(p & 1);
+        const char* const b = bbuf(p % 3);
+        bnow = b;
+        if constexpr (HALF) there = p == nst - 1 ? 0u : ~0u;
+        take_scales();  // of stage p: landed with its loads
+        load_scales(p + 1);
+        if (G == 0) issue(p + 1, abuf((p + 1) & 1), nt_);
+        else issue(p + 2, bbuf((p + 2) % 3), nt_);
+        if constexpr (LIVE > 0) {
+#pragma unroll
+          for (int i = 0; i < LIVE; ++i) fa[i] = frag(a + (i * 64 + q * 16) * kLineBytes);
+#pragma unroll
+          for (int j = 0; j < kNB / 2; ++j) fb[j] = frag(b + b_row(j) * kLineBytes);
+        }
+        // fragments are in registers; half 0 leaves A(p + 1) in flight, half 1
+        // waits for B(p + 1) and leaves B(p + 2)
+        if (G == 0) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        else {
+          wait_vmem<8>();
+        }
+      };
+      // The second half's fragments take the places of the first half's, each
+      // once the MFMAs of the next one are on their way too: an MFMA may still
+      // be reading when the next instruction issues.
+      auto again = [&](int j) {
+        if (j >= 1 && j <= kNB / 2)
+          fb[j - 1] = frag(bnow + b_row(j - 1 + kNB / 2) * kLineBytes);
+      };
+      auto compute = [&]() {
+        __builtin_amdgcn_s_setprio(2);
+        if constexpr (LIVE > 0) {
+          if constexpr (WF32) {
+#pragma unroll
+            for (int j = 0; j < kNB; ++j) {
+              const float f = j < kNB / 2 ? now.f0 : now.f1;
+              unroll<LIVE>([&](auto i_) {
+                constexpr int i = decltype(i_)::value;
+                const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+                const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    fa[i], fb[j % (kNB / 2)], z, 0, 0, i, now.a, 0, 127);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[r], f, acc[i][j][r]);
+              });
+              again(j);
+            }
+          } else {
+            asm volatile("s_nop 3");  // the scales' registers may just have been written
+            unroll<kNB>([&](auto j_) {
+              constexpr int j = decltype(j_)::value;
+              unroll<LIVE>([&](auto i_) {
+                constexpr int i = decltype(i_)::value;
+                mfma_f8_agpr<i, MODE == kDw ? j % 4 : 0>(acc[i][j], fa[i], fb[j % (kNB / 2)],
+                                                         now.a, j < 4 ? now.b0 : now.b1);
+              });
+              again(j);
+            });
+          }
+        }
+        __builtin_amdgcn_s_setprio(0);
+      };
+      if (G == 0) {
+        for (int p = 0; p < nst; ++p) {
+          read(p);
+          stage_barrier();
+          compute();
+          wait_vmem<0>();  // A(p + 1) has landed before anyone reads it
+          stage_barrier();
+        }
+        stage_barrier();
+      } else {
+        stage_barrier();
+        for (int p = 0; p < nst; ++p) {
+          read(p);
+          stage_barrier();
+          compute();
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          stage_barrier();
+        }
+        wait_vmem<0>();  // the loads past the last stage
+      }
+      stage_barrier();  // nothing is in flight, nobody reads the buffers
+    };
+    auto run_live = [&](auto grp_, auto nt_) {
+      if (mlive == 4) run(CInt<4>{}, grp_, nt_);
+      else if (MODE == kFwd && mlive == 3) run(CInt<MODE == kFwd ? 3 : 4>{}, grp_, nt_);
+      else if (MODE == kFwd && mlive == 2) run(CInt<MODE == kFwd ? 2 : 4>{}, grp_, nt_);
+      else if (MODE == kFwd && mlive == 1) run(CInt<MODE == kFwd ? 1 : 4>{}, grp_, nt_);
+      else run(CInt<0>{}, grp_, nt_);
+    };
+    if (grp == 0) run_live(CInt<0>{}, CInt<0>{});
+    else if (once) run_live(CInt<1>{}, CInt<1>{});
+    else run_live(CInt<1>{}, CInt<0>{});
+  }
+
+  // -------------------------------------------------------------- epilogue
+  // A lane holds 4 neighbouring columns of two chunks of 64 (SwiGLU: gate and
+  // up of one), 16 rows; 16 lanes make a whole line of bf16.
+  mfma_drain();
+#pragma unroll
+  for (int i = 0; i < kMB; ++i)
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) {
+      if constexpr (WF32) asm volatile("" : "+v"(acc[i][j]));
+    }
+  constexpr int CH = GATED ? 1 : 2;
+  const int c = wcol + 4 * l16;
+  float* const tops = reinterpret_cast<float*>(smem);  // [2][256], SwiGLU packed
+  auto tile_row = [&](int i, int r) {
+    if (MODE == kDw) return q * 64 + 16 * (lane >> 4) + 4 * r + i;
+    return i * 64 + q * 16 + 4 * (lane >> 4) + r;
+  };
+  auto values = [&](int i, int r, float (*v)[4]) {
+#pragma unroll
+    for (int h = 0; h < CH; ++h)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float z = acc[i][4 * h + k][r];
+        v[h][k] = GATED ? z * sigmoid_close(z) * acc[i][4 + k][r] : z;
+        if (c + 64 * h >= n_dim) v[h][k] = 0.f;
+      }
+  };
+  if constexpr (GATED) {  // once: the passes below read the result
+#pragma unroll
+    for (int i = 0; i < kMB; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float v[CH][4];
+        values(i, r, v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][k][r] = v[0][k];
+      }
+  }
+  auto value = [&](int i, int r, int h, int k) {
+    return GATED ? acc[i][k][r] : (c + 64 * h >= n_dim ? 0.f : acc[i][4 * h + k][r]);
+  };
+  if (MODE == kDw || g.y != nullptr) {
+#pragma unroll
+    for (int i = 0; i < kMB; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = tile_row(i, r);
+        const size_t at = MODE == kDw
+            ? (static_cast<size_t>(e) * g.z_dim + m0 + row) * g.in_dim + c
+            : static_cast<size_t>(seg + m0 + row) * g.out_dim + c;
+#pragma unroll
+        for (int h = 0; h < CH; ++h) {
+          if (row >= valid || c + 64 * h >= n_dim) continue;
+          uint32_t w[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            w[k] = static_cast<uint32_t>(f32_to_bf16(value(i, r, h, 2 * k))) |
+                   (static_cast<uint32_t>(f32_to_bf16(value(i, r, h, 2 * k + 1))) << 16);
+          typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+          __builtin_nontemporal_store(u32x2{w[0], w[1]},
+                                      reinterpret_cast<u32x2*>(static_cast<bf16_t*>(g.y) + at + 64 * h));
+        }
+      }
+  }
+  if constexpr (MODE == kFwd) {
+    if (g.y_codes == nullptr) return;
+    // a block of 128 columns: the wavefront's, or with SwiGLU its own 64 and
+    // those of the wavefront of the other half
+    float top[kMB][4];
+#pragma unroll
+    for (int i = 0; i < kMB; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < CH; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[4 * h + k] = value(i, r, h, k);
+        bool bad = false;
+        float m = finite_max8(v, bad);
+        m = fmaxf(m, __shfl_xor(m, 1, 64));
+        m = fmaxf(m, __shfl_xor(m, 2, 64));
+        m = fmaxf(m, __shfl_xor(m, 4, 64));
+        top[i][r] = fmaxf(m, __shfl_xor(m, 8, 64));
+        if (GATED && l16 == 0) tops[grp * kT + tile_row(i, r)] = top[i][r];
+      }
+    if constexpr (GATED) {
+      lds_barrier();
+#pragma unroll
+      for (int i = 0; i < kMB; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          top[i][r] = fmaxf(top[i][r], tops[(grp ^ 1) * kT + tile_row(i, r)]);
+    }
+#pragma unroll
+    for (int i = 0; i < kMB; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = tile_row(i, r);
+        const int s = e8m0_of(top[i][r]);
+        const float inv = e8m0_inverse(s);
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < CH; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x = value(i, r, h, k);
+            v[4 * h + k] = fabsf(x) < INFINITY ? x : __builtin_nanf("");
+          }
+        const uint2 q8 = encode8(v, inv);
+        if (row >= valid) continue;
+        uint8_t* const o = g.y_codes + static_cast<size_t>(seg + m0 + row) * g.out_dim + c;
+        if (c < n_dim) *reinterpret_cast<uint32_t*>(o) = q8.x;
+        if (!GATED && c + 64 < n_dim) *reinterpret_cast<uint32_t*>(o + 64) = q8.y;
+        if (l16 == 0 && (!GATED || grp == 0) && wcol < n_dim)
+          g.y_scale[static_cast<size_t>(wcol / kBlk) * g.line + seg + m0 + row] = static_cast<uint8_t>(s);
+      }
+  }
+}
+
+template <bool GATED, bool WF32>
+hipError_t launch_t(const BlockArgs& g, hipStream_t s) {
+  constexpr int COLS = GATED ? kT / 2 : kT;
+  const long blocks = item_grid(g.rows, g.groups, kT, (g.out_dim + COLS - 1) / COLS);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(512);
+  if (g.in_dim % kBlk != 0)
+    hipLaunchKernelGGL((block_mfma_kernel<kFwd, GATED, WF32, true>), grid, block, 0, s, g);
+  else
+    hipLaunchKernelGGL((block_mfma_kernel<kFwd, GATED, WF32, false>), grid, block, 0, s, g);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_block_mfma(bool wf32, const BlockArgs& g, hipStream_t s) {
+  if (g.act == kActSwiglu) return wf32 ? launch_t<true, true>(g, s) : launch_t<true, false>(g, s);
+  return wf32 ? launch_t<false, true>(g, s) : launch_t<false, false>(g, s);
+}
+
+hipError_t launch_block_dw_mfma(const BlockArgs& g, hipStream_t s) {
+  const long nt = (g.in_dim + kT - 1) / kT;
+  const long chunks = (static_cast<long>(g.groups) * ((g.z_dim + kT - 1) / kT) * nt + 15) / 16;
+  hipLaunchKernelGGL((block_mfma_kernel<kDw, false, false, false>),
+                     dim3(static_cast<unsigned>(8 * ((chunks + 7) / 8) * 16)), dim3(512), 0, s, g);
+  return hipGetLastError();
+}
+
+}  // namespace moe
