@@ -354,19 +354,31 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
         __builtin_amdgcn_s_setprio(2);
         if constexpr (LIVE > 0) {
           if constexpr (WF32) {
+            // Each MFMA is followed by the fmas of the second one before it,
+            // whose sums are there by then; the order is pinned.
+            constexpr int LAG = LIVE > 1 ? 2 : 1, ALL = kNB * LIVE;
+            f32x4 d[LAG + 1];
+            const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+            auto add = [&](int n) {
+              const float f = n < ALL / 2 ? now.f0 : now.f1;
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                acc[n % LIVE][n / LIVE][r] = fmaf(d[n % (LAG + 1)][r], f, acc[n % LIVE][n / LIVE][r]);
+            };
 #pragma unroll
             for (int j = 0; j < kNB; ++j) {
-              const float f = j < kNB / 2 ? now.f0 : now.f1;
               unroll<LIVE>([&](auto i_) {
                 constexpr int i = decltype(i_)::value;
-                const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-                const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                const int n = j * LIVE + i;
+                d[n % (LAG + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                     fa[i], fb[j % (kNB / 2)], z, 0, 0, i, now.a, 0, 127);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[r], f, acc[i][j][r]);
+                if (n >= LAG) add(n - LAG);
+                __builtin_amdgcn_sched_barrier(0);
               });
               again(j);
             }
+#pragma unroll
+            for (int n = ALL - LAG; n < ALL; ++n) add(n);
           } else {
             asm volatile("s_nop 3");  // the scales' registers may just have been written
             unroll<kNB>([&](auto j_) {
