@@ -58,7 +58,7 @@ __device__ __forceinline__ void mfma_f8_agpr(f32x4& c, const i32x8& a, const i32
 }
 
 // HALF: the last block of a row has 64 elements.  Its other half reads the
-// first again, and is zeroed on its way into the registers.
+// first again, and that of x is zeroed on its way into the registers.
 template <int MODE, bool GATED, bool WF32, bool HALF>
 __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
   static_assert(MODE == kFwd || (!GATED && !WF32 && !HALF), "weight gradient: plain");
@@ -278,10 +278,10 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
     return grp * 128 + j * 16;
   };
   uint32_t there = ~0u;  // HALF: 0 in the last stage
-  auto frag = [&](const char* at) {
+  auto frag = [&](const char* at, auto first_) {
     const u32x4 lo = *reinterpret_cast<const u32x4*>(at + fl0);
     u32x4 hi = *reinterpret_cast<const u32x4*>(at + fl1);
-    if constexpr (HALF) hi &= there;
+    if constexpr (HALF && decltype(first_)::value != 0) hi &= there;
     return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]),
                  static_cast<int>(lo[3]), static_cast<int>(hi[0]), static_cast<int>(hi[1]),
                  static_cast<int>(hi[2]), static_cast<int>(hi[3])};
@@ -332,9 +332,9 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
         else issue(p + 2, bbuf((p + 2) % 3), nt_);
         if constexpr (LIVE > 0) {
 #pragma unroll
-          for (int i = 0; i < LIVE; ++i) fa[i] = frag(a + (i * 64 + q * 16) * kLineBytes);
+          for (int i = 0; i < LIVE; ++i) fa[i] = frag(a + (i * 64 + q * 16) * kLineBytes, CInt<1>{});
 #pragma unroll
-          for (int j = 0; j < kNB / 2; ++j) fb[j] = frag(b + b_row(j) * kLineBytes);
+          for (int j = 0; j < kNB / 2; ++j) fb[j] = frag(b + b_row(j) * kLineBytes, CInt<0>{});
         }
         // fragments are in registers; half 0 leaves A(p + 1) in flight, half 1
         // waits for B(p + 1) and leaves B(p + 2)
@@ -348,7 +348,7 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
       // be reading when the next instruction issues.
       auto again = [&](int j) {
         if (j >= 1 && j <= kNB / 2)
-          fb[j - 1] = frag(bnow + b_row(j - 1 + kNB / 2) * kLineBytes);
+          fb[j - 1] = frag(bnow + b_row(j - 1 + kNB / 2) * kLineBytes, CInt<0>{});
       };
       auto compute = [&]() {
         __builtin_amdgcn_s_setprio(2);
