@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(HERE, "libmoe.so")
 
 SOURCES = ["route.hip", "permute.hip", "grouped_gemm.hip", "expert_gemm.hip", "combine.hip",
            "backward.hip", "moe_api.hip", "linear_tile.hip", "linear_mfma.hip", "linear_rows.hip", "checkpoint.hip", "group_rows.hip",
-           "combine_rows.hip", "linear_api.hip", "block_pack.hip", "block_tile.hip", "block_mfma.hip", "block_api.hip", "adamw.hip"]
+           "combine_rows.hip", "linear_api.hip", "block_pack.hip", "block_tile.hip", "block_mfma.hip", "block_rows.hip", "block_api.hip", "adamw.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

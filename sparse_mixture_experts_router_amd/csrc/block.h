@@ -59,6 +59,8 @@ struct BlockArgs {
   size_t line;
   int rows, groups, in_dim, out_dim, z_dim, act, parts;
   int dtype;               // of y
+  size_t place;            // block_rows.hip
+  bool split, deep;
   bool wide;               // fp32 results: products on the bf16 instruction
 };
 
@@ -72,6 +74,12 @@ hipError_t launch_block_join(const BlockArgs& g, hipStream_t s);
 int block_dw_parts(const BlockArgs& g, int cus);
 hipError_t launch_block_dw_tile(const BlockArgs& g, int cus, hipStream_t s);
 hipError_t launch_block_dw_join(const BlockArgs& g, hipStream_t s);
+
+// The product for few rows a group, in equal shares of all stages.  The plan
+// sets parts (workgroups), split (shares end inside tiles: two places of
+// `place` floats a workgroup in partial) and place.  False: too large.
+bool block_rows_plan(BlockArgs& g, int cus);
+hipError_t launch_block_rows(bool wf32, const BlockArgs& g, hipStream_t s);
 
 // Both on 256 x 256 tiles: results in bf16 or packed (not wide), unsplit.
 hipError_t launch_block_mfma(bool wf32, const BlockArgs& g, hipStream_t s);

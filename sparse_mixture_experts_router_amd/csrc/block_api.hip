@@ -111,6 +111,23 @@ bool forward_large(const BlockArgs& g) {
   const long cus = device_cus();
   return !g.wide && large_tiles(tiles, g.z_dim) && (g.rows * nt / 256 > cus / 4 || tiles * nt > cus);
 }
+bool few_rows(const BlockArgs& g) { return g.rows <= 32L * std::min(g.groups, g.rows); }
+// Few rows a group: W streamed past them.  Tiles of 128 x 128 take little W
+// without packed results (64 rows of 16 groups 2048 -> 4096 22 us, streamed 24)
+// and more rows (512 rows of 8 groups 4096 -> 2 x 14336 223 us, streamed 317;
+// 256 rows 248 and 195).
+bool forward_rows(BlockArgs& g, bool packed) {
+  if (!few_rows(g)) return false;
+  const long bytes = static_cast<long>(std::min(g.groups, g.rows)) * g.z_dim * g.in_dim;
+  if (g.in_dim <= 4096 && bytes <= (packed ? 16L << 20 : 128L << 20)) return false;
+  return block_rows_plan(g, device_cus());
+}
+size_t forward_space(BlockArgs g, bool packed) {
+  if (forward_rows(g, packed)) return g.split ? align_up(8 * g.place * g.parts) : kAlign;
+  if (forward_large(g)) return kAlign;
+  const size_t parts = block_tile_parts(g, device_cus());
+  return std::max(kAlign, align_up(parts * g.rows * g.z_dim * 4));
+}
 bool grad_large(const BlockArgs& g) {
   return !g.wide && large_tiles(static_cast<long>(g.groups) * ((g.z_dim + 255) / 256), g.in_dim);
 }
@@ -183,9 +200,7 @@ size_t moe_block_linear_workspace_size(const moe_block_linear_config* cfg) {
   if (check_linear(cfg, false) != MOE_OK) return 0;
   BlockArgs g = block_args(*cfg);
   g.wide = cfg->dtype == MOE_F32;
-  if (forward_large(g)) return kAlign;
-  const size_t parts = block_tile_parts(g, device_cus());
-  return std::max(kAlign, align_up(parts * g.rows * g.z_dim * 4));
+  return std::max(forward_space(g, false), forward_space(g, true));
 }
 
 moe_status moe_block_linear(const moe_block_linear_config* cfg, const moe_block_linear_args* a,
@@ -221,10 +236,17 @@ moe_status moe_block_linear(const moe_block_linear_config* cfg, const moe_block_
   const bool wf32 = cfg->w_scale_format == MOE_SCALE_F32;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int cus = device_cus();
+  if (forward_rows(g, g.y_codes != nullptr)) {
+    if (g.split) g.partial = static_cast<float*>(workspace);
+    const hipError_t err = launch_block_rows(wf32, g, s);
+    return err == hipSuccess ? MOE_OK : hip_fail(err, "block product kernel");
+  }
   if (forward_large(g)) {
     const hipError_t err = launch_block_mfma(wf32, g, s);
     return err == hipSuccess ? MOE_OK : hip_fail(err, "block product kernel");
   }
+  // packed results of few rows are of exact products whichever kernel makes them
+  if (g.y_codes != nullptr && few_rows(g)) g.wide = true;
   g.parts = block_tile_parts(g, cus);
   if (g.parts > 1 || g.y_codes != nullptr) g.partial = static_cast<float*>(workspace);
   hipError_t err = launch_block_tile(wf32, g, cus, s);

@@ -1,0 +1,468 @@
+// The product in 8-bit floating point with a scale for each block of 128, for
+// few rows a group (decode): bound by the bytes of W.
+//
+// A tile is 32 or 64 rows by 256 rows of W (SwiGLU: 128 gate rows and the up
+// rows of the same columns, so that a block of packed results is whole).  Tiles
+// differ in number from call to call and seldom fill the device evenly, so a
+// fixed grid takes equal shares of the list of all stages (tile after tile,
+// block of K after block): a workgroup's share may begin and end inside a tile.
+// The sums of such parts go to the workgroup's two places in the workspace, and
+// block_rows_join_kernel adds them up, one after the other.
+//
+// Eight wavefronts of 16 gate and 16 up rows of W (else 32 rows) by all rows of
+// the tile.  A stage is a block of 128 bytes of each row, loaded straight into
+// LDS.  Codes are widened to bf16, exactly, with the scales that are powers of
+// two, and multiplied by the bf16 instruction: the matrix cores wait for HBM
+// anyway, and the sums are of exact products (block_tile.hip says what the 8-bit
+// instruction drops).
+//
+// 64 rows of 8 groups: 4096 -> 2 x 14336 in 158 us and 14336 -> 4096 in 78 us,
+// 6 TB/s of W (tiles of 128 x 128: 233 and 130); 128 rows of 256 groups 7168 ->
+// 2 x 2048 in 450 us, 6.6 TB/s (583).
+#include "block.h"
+#include "lds_ring.h"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+constexpr int kCols = 256;  // rows of W of a tile
+
+// Where share i of n begins.  The plan keeps units * n under 2^32.
+__device__ __forceinline__ uint32_t share_begin(uint32_t units, int i, uint32_t n) {
+  return units * static_cast<uint32_t>(i) / n;
+}
+
+template <int N> struct CInt { static constexpr int value = N; };
+
+// D: stages of the ring.  2: two workgroups share a compute unit.
+template <int MB, int D, bool GATED, bool WF32>
+__global__ __launch_bounds__(512, D == 2 ? 4 : 2) void block_rows_kernel(BlockArgs g) {
+  constexpr int BM = MB * 16;
+  constexpr int COLS = GATED ? kCols / 2 : kCols, WC = COLS / 8;  // result columns: tile, wavefront
+  constexpr int NO = GATED ? 1 : 2;
+  constexpr int kStage = (BM + kCols) * kLineBytes;
+  constexpr int AL = (BM / 8 + 7) / 8;  // a wavefront's loads of x
+  // a wavefront's loads of a stage, scales included: at least so many
+  constexpr int LOADS = 4 + AL + MB;
+  __shared__ __attribute__((aligned(1024))) char smem[D * kStage];
+
+  const int nt = (g.out_dim + COLS - 1) / COLS;
+  const int nst = (g.in_dim + kBlk - 1) / kBlk;
+  const TileScan scan = scan_tiles(g.offsets, g.groups, g.rows, BM);
+  // shares of stages, or of whole tiles; every XCD has neighbouring ones
+  const uint32_t units = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(scan.total)) * nt *
+                         (g.split ? nst : 1);
+  const uint32_t shares = min(static_cast<uint32_t>(g.parts), units);
+  const int me = (blockIdx.x & 7) * (g.parts >> 3) + (blockIdx.x >> 3);
+  if (static_cast<uint32_t>(me) >= shares) return;
+  const uint32_t u0 = share_begin(units, me, shares), u1 = share_begin(units, me + 1, shares);
+
+  const int lane = threadIdx.x & 63, l16 = lane & 15, quad = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t chunk = line_lane_chunk(lane, 0) * 16;
+  const int key = swz128_key(l16);
+  const int fl0 = l16 * kLineBytes + ((quad ^ key) << 4);
+  const int fl1 = l16 * kLineBytes + (((4 + quad) ^ key) << 4);
+  // 32 rows: every load of x by two wavefronts, for the count's sake
+  const int arow = wave * 8 % (BM < 64 ? BM : 64);
+  const bool half_last = (g.in_dim & 64) != 0;
+  const uint32_t row_bytes = static_cast<uint32_t>(g.in_dim);
+
+  for (uint32_t u = u0; u < u1;) {
+    const uint32_t item = g.split ? u / nst : u;
+    const int s0 = g.split ? u - item * nst : 0;
+    const int s1 = g.split ? min(nst, s0 + static_cast<int>(u1 - u)) : nst;
+    TileAt at;
+    int col;
+    item_at(scan, g.offsets, g.groups, g.rows, BM, nt, item, at, col);
+    const int e = __builtin_amdgcn_readfirstlane(at.e);
+    const int row0 = __builtin_amdgcn_readfirstlane(at.begin + at.m * BM);
+    const int valid = min(BM, __builtin_amdgcn_readfirstlane(at.end) - row0);
+    const int n0 = __builtin_amdgcn_readfirstlane(col) * COLS;
+    const int wcol = n0 + wave * WC;  // the wavefront's first column
+
+    // Rows a multiple of 8 KB apart: workgroups in step with each other would
+    // ask for blocks that all lie in the same few channels of HBM, so each
+    // begins elsewhere in its part of K (64 rows of 16 groups 8192 -> 4096 117
+    // -> 81 us).  Other rows are better read from their beginning (64 rows of 8
+    // groups 4096 -> 2 x 14336 158 us, begun elsewhere 162).
+    const int len = s1 - s0;
+    const int turn = g.in_dim % 8192 == 0 ? (static_cast<uint32_t>(me) * 0x9e3779b1u >> 8) % len : 0;
+    auto stage_of = [&](int q) {  // q-th of the part; past the end the last
+      const int k = min(q, len - 1) + turn;
+      return s0 + (k < len ? k : k - len);
+    };
+
+    // ------------------------------------------------- this lane's sources
+    uint32_t aoff[AL], boff[4];
+    const char* const abase = reinterpret_cast<const char*>(g.x) + static_cast<size_t>(row0) * row_bytes;
+    const char* const bbase = reinterpret_cast<const char*>(g.w) +
+                              (static_cast<size_t>(e) * g.z_dim + n0 +
+                               (GATED && wave >= 4 ? g.out_dim : 0)) * row_bytes;
+#pragma unroll
+    for (int j = 0; j < AL; ++j) {
+      const int r = min(j * 64 + arow + (lane >> 3), valid - 1);
+      aoff[j] = static_cast<uint32_t>(r) * row_bytes + chunk;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = (GATED ? wave & 3 : wave) * 32 + j * 8 + (lane >> 3);
+      boff[j] = static_cast<uint32_t>(min(c, g.out_dim - 1 - n0)) * row_bytes + chunk;
+    }
+    // past the end the last stage again, into a buffer that nobody reads any
+    // more: the count of loads in flight stays the same
+    auto issue = [&](int q) {
+      char* const buf = smem + q % D * kStage;
+      const int p = stage_of(q);
+      const char* const a = abase + static_cast<size_t>(p) * kLineBytes;
+      const char* const b = bbase + static_cast<size_t>(p) * kLineBytes;
+      // a last block of 64: in place of its other half the first again, which
+      // meets zeros in x
+      const uint32_t back = half_last && p == nst - 1 ? chunk & 64 : 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        char* const to = buf + (BM + wave * 32 + j * 8) * kLineBytes;
+        // W of a group whose rows fit one tile is read once: past the caches
+        if (MB == 2) load_lds16_nt(b + (boff[j] - back), to);
+        else load_lds16(b + (boff[j] - back), to);
+      }
+#pragma unroll
+      for (int j = 0; j < AL; ++j)
+        load_lds16(a + (aoff[j] - back), buf + (j * 64 + arow) * kLineBytes);
+    };
+
+    // ---------------------------------------------------------------- scales
+    const uint8_t* const as = g.x_scale + row0;
+    uint32_t ao[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) ao[i] = min(i * 16 + l16, valid - 1);
+    size_t bat[2];
+    const int ob = (g.z_dim + kBlk - 1) / kBlk;
+#pragma unroll
+    for (int h = 0; h < (GATED ? 2 : 1); ++h)
+      bat[h] = (static_cast<size_t>(e) * ob + (min(wcol, g.out_dim - 1) + h * g.out_dim) / kBlk) * nst;
+    struct Scales {
+      int a[MB], b[2];
+      float f[2];
+    };
+    auto load_scales = [&](int q, Scales& s) {
+      const int p = stage_of(q);
+#pragma unroll
+      for (int i = 0; i < MB; ++i) s.a[i] = (as + p * g.line)[ao[i]];
+#pragma unroll
+      for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+        if constexpr (WF32) s.f[h] = static_cast<const float*>(g.w_scale)[bat[h] + p];
+        else s.b[h] = static_cast<const uint8_t*>(g.w_scale)[bat[h] + p];
+      }
+      asm volatile("" ::: "memory");
+    };
+
+    f32x4 acc[MB][2];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // ------------------------------------------------------------- main loop
+    // Stage p + D - 1 is asked for once everybody is done with p - 1, whose
+    // buffer it takes; its scales come just before it.
+    Scales sc[D];
+    lds_barrier();  // everybody is done with the buffers of the last tile
+#pragma unroll
+    for (int p = 0; p < D - 1; ++p) {
+      load_scales(p, sc[p]);
+      issue(p);
+    }
+    auto step = [&](int q, auto slot) {
+      constexpr int S = decltype(slot)::value;
+      wait_vmem<(D - 2) * LOADS>();
+      stage_barrier();
+      load_scales(q + D - 1, sc[(S + D - 1) % D]);
+      issue(q + D - 1);
+      const Scales& cur = sc[S];
+      const char* const buf = smem + q % D * kStage;
+      const uint32_t there = half_last && stage_of(q) == nst - 1 ? 0u : ~0u;
+      auto frag = [&](const char* from, uint32_t mask) {
+        const u32x4 lo = *reinterpret_cast<const u32x4*>(from + fl0);
+        const u32x4 hi = *reinterpret_cast<const u32x4*>(from + fl1) & mask;
+        return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]),
+                     static_cast<int>(lo[3]), static_cast<int>(hi[0]), static_cast<int>(hi[1]),
+                     static_cast<int>(hi[2]), static_cast<int>(hi[3])};
+      };
+      i32x8 b[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        b[j] = frag(buf + (BM + (GATED ? j * 128 + wave * 16 : wave * 32 + j * 16)) * kLineBytes, ~0u);
+      const int hb = GATED ? 1 : 0;
+      u32x4 wb[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          wb[j][t] = widen8(b[j], t, WF32 ? 1.0f : e8m0_value(cur.b[j * hb]));
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        if (i * 16 >= valid) break;  // the same for the whole workgroup
+        const i32x8 a = frag(buf + i * 16 * kLineBytes, there);
+        const float as = e8m0_value(cur.a[i]);
+        f32x4 d[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) d[j] = WF32 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[i][j];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const u32x4 wa = widen8(a, t, as);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) d[j] = Mfma<bf16_t>::step(wa, wb[j][t], d[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if constexpr (WF32) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[j][r], cur.f[j * hb], acc[i][j][r]);
+          } else {
+            acc[i][j] = d[j];
+          }
+        }
+      }
+    };
+    // Whole rounds of the ring first: a way out of the middle of a round would
+    // make the compiler wait for every load at its start.
+    int q = 0;
+    for (; q + D <= len; q += D) {
+      step(q, CInt<0>{});
+      step(q + 1, CInt<1>{});
+      if constexpr (D > 2) step(q + 2, CInt<2>{});
+      if constexpr (D > 3) step(q + 3, CInt<3>{});
+    }
+    if (q < len) step(q, CInt<0>{});
+    if constexpr (D > 2) {
+      if (q + 1 < len) step(q + 1, CInt<1>{});
+    }
+    if constexpr (D > 3) {
+      if (q + 2 < len) step(q + 2, CInt<2>{});
+    }
+    wait_vmem<0>();  // the loads past the last stage
+    // see block_tile.hip: no matrix instruction may move into a branch below
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(acc[i][j]));
+    const bool second = u0 < u - s0;  // a part that ends the share, after other tiles
+    u += g.split ? s1 - s0 : 1;
+    // opaque, or the addresses below are made before the loop and held through it
+    int r4 = 4 * quad, c16 = l16;
+    asm volatile("" : "+v"(r4), "+v"(c16));
+
+    // ------------------------------------------------------------ epilogue
+    // A lane: column c16 of each of its blocks, rows 16 i + 4 quad + r.
+    if (s1 - s0 < nst) {
+      float* const o = g.partial + (2 * me + second) * g.place;
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * i + r4 + r;
+          if (row >= valid) continue;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            o[row * kCols + (GATED ? j * 128 + wave * 16 : wave * 32 + j * 16) + c16] = acc[i][j][r];
+        }
+      continue;
+    }
+    if constexpr (GATED) {
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][0][r] = acc[i][0][r] * sigmoid_close(acc[i][0][r]) * acc[i][1][r];
+    }
+    const bool busy = wcol < g.out_dim;  // WC divides 64: a wavefront is in or out
+    if (g.y != nullptr && busy) {
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * i + r4 + r;
+          if (row >= valid) continue;
+          const size_t o = static_cast<size_t>(row0 + row) * g.out_dim + wcol + c16;
+#pragma unroll
+          for (int j = 0; j < NO; ++j) {
+            if (g.dtype == 1) static_cast<bf16_t*>(g.y)[o + j * 16] = f32_to_bf16(acc[i][j][r]);
+            else static_cast<float*>(g.y)[o + j * 16] = acc[i][j][r];
+          }
+        }
+    }
+    if (g.y_codes == nullptr) continue;
+    // a block of 128 columns is 8 / NO wavefronts: their largest values meet in LDS
+    float* const tops = reinterpret_cast<float*>(smem);  // [8][BM]
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < NO; ++j) {
+          const float x = fabsf(acc[i][j][r]);
+          if (busy && x < INFINITY) m = fmaxf(m, x);
+        }
+        m = fmaxf(m, __shfl_xor(m, 1, 64));
+        m = fmaxf(m, __shfl_xor(m, 2, 64));
+        m = fmaxf(m, __shfl_xor(m, 4, 64));
+        m = fmaxf(m, __shfl_xor(m, 8, 64));
+        if (c16 == 0) tops[wave * BM + 16 * i + r4 + r] = m;
+      }
+    lds_barrier();
+    if (!busy) continue;
+    constexpr int PER = 8 / NO;  // wavefronts of a block
+    const int w0 = wave / PER * PER;
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * i + r4 + r;
+        if (row >= valid) continue;
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) m = fmaxf(m, tops[(w0 + k) * BM + row]);
+        const int s = e8m0_of(m);
+        const float inv = e8m0_inverse(s);
+#pragma unroll
+        for (int j = 0; j < NO; ++j) {
+          const float x = acc[i][j][r];
+          const float v = fabsf(x) < INFINITY ? x * inv : __builtin_nanf("");
+          g.y_codes[static_cast<size_t>(row0 + row) * g.out_dim + wcol + j * 16 + c16] =
+              static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v, 0.f, 0, false));
+        }
+        if (c16 == 0 && wave == w0)
+          g.y_scale[static_cast<size_t>(wcol / kBlk) * g.line + row0 + row] = static_cast<uint8_t>(s);
+      }
+  }
+}
+
+// The tiles whose stages lie in several shares: y = act(sum of their parts), 16
+// rows by 128 columns a workgroup, 16 lanes a row.
+template <bool GATED>
+__global__ __launch_bounds__(256) void block_rows_join_kernel(BlockArgs g, int bm) {
+  constexpr int COLS = GATED ? kCols / 2 : kCols;
+  const int nt = (g.out_dim + COLS - 1) / COLS;
+  const int nst = (g.in_dim + kBlk - 1) / kBlk;
+  const TileScan scan = scan_tiles(g.offsets, g.groups, g.rows, bm);
+  const uint32_t items = static_cast<uint32_t>(scan.total) * nt, units = items * nst;
+  const uint32_t item = blockIdx.x;
+  if (item >= items) return;
+  const uint32_t shares = min(static_cast<uint32_t>(g.parts), units);
+  // the share that holds stage u is the last one that begins at u or before
+  const int i0 = ((item * nst + 1) * shares - 1) / units;
+  const int i1 = ((item + 1) * nst * shares - 1) / units;
+  if (i0 == i1) return;
+  const float* const first =
+      g.partial + (2 * i0 + (share_begin(units, i0, shares) < item * nst)) * g.place;
+  TileAt at;
+  int col;
+  item_at(scan, g.offsets, g.groups, g.rows, bm, nt, item, at, col);
+  const int r = blockIdx.y * 16 + (threadIdx.x >> 4), l16 = threadIdx.x & 15;
+  const int row0 = at.begin + at.m * bm, row = row0 + r;
+  const bool live = row < min(row0 + bm, at.end);
+  const int c = blockIdx.z * kBlk + l16 * 8, n = col * COLS + c;
+  const bool in = live && n < g.out_dim;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (in) {
+    float up[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    auto add = [&](const float* from) {
+      float w[8], x[8];
+      load8<float>(from + r * kCols + c, w);
+      if (GATED) load8<float>(from + r * kCols + c + COLS, x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] += w[k];
+        if (GATED) up[k] += x[k];
+      }
+    };
+    add(first);
+#pragma unroll 4
+    for (int i = i0 + 1; i <= i1; ++i) add(g.partial + 2 * i * g.place);
+    if (GATED) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = v[k] * sigmoid_close(v[k]) * up[k];
+    }
+    if (g.y != nullptr) {
+      const size_t o = static_cast<size_t>(row) * g.out_dim + n;
+      if (g.dtype == 1) store8<bf16_t>(static_cast<bf16_t*>(g.y) + o, v);
+      else store8<float>(static_cast<float*>(g.y) + o, v);
+    }
+  }
+  if (g.y_codes == nullptr) return;
+  bool bad = false;
+  float m = finite_max8(v, bad);
+  m = fmaxf(m, __shfl_xor(m, 1, 64));
+  m = fmaxf(m, __shfl_xor(m, 2, 64));
+  m = fmaxf(m, __shfl_xor(m, 4, 64));
+  m = fmaxf(m, __shfl_xor(m, 8, 64));
+  const int s = e8m0_of(m);
+  if (in)
+    *reinterpret_cast<uint2*>(g.y_codes + static_cast<size_t>(row) * g.out_dim + n) =
+        encode8_finite(v, e8m0_inverse(s), bad);
+  if (live && l16 == 0 && n < g.out_dim)
+    g.y_scale[static_cast<size_t>(n / kBlk) * g.line + row] = static_cast<uint8_t>(s);
+}
+
+int row_blocks(const BlockArgs& g) {
+  const long each = g.rows / std::max(1, std::min(g.groups, g.rows));
+  return each <= 16 ? 2 : 4;
+}
+long items_of(const BlockArgs& g, int bm) {
+  const int cols = g.act == kActSwiglu ? kCols / 2 : kCols;
+  return (g.rows / bm + std::min<long>(g.groups, g.rows)) * ((g.out_dim + cols - 1) / cols);
+}
+
+template <int MB, bool GATED, bool WF32>
+hipError_t launch_t(const BlockArgs& g, hipStream_t s) {
+  constexpr int BM = MB * 16;
+  const dim3 grid(g.parts);
+  if (g.deep)
+    hipLaunchKernelGGL((block_rows_kernel<MB, MB == 2 ? 4 : 3, GATED, WF32>), grid, dim3(512), 0, s, g);
+  else
+    hipLaunchKernelGGL((block_rows_kernel<MB, 2, GATED, WF32>), grid, dim3(512), 0, s, g);
+  if (g.split)
+    hipLaunchKernelGGL((block_rows_join_kernel<GATED>),
+                       dim3(static_cast<unsigned>(items_of(g, BM)), MB, GATED ? 1 : 2), dim3(256), 0, s,
+                       g, BM);
+  return hipGetLastError();
+}
+template <bool GATED, bool WF32>
+hipError_t launch_mb(const BlockArgs& g, hipStream_t s) {
+  return row_blocks(g) == 2 ? launch_t<2, GATED, WF32>(g, s) : launch_t<4, GATED, WF32>(g, s);
+}
+
+}  // namespace
+
+bool block_rows_plan(BlockArgs& g, int cus) {
+  const int mb = row_blocks(g);
+  const long items = items_of(g, mb * 16), nst = (g.in_dim + kBlk - 1) / kBlk;
+  // A deep ring where a compute unit has one tile at most (64 rows of 16 groups
+  // 4096 -> 4096 57 -> 43.5 us), else two workgroups (64 rows of 16 groups 4096
+  // -> 2 x 4096 92 -> 86).
+  g.deep = items <= cus;
+  const long slots = std::max(8, cus * (g.deep ? 1 : 2) / 8 * 8);
+  // Shares that end inside tiles cost a second launch of about 5 us and a pass
+  // over the sums: worth it where whole tiles would leave a workgroup idle for
+  // more than 8 stages (2 rows of 8 groups 2048 -> 4096 15.8 -> 12.1 us, 1024
+  // -> 4096 10.2 -> 11.2), or where the groups that have rows are too few to
+  // tell (128 rows of 256 groups 7168 -> 2 x 2048 585 -> 452).
+  const long idle = (slots - 1 - (items + slots - 1) % slots) * nst / slots;
+  const bool unknown = g.rows < 4L * g.groups && items > slots && nst >= 32;
+  g.split = idle > 8 || unknown;
+  const long want = ((g.split ? items * nst / 4 : items) + 7) / 8 * 8;
+  g.parts = static_cast<int>(std::max(8L, std::min(slots, want)));
+  g.place = static_cast<size_t>(std::min(g.rows, mb * 16)) * kCols;
+  return (items + 1) * (g.split ? nst : 1) * g.parts < (1L << 32);
+}
+
+hipError_t launch_block_rows(bool wf32, const BlockArgs& g, hipStream_t s) {
+  if (g.act == kActSwiglu) return wf32 ? launch_mb<true, true>(g, s) : launch_mb<true, false>(g, s);
+  return wf32 ? launch_mb<false, true>(g, s) : launch_mb<false, false>(g, s);
+}
+
+}  // namespace moe

@@ -171,11 +171,20 @@ __device__ __forceinline__ TileAt find_tile(const TileScan& t, const int32_t* of
   return a;
 }
 
-// Work item (group, row tile, column tile) of workgroup blockIdx.x on a grid
-// of 8 equal shares: workgroups take the 8 XCDs in turn, and each XCD walks a
-// contiguous share of the list, so the tiles it runs at once share rows of x
-// and of W in its L2.  Inside a group the tiles go in bands of 8 row tiles,
-// column by column.  False: nothing to do.
+// Work item w (group, row tile, column tile) of the list of all of them: inside
+// a group the tiles go in bands of 8 row tiles, column by column.
+__device__ __forceinline__ void item_at(const TileScan& t, const int32_t* offsets, int groups,
+                                        int rows, int bm, int nt, long w, TileAt& at, int& col) {
+  at = find_tile(t, offsets, groups, rows, bm, static_cast<int>(w / nt));
+  const int q = static_cast<int>(w - static_cast<long>(at.before) * nt);
+  const int band = q / (8 * nt), tw = min(8, at.tiles - band * 8), r = q - band * 8 * nt;
+  col = r / tw;
+  at.m = band * 8 + r % tw;
+}
+// The item of workgroup blockIdx.x on a grid of 8 equal shares: workgroups take
+// the 8 XCDs in turn, and each XCD walks a contiguous share of the list, so the
+// tiles it runs at once share rows of x and of W in its L2.  False: nothing to
+// do.
 __device__ __forceinline__ bool find_item(const int32_t* offsets, int groups, int rows, int bm,
                                           int nt, TileAt& at, int& col) {
   const TileScan t = scan_tiles(offsets, groups, rows, bm);
@@ -183,12 +192,7 @@ __device__ __forceinline__ bool find_item(const int32_t* offsets, int groups, in
   const long items = static_cast<long>(t.total) * nt;
   const long lo = items * xcd / 8, hi = items * (xcd + 1) / 8;
   if (lo + idx >= hi) return false;
-  const long w = lo + idx;
-  at = find_tile(t, offsets, groups, rows, bm, static_cast<int>(w / nt));
-  const int q = static_cast<int>(w - static_cast<long>(at.before) * nt);
-  const int band = q / (8 * nt), tw = min(8, at.tiles - band * 8), r = q - band * 8 * nt;
-  col = r / tw;
-  at.m = band * 8 + r % tw;
+  item_at(t, offsets, groups, rows, bm, nt, lo + idx, at, col);
   return true;
 }
 inline long item_grid(long rows, long groups, int bm, long nt) {

@@ -384,6 +384,45 @@ def test_linear_large(act, w_scale):
         c.check(c.run(), ref)
 
 
+FEW = [  # sizes, in, out: rows few enough that W is streamed past them
+    ([1], 4160, 64), ([3, 0, 1], 4224, 192),
+    ([16, 0, 3, 40], 8192, 320),       # rows a multiple of 8 KB, two tiles of a group
+    ([20, 33, 17, 0, 31], 4160, 704),  # tiles of 64 rows, a half block
+    ([1, 2] * 140, 4160, 64),          # more tiles than compute units, shares that end inside them
+    ([21] * 70, 320, 576), ([2] * 70, 320, 576),  # whole tiles, more than compute units
+    ([1] * 12, 4672, 1344)]
+
+
+@pytest.mark.parametrize("w_scale", ["e8m0", "f32"])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("sizes,K,F", FEW, ids=lambda v: str(v)[:30])
+def test_linear_few_rows(sizes, K, F, act, w_scale):
+    dtype = "f32" if (len(sizes) + (act == "none")) % 2 else "bf16"
+    c = Product(sizes, K, F, act, dtype, w_scale, first=2, spare=3, seed=K + F)
+    ref = c.reference()
+    c.check(c.run(codes=True), ref)
+    c.check(c.run(codes=True, plain=False), ref)
+    c.check(c.run(), ref)
+
+
+def test_linear_few_rows_nan_codes_and_repeats():
+    c = Product([9, 5], 4672, 192, seed=5)
+    first = c.run(codes=True)
+    again = c.run(codes=True)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    c.x[3, 4671], c.w[1, 7, 3] = 0x7F, 0xFF
+    for out in (c.run(codes=True), c.run(codes=True)):
+        y = to_np(out[0])
+        nan = np.zeros_like(y, dtype=bool)
+        nan[3], nan[9:14, 7] = True, True
+        assert (np.isnan(y) == nan).all()
+        assert ((to_np(out[1]) & 0x7F == 0x7F) == nan).all()
+    for off in ([-5, 1 << 30, 7], [90, 10, 200], [1 << 30, 1 << 30, 1 << 30], [-9, -9, -1]):
+        c.offsets = torch.tensor(off, dtype=torch.int32, device=DEV)
+        c.run(codes=True)
+    torch.cuda.synchronize()
+
+
 def test_linear_nan_codes_and_repeats():
     c = Product([40, 90], 256, 192, seed=5)
     first = c.run(codes=True)
