@@ -119,7 +119,7 @@ bool few_rows(const BlockArgs& g) { return g.rows <= 32L * std::min(g.groups, g.
 bool forward_rows(BlockArgs& g, bool packed) {
   if (!few_rows(g)) return false;
   const long bytes = static_cast<long>(std::min(g.groups, g.rows)) * g.z_dim * g.in_dim;
-  if (g.in_dim <= 4096 && bytes <= (packed ? 16L << 20 : 128L << 20)) return false;
+  if (g.in_dim <= 4096 && bytes <= (packed ? 16L << 20 : 128L << 20) && !(packed && g.in_dim <= 1024)) return false;
   return block_rows_plan(g, device_cus());
 }
 size_t forward_space(BlockArgs g, bool packed) {

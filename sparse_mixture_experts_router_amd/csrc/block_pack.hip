@@ -7,7 +7,13 @@
 //
 // v / 2^e is exact, so a code has one rounding (at most 2^-4 of the value), and
 // turned codes and row codes are made from the same fp32 values.  Every call is
-// one pass: bound by HBM.
+// one pass.
+//
+// Bound by HBM where groups fill their blocks (32768 rows of 8 groups, both
+// forms of 7168 bf16 columns 172 us, 5.5 TB/s); groups of about 128 rows, whose
+// last blocks are half empty, by the vector unit and by each workgroup's chain
+// of offsets, loads and stores (SwiGLU's gradient of 32768 rows of 256 groups,
+// 4096 columns: 198 us, 3.4 TB/s).
 #include "block.h"
 
 namespace moe {
@@ -22,12 +28,12 @@ struct RowBlock {
 __device__ __forceinline__ RowBlock find_block(const int32_t* offsets, int groups, int rows,
                                                int b) {
   if (offsets == nullptr) return RowBlock{b * kBlk, min(rows, (b + 1) * kBlk)};
-  int lo = 0, hi = groups - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (turned_first(min(max(offsets[mid], 0), rows), mid) <= b) lo = mid;
-    else hi = mid - 1;
+  int before = 0;  // groups that start at or before b
+  for (int e = threadIdx.x & 63; e - static_cast<int>(threadIdx.x & 63) < groups; e += 64) {
+    const bool hit = e < groups && turned_first(min(max(offsets[min(e, groups - 1)], 0), rows), e) <= b;
+    before += __popcll(__ballot(hit));
   }
+  const int lo = max(before - 1, 0);
   const int2 r = group_range(offsets, lo, rows);
   const long at = static_cast<long>(r.x) + static_cast<long>(b - turned_first(r.x, lo)) * kBlk;
   if (at < r.x || at >= r.y) return RowBlock{0, 0};
@@ -81,19 +87,45 @@ __device__ __forceinline__ void values8(const PackArgs& g, int row, int c, float
   }
 }
 
-// The largest of the 16 lanes that hold a row's block.
+// The largest of the 16 lanes that hold a row's block (values >= 0).
+template <int N> __device__ __forceinline__ float max_turned(float m) {  // and that of N lanes on
+  const int o = __builtin_amdgcn_mov_dpp(static_cast<int>(__float_as_uint(m)), 0x120 + N, 0xf, 0xf, true);
+  return fmaxf(m, __uint_as_float(static_cast<uint32_t>(o)));
+}
 __device__ __forceinline__ float max16(float m) {
-  m = fmaxf(m, __shfl_xor(m, 1, 64));
-  m = fmaxf(m, __shfl_xor(m, 2, 64));
-  m = fmaxf(m, __shfl_xor(m, 4, 64));
-  return fmaxf(m, __shfl_xor(m, 8, 64));
+  return max_turned<1>(max_turned<2>(max_turned<4>(max_turned<8>(m))));
+}
+
+// The gradient of SwiGLU reads the same z and dy for the gate's columns and the
+// up projection's, so one thread makes both (H = 2, where each has whole blocks
+// of columns).  Values of gate column c and of its up column, or of column c.
+template <typename T, int ACT, bool BACK, int H, int R>
+__device__ __forceinline__ void values(const PackArgs& g, int row, int c, float (*v)[R][8], int r) {
+  if constexpr (H == 1) {
+    values8<T, ACT, BACK>(g, row, c, v[0][r]);
+  } else {
+    int src = row;
+    if (g.row_index != nullptr) src = min(max(g.row_index[row], 0), g.x_rows - 1);
+    const int half = g.cols / 2;
+    const T* const z = static_cast<const T*>(g.x) + static_cast<size_t>(src) * g.cols + c;
+    float a[8], b[8], d[8];
+    load8<T>(z, a);
+    load8<T>(z + half, b);
+    load8<T>(static_cast<const T*>(g.dy) + static_cast<size_t>(row) * half + c, d);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float p = sigmoid_close(a[i]);
+      v[0][r][i] = d[i] * b[i] * p * (1.0f + a[i] * (1.0f - p));
+      v[1][r][i] = d[i] * a[i] * p;
+    }
+  }
 }
 
 constexpr int kRowsWg = 16;
 
 // Rows only: a workgroup packs 16 rows, 16 lanes to a block of 128 columns.
-template <typename T, int ACT, bool BACK>
-__global__ __launch_bounds__(256) void pack_rows_kernel(PackArgs g, int blocks_wg) {
+template <typename T, int ACT, bool BACK, int H>
+__global__ __launch_bounds__(256) void pack_rows_kernel(PackArgs g) {
   const int tid = threadIdx.x, l16 = tid & 15;
   const int row = blockIdx.x * kRowsWg + (tid >> 4);
   int first = 0, last = g.rows;
@@ -102,45 +134,62 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(PackArgs g, int blocks_w
     last = min(max(g.offsets[g.groups], 0), g.rows);
   }
   const bool live = row >= first && row < last;
-  const int blocks = (g.cols + kBlk - 1) / kBlk;
-  const int b0 = blockIdx.y * blocks_wg, b1 = min(blocks, b0 + blocks_wg);
-  for (int b = b0; b < b1; ++b) {
-    const int c = b * kBlk + l16 * 8;
-    const bool in = live && c < g.cols;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (in) values8<T, ACT, BACK>(g, row, c, v);
+  const int b = blockIdx.y, c = b * kBlk + l16 * 8;
+  const bool in = live && c < g.cols;
+  float v[H][1][8] = {};
+  if (in) values<T, ACT, BACK, H, 1>(g, row, c, v, 0);
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
     bool bad = false;
-    const int e = e8m0_of(max16(finite_max8(v, bad)));
+    const int e = e8m0_of(max16(finite_max8(v[h][0], bad)));
     if (in)
-      *reinterpret_cast<uint2*>(g.codes + static_cast<size_t>(row) * g.cols + c) =
-          encode8_finite(v, e8m0_inverse(e), bad);
-    if (live && l16 == 0) g.scale[b * g.line + row] = static_cast<uint8_t>(e);
+      *reinterpret_cast<uint2*>(g.codes + static_cast<size_t>(row) * g.cols + h * (g.cols / 2) + c) =
+          encode8_finite(v[h][0], e8m0_inverse(e), bad);
+    if (live && l16 == 0) g.scale[(b + h * gridDim.y) * g.line + row] = static_cast<uint8_t>(e);
   }
 }
 
-// Both forms: a workgroup packs 128 rows of a group by 128 columns; a thread
-// holds 8 columns of 8 consecutive rows.  Column sums of maxima go through LDS,
-// and so do the turned codes: 8-byte pieces (8 rows of a column), piece p of
+// Turned codes go through LDS: 8-byte pieces (8 rows of a column), piece p of
 // column c at place p ^ (c / 8 mod 16), so that the 16 lanes of a row's columns
 // write to different banks.
 struct TileShared {
   __attribute__((aligned(16))) uint8_t t[kBlk * kBlk];
-  float top[4][kBlk];
+  float top[8][kBlk], inv[kBlk];
 };
-__device__ __forceinline__ void turn_codes(TileShared& sh, const uint32_t (*q)[8], int l16,
-                                           int slot) {
-  // q[r]: 8 codes of row r as two words, [0]: columns 0-3, [1]: 4-7
+// v[r][j] * inv[j] of rows R slot .. and 8 columns as codes of columns: the
+// conversion takes two values, which are neighbours in the column, so that
+// nothing is left to transpose.
+template <int R>
+__device__ __forceinline__ void turn_codes(TileShared& sh, const float (*v)[8], const float* inv,
+                                           int l16, int slot) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    uint32_t lo = 0, hi = 0;
+    int w[R / 4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      lo |= ((q[j >> 2][r] >> (8 * (j & 3))) & 0xffu) << (8 * r);
-      hi |= ((q[j >> 2][r + 4] >> (8 * (j & 3))) & 0xffu) << (8 * r);
+    for (int h = 0; h < R / 4; ++h) {
+      const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h][j] * inv[j], v[4 * h + 1][j] * inv[j], 0, false);
+      w[h] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2][j] * inv[j], v[4 * h + 3][j] * inv[j], lo, true);
     }
-    const int col = l16 * 8 + j;
-    *reinterpret_cast<uint2*>(sh.t + col * kBlk + ((slot ^ l16) << 3)) = make_uint2(lo, hi);
+    uint8_t* const at = sh.t + (l16 * 8 + j) * kBlk + (((R * slot / 8) ^ l16) << 3) + R * slot % 8;
+    if constexpr (R == 8) *reinterpret_cast<uint2*>(at) = make_uint2(static_cast<uint32_t>(w[0]), static_cast<uint32_t>(w[1]));
+    else *reinterpret_cast<uint32_t*>(at) = static_cast<uint32_t>(w[0]);
   }
+}
+// Infinities to NaN, as codes have them.
+template <int R> __device__ __forceinline__ void finite_or_nan(float (*v)[8]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(fabsf(v[r][i]) < INFINITY)) v[r][i] = __builtin_nanf("");
+}
+// The largest of lanes l, l ^ 16, l ^ 32, l ^ 48 (as bits of values >= 0): the
+// swaps trade rows of 16, then halves, between two copies.
+__device__ __forceinline__ uint32_t max_rows(uint32_t m) {
+  const auto a = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+  m = max(static_cast<uint32_t>(a[0]), static_cast<uint32_t>(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+  return max(static_cast<uint32_t>(b[0]), static_cast<uint32_t>(b[1]));
 }
 // 16 codes of a column, rows 16 h .. + 15.
 __device__ __forceinline__ uint4 turned16(const TileShared& sh, int col, int h) {
@@ -150,75 +199,95 @@ __device__ __forceinline__ uint4 turned16(const TileShared& sh, int col, int h) 
   return make_uint4(a.x, a.y, b.x, b.y);
 }
 
-template <typename T, int ACT, bool BACK>
-__global__ __launch_bounds__(256) void pack_both_kernel(PackArgs g) {
-  __shared__ TileShared sh;
+// Both forms: a workgroup packs 128 rows of a group by 128 columns (H = 2: and
+// the up columns); a thread holds 8 columns of 4 consecutive rows.
+template <typename T, int ACT, bool BACK, int H>
+__global__ __launch_bounds__(512, 4) void pack_both_kernel(PackArgs g) {
+  __shared__ TileShared sh[H];
   const int tid = threadIdx.x, l16 = tid & 15, slot = tid >> 4;
-  const int blocks = (g.cols + kBlk - 1) / kBlk;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int blocks = H == 2 ? g.cols / (2 * kBlk) : (g.cols + kBlk - 1) / kBlk;
   const int tb = blockIdx.x / blocks, cb = blockIdx.x % blocks;
   const RowBlock rb = find_block(g.offsets, g.groups, g.rows, tb);
   if (rb.end <= rb.begin) return;
-  const int c = cb * kBlk + l16 * 8;
+  const int c = cb * kBlk + l16 * 8, half = g.cols / 2;
   const bool cin = c < g.cols;
-  float v[8][8];
-  bool bad = false;
+  const int row0 = rb.begin + slot * 4;
+  float v[H][4][8] = {};
+  uint32_t top[H][8] = {};  // of the columns, as bits
+  if (rb.begin + wave * 16 < rb.end) {  // the wavefront has rows
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    const int row = rb.begin + slot * 8 + r;
+    for (int r = 0; r < 4; ++r)
+      if (cin && row0 + r < rb.end) values<T, ACT, BACK, H, 4>(g, row0 + r, c, v, r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[r][i] = 0.f;
-    if (cin && row < rb.end) values8<T, ACT, BACK>(g, row, c, v[r]);
-  }
-  float col[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int h = 0; h < H; ++h) {
+      bool bad = false;
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    const int row = rb.begin + slot * 8 + r;
-    const float m = finite_max8(v[r], bad);
+      for (int r = 0; r < 4; ++r) {
+        const int row = row0 + r;
+        const float m = finite_max8(v[h][r], bad);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = fabsf(v[r][i]);
-      col[i] = fmaxf(col[i], a < INFINITY ? a : 0.f);
+        for (int i = 0; i < 8; ++i) top[h][i] = max(top[h][i], __float_as_uint(v[h][r][i]) & 0x7fffffffu);
+        if (g.codes != nullptr) {
+          const int e = e8m0_of(max16(m));
+          if (cin && row < rb.end)
+            *reinterpret_cast<uint2*>(g.codes + static_cast<size_t>(row) * g.cols + h * half + c) =
+                encode8_finite(v[h][r], e8m0_inverse(e), bad);
+          if (l16 == 0 && row < rb.end)
+            g.scale[(cb + h * blocks) * g.line + row] = static_cast<uint8_t>(e);
+        }
+      }
+      if (__builtin_expect(bad, 0)) {
+        finite_or_nan<4>(v[h]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float m = 0.f;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(v[h][r][i]));  // NaN does not count
+          top[h][i] = __float_as_uint(m);
+        }
+      }
     }
-    if (g.codes != nullptr) {
-      const int e = e8m0_of(max16(m));
-      if (cin && row < rb.end)
-        *reinterpret_cast<uint2*>(g.codes + static_cast<size_t>(row) * g.cols + c) =
-            encode8_finite(v[r], e8m0_inverse(e), bad);
-      if (l16 == 0 && row < rb.end) g.scale[cb * g.line + row] = static_cast<uint8_t>(e);
-    }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    col[i] = fmaxf(col[i], __shfl_xor(col[i], 16, 64));
-    col[i] = fmaxf(col[i], __shfl_xor(col[i], 32, 64));
-    if ((tid & 63) < 16) sh.top[tid >> 6][l16 * 8 + i] = col[i];
+  for (int h = 0; h < H; ++h) {
+    float col[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) col[i] = __uint_as_float(max_rows(top[h][i]));
+    if ((tid & 63) < 16) {
+      *reinterpret_cast<float4*>(&sh[h].top[wave][l16 * 8]) = make_float4(col[0], col[1], col[2], col[3]);
+      *reinterpret_cast<float4*>(&sh[h].top[wave][l16 * 8 + 4]) = make_float4(col[4], col[5], col[6], col[7]);
+    }
   }
   __syncthreads();
-  float inv[8];
+  if (tid < H * kBlk) {
+    const int h = tid / kBlk, k = tid % kBlk;
+    float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int k = l16 * 8 + i;
-    const int e = e8m0_of(fmaxf(fmaxf(sh.top[0][k], sh.top[1][k]), fmaxf(sh.top[2][k], sh.top[3][k])));
-    inv[i] = e8m0_inverse(e);
-    if (slot == 0 && cin) g.scale_t[static_cast<size_t>(tb) * g.cols + c + i] = static_cast<uint8_t>(e);
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, sh[h].top[w][k]);
+    const int e = e8m0_of(m);
+    sh[h].inv[k] = e8m0_inverse(e);
+    if (cb * kBlk + k < g.cols)
+      g.scale_t[static_cast<size_t>(tb) * g.cols + h * half + cb * kBlk + k] = static_cast<uint8_t>(e);
   }
-  uint32_t q[2][8];
-#pragma unroll
-  for (int r = 0; r < 8; ++r) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[r][i] *= inv[i];
-    const uint2 u = encode8_finite(v[r], 1.0f, bad);
-    q[0][r] = u.x;
-    q[1][r] = u.y;
-  }
-  turn_codes(sh, q, l16, slot);
   __syncthreads();
-  uint8_t* const out = g.codes_t + (static_cast<size_t>(tb) * g.cols + cb * kBlk) * kBlk;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int p = k * 256 + tid;  // 16-byte pieces of the tile, column after column
-    if (cb * kBlk + (p >> 3) < g.cols)
-      *reinterpret_cast<uint4*>(out + static_cast<size_t>(p) * 16) = turned16(sh, p >> 3, p & 7);
+  for (int h = 0; h < H; ++h) {
+    float inv[8];
+    load8<float>(&sh[h].inv[l16 * 8], inv);
+    turn_codes<4>(sh[h], v[h], inv, l16, slot);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    uint8_t* const out =
+        g.codes_t + (static_cast<size_t>(tb) * g.cols + h * half + cb * kBlk) * kBlk;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int p = k * 512 + tid;  // 16-byte pieces of the tile, column after column
+      if (cb * kBlk + (p >> 3) < g.cols)
+        *reinterpret_cast<uint4*>(out + static_cast<size_t>(p) * 16) = turned16(sh[h], p >> 3, p & 7);
+    }
   }
 }
 
@@ -259,18 +328,21 @@ __global__ __launch_bounds__(256) void pack_weights_kernel(PackWeightArgs g) {
     if (g.codes_t != nullptr)
       g.scale_t[(static_cast<size_t>(e) * ib + cb) * ob + rbk] = static_cast<uint8_t>(s);
   }
-  uint32_t q[2][8];
+  if (g.codes != nullptr && cin) {
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    const int row = rbk * kBlk + slot * 8 + r;
-    const uint2 u = encode8_finite(v[r], inv, bad);
-    q[0][r] = u.x;
-    q[1][r] = u.y;
-    if (g.codes != nullptr && cin && row < g.out)
-      *reinterpret_cast<uint2*>(g.codes + mat + static_cast<size_t>(row) * g.in + c) = u;
+    for (int r = 0; r < 8; ++r) {
+      const int row = rbk * kBlk + slot * 8 + r;
+      if (row < g.out)
+        *reinterpret_cast<uint2*>(g.codes + mat + static_cast<size_t>(row) * g.in + c) =
+            encode8_finite(v[r], inv, bad);
+    }
   }
   if (g.codes_t == nullptr) return;
-  turn_codes(sh, q, l16, slot);
+  if (__builtin_expect(bad, 0)) finite_or_nan<8>(v);
+  float all[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) all[i] = inv;
+  turn_codes<8>(sh, v, all, l16, slot);
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -281,21 +353,26 @@ __global__ __launch_bounds__(256) void pack_weights_kernel(PackWeightArgs g) {
   }
 }
 
-template <typename T, int ACT, bool BACK>
-hipError_t pack_t(const PackArgs& g, hipStream_t s) {
-  const int blocks = (g.cols + kBlk - 1) / kBlk;
+template <typename T, int ACT, bool BACK, int H>
+hipError_t pack_h(const PackArgs& g, hipStream_t s) {
+  const int blocks = (g.cols / H + kBlk - 1) / kBlk;
   if (g.codes_t != nullptr) {
     const long n = (g.rows / kBlk + static_cast<long>(g.groups)) * blocks;
-    hipLaunchKernelGGL((pack_both_kernel<T, ACT, BACK>), dim3(static_cast<unsigned>(n)), dim3(256),
+    hipLaunchKernelGGL((pack_both_kernel<T, ACT, BACK, H>), dim3(static_cast<unsigned>(n)), dim3(512),
                        0, s, g);
     return hipGetLastError();
   }
-  const int rows_wg = (g.rows + kRowsWg - 1) / kRowsWg;
-  const int per = 1;
-  hipLaunchKernelGGL((pack_rows_kernel<T, ACT, BACK>),
-                     dim3(static_cast<unsigned>(rows_wg), (blocks + per - 1) / per), dim3(256), 0,
-                     s, g, per);
+  hipLaunchKernelGGL((pack_rows_kernel<T, ACT, BACK, H>),
+                     dim3(static_cast<unsigned>((g.rows + kRowsWg - 1) / kRowsWg), blocks), dim3(256), 0,
+                     s, g);
   return hipGetLastError();
+}
+template <typename T, int ACT, bool BACK>
+hipError_t pack_t(const PackArgs& g, hipStream_t s) {
+  if constexpr (ACT == kActSwiglu && BACK) {
+    if (g.cols % (2 * kBlk) == 0) return pack_h<T, ACT, BACK, 2>(g, s);
+  }
+  return pack_h<T, ACT, BACK, 1>(g, s);
 }
 template <typename T>
 hipError_t pack_act(const PackArgs& g, hipStream_t s) {
