@@ -34,15 +34,23 @@ constexpr int kFwd = 0, kDw = 1;
 // What a stage reads past the end of a row (the last 64 of a block of 128).
 __device__ __align__(16) const uint32_t zero_chunk[4] = {0u, 0u, 0u, 0u};
 
-template <int BT> struct Ring { static constexpr int kDepth = BT == 128 ? 2 : 3; };
+// Stages of the ring.  The fp32 weight gradient of 128 x 128 tiles has one:
+// without a second buffer, and with 168 registers, three workgroups share a
+// compute unit, and while one waits or stores the others multiply (16384 rows
+// of 64 groups, dw 7168 x 2048: 1093 us with two stages, 1074 with one; stores
+// past the caches 832; tiles dealt to the XCDs in chunks 824, 4.6 TB/s of
+// results).
+template <int BT, int MODE, bool WIDE> struct Ring {
+  static constexpr int kDepth = BT == 64 ? 3 : MODE == kDw && WIDE ? 1 : 2;
+};
 
 template <int BT, int MODE, bool GATED, bool WF32, bool WIDE>
-__global__ __launch_bounds__(256) void block_tile_kernel(BlockArgs g) {
+__global__ __launch_bounds__(256, (Ring<BT, MODE, WIDE>::kDepth == 1 ? 3 : 1)) void block_tile_kernel(BlockArgs g) {
   static_assert(MODE == kFwd || (!GATED && !WF32), "weight gradient: plain");
   constexpr int WT = BT / 2, NBK = WT / 16;       // a wavefront's rows (columns), 16-row blocks
   constexpr int NBO = GATED ? NBK / 2 : NBK;      // result columns of a lane
   constexpr int COLS = GATED ? BT / 2 : BT;
-  constexpr int D = Ring<BT>::kDepth, kStage = 2 * BT * kLineBytes;
+  constexpr int D = Ring<BT, MODE, WIDE>::kDepth, kStage = 2 * BT * kLineBytes;
   constexpr int LD = BT / 32;                     // a wavefront's loads of an operand's stage
   __shared__ __attribute__((aligned(1024))) char smem[D * kStage];
 
@@ -61,16 +69,23 @@ __global__ __launch_bounds__(256) void block_tile_kernel(BlockArgs g) {
     valid = min(BT, __builtin_amdgcn_readfirstlane(at.end) - seg - m0);
     nst = (g.in_dim + kBlk - 1) / kBlk;
   } else {
+    // Tiles of a group in bands of 4 row tiles, column by column, dealt to the
+    // XCDs in chunks of 16 (see block_mfma.hip).
+    constexpr int BAND = BT == 64 ? 1 : 4, CHUNK = BT == 64 ? 1 : 16;
     const int mt = (g.z_dim + BT - 1) / BT;
-    const int per = mt * nt;
-    e = blockIdx.x / per;
-    const int q = blockIdx.x - e * per;
-    m0 = q % mt * BT;
-    n0 = q / mt * COLS;
+    const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
+    const long per = static_cast<long>(mt) * nt;
+    const long w = (static_cast<long>(idx / CHUNK) * 8 + xcd) * CHUNK + idx % CHUNK;
+    if (w >= per * g.groups) return;
+    e = static_cast<int>(w / per);
+    const int q = static_cast<int>(w - e * per);
+    const int band = q / (BAND * nt), h = min(BAND, mt - band * BAND), r = q - band * BAND * nt;
+    m0 = (band * BAND + r % h) * BT;
+    n0 = r / h * COLS;
     valid = min(BT, g.z_dim - m0);
-    const int2 r = group_range(g.offsets, e, g.rows);
-    seg = __builtin_amdgcn_readfirstlane(turned_first(r.x, e));
-    nst = __builtin_amdgcn_readfirstlane((r.y - r.x + kBlk - 1) / kBlk);
+    const int2 range = group_range(g.offsets, e, g.rows);
+    seg = __builtin_amdgcn_readfirstlane(turned_first(range.x, e));
+    nst = __builtin_amdgcn_readfirstlane((range.y - range.x + kBlk - 1) / kBlk);
   }
   const int part = blockIdx.y;
   const int s0 = static_cast<int>(static_cast<long>(nst) * part / g.parts);
@@ -218,11 +233,19 @@ __global__ __launch_bounds__(256) void block_tile_kernel(BlockArgs g) {
     for (int p = 0; p < D - 1; ++p) issue(s0 + p);
   }
   for (int p = s0; p < s1; ++p) {
-    wait_vmem<(D - 2) * 2 * LD>();
-    stage_barrier();
-    load_scales(min(p + 1, s1 - 1), next);
-    asm volatile("" ::: "memory");
-    issue(p + D - 1);
+    if constexpr (D == 1) {
+      if (p > s0) lds_barrier();
+      issue(p);
+      load_scales(min(p + 1, s1 - 1), next);
+      wait_vmem<0>();
+      stage_barrier();
+    } else {
+      wait_vmem<(D > 2 ? D - 2 : 0) * 2 * LD>();
+      stage_barrier();
+      load_scales(min(p + 1, s1 - 1), next);
+      asm volatile("" ::: "memory");
+      issue(p + D - 1);
+    }
     const char* const buf = smem + (p - s0) % D * kStage;
     i32x8 a[NBK], b[NBK];
     auto frag = [&](const char* at) {
@@ -343,7 +366,10 @@ __global__ __launch_bounds__(256) void block_tile_kernel(BlockArgs g) {
         else if constexpr (NBO == 2) *reinterpret_cast<uint32_t*>(o) = w[0];
         else *o = static_cast<bf16_t>(w[0]);
       } else {
-        put(static_cast<float*>(g.y) + at, v);
+        float* const o = static_cast<float*>(g.y) + at;
+        if constexpr (MODE == kDw && NBO == 4)
+          __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(o));
+        else put(o, v);
       }
     }
 }
@@ -472,7 +498,8 @@ hipError_t launch_block_dw_tile(const BlockArgs& g, int cus, hipStream_t s) {
     return static_cast<long>(g.groups) * ((g.z_dim + bt - 1) / bt) * ((g.in_dim + bt - 1) / bt);
   };
   auto go = [&](auto kernel, int bt) {
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tiles(bt)), g.parts), dim3(256), 0, s, g);
+    const long chunk = bt == 64 ? 1 : 16, grid = ((tiles(bt) + chunk - 1) / chunk + 7) / 8 * 8 * chunk;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid), g.parts), dim3(256), 0, s, g);
   };
   if (tiles(128) < cus) {
     if (g.wide) go(block_tile_kernel<64, kDw, false, false, true>, 64);
