@@ -131,6 +131,25 @@ def test_from_nothing():
             assert float(t["m_scale"][1]) == 0 and not t["m"][256:512].any()
 
 
+def test_values_near_the_ends_of_the_range():
+    """Gradients and states from 1e-25 to 1e18 in neighbouring blocks, zeros among
+    them, beside ordinary ones: the short forms and the long ones."""
+    for grad in ("f32", "bf16"):
+        t = tensor(256 * 40, "f32", grad, False, True, 5)
+        size = 10.0 ** torch.linspace(-25, 18, 40, device=DEV).repeat_interleave(256)
+        t["grad"] = (t["grad"].float() * 1e3 * size).to(DT[grad])
+        t["grad"][::7] = 0
+        for n in ("m_scale", "v_scale"):
+            t[n] *= size[::256] * 1e3
+            t[n][::5] = 0
+        t["param"] *= 1e3
+        step_and_check([t], label="ends of the range")
+    t = tensor(2048 * 8, "bf16", "bf16", False, True, 6)
+    t["grad"][::2] = 0
+    t["v_scale"][::2] = 0
+    step_and_check([t], label="no root")
+
+
 def test_scale_zero_leaves_everything():
     t = tensor(3000, "bf16", "bf16", True, True, 1)
     t["grad"][5] = float("nan")
