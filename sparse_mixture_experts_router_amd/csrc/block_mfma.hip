@@ -97,11 +97,14 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
     int col;
     if (!find_item(g.offsets, g.groups, g.rows, kT, nt, at, col)) return;
     e = __builtin_amdgcn_readfirstlane(at.e);
-    m0 = __builtin_amdgcn_readfirstlane(at.m) * kT;
     n0 = __builtin_amdgcn_readfirstlane(col) * COLS;
     seg = __builtin_amdgcn_readfirstlane(at.begin);
     count = __builtin_amdgcn_readfirstlane(at.end) - seg;
-    valid = min(kT, count - m0);
+    // A group's rows in tiles of equal height, in steps of 64: a tile of few
+    // rows takes its share of W's bytes, not of its products.
+    const int high = (count + 64 * at.tiles - 1) / (64 * at.tiles) * 64;
+    m0 = __builtin_amdgcn_readfirstlane(at.m * high);
+    valid = min(__builtin_amdgcn_readfirstlane(high), count - m0);
     nst = (g.in_dim + kBlk - 1) / kBlk;
   }
 
