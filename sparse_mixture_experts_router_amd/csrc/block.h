@@ -132,6 +132,15 @@ __device__ __forceinline__ float finite_max8(const float* v, bool& bad) {
   }
   return __uint_as_float(top);
 }
+// The largest of a row of 16 lanes (values >= 0), in all of them.
+template <int N> __device__ __forceinline__ float max_turned(float m) {  // and that of N lanes on
+  const int o = __builtin_amdgcn_mov_dpp(static_cast<int>(__float_as_uint(m)), 0x120 + N, 0xf, 0xf, true);
+  return fmaxf(m, __uint_as_float(static_cast<uint32_t>(o)));
+}
+__device__ __forceinline__ float max16(float m) {
+  return max_turned<1>(max_turned<2>(max_turned<4>(max_turned<8>(m))));
+}
+
 // 8 codes of v * inv; what is not finite becomes NaN.
 __device__ __forceinline__ uint2 encode8_finite(const float* v, float inv, bool bad) {
   if (__builtin_expect(bad, 0)) {

@@ -511,10 +511,7 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
           for (int k = 0; k < 4; ++k) v[4 * h + k] = value(i, r, h, k);
         bool bad = false;
         float m = finite_max8(v, bad);
-        m = fmaxf(m, __shfl_xor(m, 1, 64));
-        m = fmaxf(m, __shfl_xor(m, 2, 64));
-        m = fmaxf(m, __shfl_xor(m, 4, 64));
-        top[i][r] = fmaxf(m, __shfl_xor(m, 8, 64));
+        top[i][r] = max16(m);
         if (GATED && l16 == 0) tops[grp * kT + tile_row(i, r)] = top[i][r];
       }
     if constexpr (GATED) {

@@ -87,15 +87,6 @@ __device__ __forceinline__ void values8(const PackArgs& g, int row, int c, float
   }
 }
 
-// The largest of the 16 lanes that hold a row's block (values >= 0).
-template <int N> __device__ __forceinline__ float max_turned(float m) {  // and that of N lanes on
-  const int o = __builtin_amdgcn_mov_dpp(static_cast<int>(__float_as_uint(m)), 0x120 + N, 0xf, 0xf, true);
-  return fmaxf(m, __uint_as_float(static_cast<uint32_t>(o)));
-}
-__device__ __forceinline__ float max16(float m) {
-  return max_turned<1>(max_turned<2>(max_turned<4>(max_turned<8>(m))));
-}
-
 // The gradient of SwiGLU reads the same z and dy for the gate's columns and the
 // up projection's, so one thread makes both (H = 2, where each has whole blocks
 // of columns).  Values of gate column c and of its up column, or of column c.

@@ -307,10 +307,7 @@ __global__ __launch_bounds__(512, D == 2 ? 4 : 2) void block_rows_kernel(BlockAr
           const float x = fabsf(acc[i][j][r]);
           if (busy && x < INFINITY) m = fmaxf(m, x);
         }
-        m = fmaxf(m, __shfl_xor(m, 1, 64));
-        m = fmaxf(m, __shfl_xor(m, 2, 64));
-        m = fmaxf(m, __shfl_xor(m, 4, 64));
-        m = fmaxf(m, __shfl_xor(m, 8, 64));
+        m = max16(m);
         if (c16 == 0) tops[wave * BM + 16 * i + r4 + r] = m;
       }
     lds_barrier();
@@ -396,10 +393,7 @@ __global__ __launch_bounds__(256) void block_rows_join_kernel(BlockArgs g, int b
   if (g.y_codes == nullptr) return;
   bool bad = false;
   float m = finite_max8(v, bad);
-  m = fmaxf(m, __shfl_xor(m, 1, 64));
-  m = fmaxf(m, __shfl_xor(m, 2, 64));
-  m = fmaxf(m, __shfl_xor(m, 4, 64));
-  m = fmaxf(m, __shfl_xor(m, 8, 64));
+  m = max16(m);
   const int s = e8m0_of(m);
   if (in)
     *reinterpret_cast<uint2*>(g.y_codes + static_cast<size_t>(row) * g.out_dim + n) =

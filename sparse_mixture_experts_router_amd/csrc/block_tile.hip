@@ -413,10 +413,7 @@ __global__ __launch_bounds__(256) void block_join_kernel(BlockArgs g) {
   if (g.y_codes == nullptr) return;
   bool bad = false;
   float m = finite_max8(v, bad);
-  m = fmaxf(m, __shfl_xor(m, 1, 64));
-  m = fmaxf(m, __shfl_xor(m, 2, 64));
-  m = fmaxf(m, __shfl_xor(m, 4, 64));
-  m = fmaxf(m, __shfl_xor(m, 8, 64));
+  m = max16(m);
   const int s = e8m0_of(m);
   if (in)
     *reinterpret_cast<uint2*>(g.y_codes + static_cast<size_t>(row) * g.out_dim + c) =
