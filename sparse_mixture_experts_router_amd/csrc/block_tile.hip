@@ -39,10 +39,17 @@ __device__ __align__(16) const uint32_t zero_chunk[4] = {0u, 0u, 0u, 0u};
 // compute unit, and while one waits or stores the others multiply (16384 rows
 // of 64 groups, dw 7168 x 2048: 1093 us with two stages, 1074 with one; stores
 // past the caches 832; tiles dealt to the XCDs in chunks 824, 4.6 TB/s of
-// results).
+// results; 991 where the operands come from HBM).
 template <int BT, int MODE, bool WIDE> struct Ring {
   static constexpr int kDepth = BT == 64 ? 3 : MODE == kDw && WIDE ? 1 : 2;
 };
+
+// Tiles of the weight gradient that one XCD takes in a row: 16 x 8 where that
+// leaves every XCD several times as many (operands from HBM: 16384 rows of 64
+// groups, fp32 dw 7168 x 2048 991 us, 4 x 4 tiles 1030), else 4 x 4.
+__host__ __device__ inline int dw_chunk(int bt, long tiles) {
+  return bt == 64 ? 1 : tiles >= 8 * 128 * 8 ? 128 : 16;
+}
 
 template <int BT, int MODE, bool GATED, bool WF32, bool WIDE>
 __global__ __launch_bounds__(256, (Ring<BT, MODE, WIDE>::kDepth == 1 ? 3 : 1)) void block_tile_kernel(BlockArgs g) {
@@ -69,18 +76,18 @@ __global__ __launch_bounds__(256, (Ring<BT, MODE, WIDE>::kDepth == 1 ? 3 : 1)) v
     valid = min(BT, __builtin_amdgcn_readfirstlane(at.end) - seg - m0);
     nst = (g.in_dim + kBlk - 1) / kBlk;
   } else {
-    // Tiles of a group in bands of 4 row tiles, column by column, dealt to the
-    // XCDs in chunks of 16 (see block_mfma.hip).
-    constexpr int BAND = BT == 64 ? 1 : 4, CHUNK = BT == 64 ? 1 : 16;
+    // Tiles of a group in bands of row tiles, column by column, dealt to the
+    // XCDs in chunks (see block_mfma.hip).
     const int mt = (g.z_dim + BT - 1) / BT;
     const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
     const long per = static_cast<long>(mt) * nt;
-    const long w = (static_cast<long>(idx / CHUNK) * 8 + xcd) * CHUNK + idx % CHUNK;
+    const int chunk = dw_chunk(BT, per * g.groups), rows = chunk >= 128 ? 16 : chunk >= 16 ? 4 : 1;
+    const long w = (static_cast<long>(idx / chunk) * 8 + xcd) * chunk + idx % chunk;
     if (w >= per * g.groups) return;
     e = static_cast<int>(w / per);
     const int q = static_cast<int>(w - e * per);
-    const int band = q / (BAND * nt), h = min(BAND, mt - band * BAND), r = q - band * BAND * nt;
-    m0 = (band * BAND + r % h) * BT;
+    const int band = q / (rows * nt), h = min(rows, mt - band * rows), r = q - band * rows * nt;
+    m0 = (band * rows + r % h) * BT;
     n0 = r / h * COLS;
     valid = min(BT, g.z_dim - m0);
     const int2 range = group_range(g.offsets, e, g.rows);
@@ -495,7 +502,7 @@ hipError_t launch_block_dw_tile(const BlockArgs& g, int cus, hipStream_t s) {
     return static_cast<long>(g.groups) * ((g.z_dim + bt - 1) / bt) * ((g.in_dim + bt - 1) / bt);
   };
   auto go = [&](auto kernel, int bt) {
-    const long chunk = bt == 64 ? 1 : 16, grid = ((tiles(bt) + chunk - 1) / chunk + 7) / 8 * 8 * chunk;
+    const long chunk = dw_chunk(bt, tiles(bt)), grid = ((tiles(bt) + chunk - 1) / chunk + 7) / 8 * 8 * chunk;
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid), g.parts), dim3(256), 0, s, g);
   };
   if (tiles(128) < cus) {
