@@ -55,12 +55,13 @@ struct BlockArgs {
   void* y;                 // [rows, out] or null; weight gradient: dw [groups, z, in]
   uint8_t* y_codes;        // [rows, out] or null
   uint8_t* y_scale;        // [ceil(out / 128), line]
-  float* partial;          // [parts, rows, z] (weight gradient [parts, groups, z, in]) or null
+  float* partial;          // [parts, rows, z] (weight gradient [parts, groups, z, in]; few rows:
+                           // two places a workgroup), or null
   size_t line;
   int rows, groups, in_dim, out_dim, z_dim, act, parts;
   int dtype;               // of y
-  size_t place;            // block_rows.hip
-  bool split, deep;
+  size_t place;            // block_rows.hip: floats of a place in partial
+  bool split, deep;        // block_rows.hip: shares end inside tiles; a ring of 3 or 4 stages
   bool wide;               // fp32 results: products on the bf16 instruction
 };
 

@@ -16,7 +16,7 @@
 // anyway, and the sums are of exact products (block_tile.hip says what the 8-bit
 // instruction drops).
 //
-// 64 rows of 8 groups: 4096 -> 2 x 14336 in 158 us and 14336 -> 4096 in 78 us,
+// 64 rows of 8 groups: 4096 -> 2 x 14336 in 160 us and 14336 -> 4096 in 77 us,
 // 6 TB/s of W (tiles of 128 x 128: 233 and 130); 128 rows of 256 groups 7168 ->
 // 2 x 2048 in 450 us, 6.6 TB/s (583).
 #include "block.h"
@@ -441,13 +441,14 @@ bool block_rows_plan(BlockArgs& g, int cus) {
   g.deep = items <= cus;
   const long slots = std::max(8, cus * (g.deep ? 1 : 2) / 8 * 8);
   // Shares that end inside tiles cost a second launch of about 5 us and a pass
-  // over the sums: worth it where whole tiles would leave a workgroup idle for
-  // more than 8 stages (2 rows of 8 groups 2048 -> 4096 15.8 -> 12.1 us, 1024
-  // -> 4096 10.2 -> 11.2), or where the groups that have rows are too few to
-  // tell (128 rows of 256 groups 7168 -> 2 x 2048 585 -> 452).
+  // over the sums: worth it where whole tiles would leave a workgroup idle for 4
+  // stages of 16 or more (2 rows of 8 groups, W from HBM: 4096 -> 2 x 14336 53 ->
+  // 48 us, 14336 -> 4096 92 -> 28; W in the caches: 2048 -> 4096 15.8 -> 12.1,
+  // 1024 -> 4096 10.2 -> 11.2), or where the groups that have rows are too few
+  // to tell (128 rows of 256 groups 7168 -> 2 x 2048 585 -> 452).
   const long idle = (slots - 1 - (items + slots - 1) % slots) * nst / slots;
   const bool unknown = g.rows < 4L * g.groups && items > slots && nst >= 32;
-  g.split = idle > 8 || unknown;
+  g.split = (idle >= 4 && nst >= 16) || unknown;
   const long want = ((g.split ? items * nst / 4 : items) + 7) / 8 * 8;
   g.parts = static_cast<int>(std::max(8L, std::min(slots, want)));
   g.place = static_cast<size_t>(std::min(g.rows, mb * 16)) * kCols;
