@@ -639,7 +639,8 @@ typedef struct {
  * in k, what lies under 2^-13 of the largest: about 1.4e-5 of the result's norm.
  * With y in fp32, and in packed results of at most 32 rows a group on average
  * (rows <= 32 min(groups, rows)), codes are widened to bf16 instead and each
- * product is exact (operands whose value is under 2^-126 may count as 0).
+ * product is exact; other results of so few rows may be, too.  There operands
+ * whose value is under 2^-126 may count as 0.
  * Either or both are given.  Rows of no group are left as they were.
  * offsets as in moe_linear_args.  A NaN code gives NaN; the E8M0 byte 255 is
  * not a scale.  x, w, y and y_codes 16-byte aligned.  No output may overlap an

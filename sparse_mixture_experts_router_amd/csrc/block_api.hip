@@ -107,33 +107,32 @@ BlockArgs block_args(const moe_block_linear_config& c) {
 // 40.0 and 58.4, 2048 rows 44.3 and 33.3, 8192 rows of 64 groups 2048 -> 1024
 // 32.6 and 40.2.  Weight gradient of 8192 rows of 8 groups: 2048 x 2048 38.5 and
 // 52.0, 1024 x 512 15.1 and 10.8.
-bool large_tiles(long row_tiles, int cols) {
-  return row_tiles * ((cols + 255) / 256) > device_cus() / 4;
+bool large_tiles(long row_tiles, int cols, int cus) {
+  return row_tiles * ((cols + 255) / 256) > cus / 4;
 }
-bool forward_large(const BlockArgs& g) {
+bool forward_large(const BlockArgs& g, long cus) {
   const long tiles = g.rows / 256 + std::min(g.groups, g.rows), nt = (g.z_dim + 255) / 256;
-  const long cus = device_cus();
-  return !g.wide && large_tiles(tiles, g.z_dim) && (g.rows * nt / 256 > cus / 4 || tiles * nt > cus);
+  return !g.wide && large_tiles(tiles, g.z_dim, cus) && (g.rows * nt / 256 > cus / 4 || tiles * nt > cus);
 }
 bool few_rows(const BlockArgs& g) { return g.rows <= 32L * std::min(g.groups, g.rows); }
 // Few rows a group: W streamed past them.  Tiles of 128 x 128 take little W
 // without packed results (64 rows of 16 groups 2048 -> 4096 22 us, streamed 24)
 // and more rows (512 rows of 8 groups 4096 -> 2 x 14336 223 us, streamed 317;
 // 256 rows 248 and 195).
-bool forward_rows(BlockArgs& g, bool packed) {
+bool forward_rows(BlockArgs& g, bool packed, int cus) {
   if (!few_rows(g)) return false;
   const long bytes = static_cast<long>(std::min(g.groups, g.rows)) * g.z_dim * g.in_dim;
   if (g.in_dim <= 4096 && bytes <= (packed ? 16L << 20 : 128L << 20) && !(packed && g.in_dim <= 1024)) return false;
-  return block_rows_plan(g, device_cus());
+  return block_rows_plan(g, cus);
 }
-size_t forward_space(BlockArgs g, bool packed) {
-  if (forward_rows(g, packed)) return g.split ? align_up(8 * g.place * g.parts) : kAlign;
-  if (forward_large(g)) return kAlign;
-  const size_t parts = block_tile_parts(g, device_cus());
+size_t forward_space(BlockArgs g, bool packed, int cus) {
+  if (forward_rows(g, packed, cus)) return g.split ? align_up(8 * g.place * g.parts) : kAlign;
+  if (forward_large(g, cus)) return kAlign;
+  const size_t parts = block_tile_parts(g, cus);
   return std::max(kAlign, align_up(parts * g.rows * g.z_dim * 4));
 }
-bool grad_large(const BlockArgs& g) {
-  return !g.wide && large_tiles(static_cast<long>(g.groups) * ((g.z_dim + 255) / 256), g.in_dim);
+bool grad_large(const BlockArgs& g, int cus) {
+  return !g.wide && large_tiles(static_cast<long>(g.groups) * ((g.z_dim + 255) / 256), g.in_dim, cus);
 }
 
 moe_status check_space(const void* ws, size_t have, size_t need) {
@@ -204,7 +203,8 @@ size_t moe_block_linear_workspace_size(const moe_block_linear_config* cfg) {
   if (check_linear(cfg, false) != MOE_OK) return 0;
   BlockArgs g = block_args(*cfg);
   g.wide = cfg->dtype == MOE_F32;
-  return std::max(forward_space(g, false), forward_space(g, true));
+  const int cus = device_cus();
+  return std::max(forward_space(g, false, cus), forward_space(g, true, cus));
 }
 
 moe_status moe_block_linear(const moe_block_linear_config* cfg, const moe_block_linear_args* a,
@@ -240,12 +240,12 @@ moe_status moe_block_linear(const moe_block_linear_config* cfg, const moe_block_
   const bool wf32 = cfg->w_scale_format == MOE_SCALE_F32;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int cus = device_cus();
-  if (forward_rows(g, g.y_codes != nullptr)) {
+  if (forward_rows(g, g.y_codes != nullptr, cus)) {
     if (g.split) g.partial = static_cast<float*>(workspace);
     const hipError_t err = launch_block_rows(wf32, g, s);
     return err == hipSuccess ? MOE_OK : hip_fail(err, "block product kernel");
   }
-  if (forward_large(g)) {
+  if (forward_large(g, cus)) {
     const hipError_t err = launch_block_mfma(wf32, g, s);
     return err == hipSuccess ? MOE_OK : hip_fail(err, "block product kernel");
   }
@@ -262,8 +262,9 @@ size_t moe_block_weight_grad_workspace_size(const moe_block_linear_config* cfg) 
   if (check_linear(cfg, true) != MOE_OK) return 0;
   BlockArgs g = block_args(*cfg);
   g.wide = cfg->dtype == MOE_F32;
-  if (grad_large(g)) return kAlign;
-  const size_t parts = block_dw_parts(g, device_cus());
+  const int cus = device_cus();
+  if (grad_large(g, cus)) return kAlign;
+  const size_t parts = block_dw_parts(g, cus);
   return parts > 1 ? align_up(parts * g.groups * g.z_dim * g.in_dim * 4) : kAlign;
 }
 
@@ -295,7 +296,7 @@ moe_status moe_block_weight_grad(const moe_block_linear_config* cfg,
   g.wide = cfg->dtype == MOE_F32;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int cus = device_cus();
-  if (grad_large(g)) {
+  if (grad_large(g, cus)) {
     const hipError_t err = launch_block_dw_mfma(g, s);
     return err == hipSuccess ? MOE_OK : hip_fail(err, "weight gradient kernel");
   }

@@ -476,7 +476,16 @@ hipError_t launch_fwd_bt(bool wf32, const BlockArgs& g, hipStream_t s) {
 int block_tile_parts(const BlockArgs& g, int cus) {
   const long tiles = row_tiles(g, 64) * ((g.z_dim + 63) / 64);
   const int nst = (g.in_dim + kBlk - 1) / kBlk;
-  if (!small_tiles(g, cus) || tiles >= cus) return 1;
+  if (!small_tiles(g, cus)) {
+    // Two workgroups fit a compute unit: with no more tiles than units, as far
+    // as the host can tell, K is halved or more (512 rows of 8 groups 14336 ->
+    // 4096 136 -> 108 us, 4096 -> 4096 40.8 -> 33.1).
+    const long present = std::min(g.groups, g.rows);
+    const long est = std::max(present, (g.rows + 32 * present) / 128) * ((g.z_dim + 127) / 128);
+    if (est > cus || nst < 32) return 1;
+    return static_cast<int>(std::min<long>({2 * cus / est, nst / 16, 16}));
+  }
+  if (tiles >= cus) return 1;
   return static_cast<int>(std::max<long>(1, std::min<long>({cus / tiles, nst / 4, 16})));
 }
 
