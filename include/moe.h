@@ -560,7 +560,7 @@ typedef enum {
 
 /* cols a multiple of 64 up to 2^21 (128 with the gradient of SwiGLU), rows
  * < 2^27, x_rows < 2^30, groups <= 512, and
- *   (rows / 128 + groups) (blocks of cols) <= 2^23     (rows / 128 rounded down).
+ *   (rows / 128 + groups) (blocks of cols) < 2^23      (rows / 128 rounded down).
  * Other sizes are MOE_ERR_UNSUPPORTED. */
 typedef struct {
   int32_t rows;       /* packed rows                                           */

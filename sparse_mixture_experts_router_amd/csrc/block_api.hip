@@ -31,9 +31,9 @@ moe_status check_pack(const moe_block_pack_config* c, const moe_block_pack_args*
   if (c->cols > (1 << 21)) return fail(MOE_ERR_UNSUPPORTED, "cols > 2^21");
   if (c->rows >= (1 << 27) || c->x_rows >= (1 << 30))
     return fail(MOE_ERR_UNSUPPORTED, "too many rows");
-  // workgroups of 256 threads, fewer than 2^24 of them: 128 rows by 128 columns
-  // each, or 16 rows of one block column or more
-  if ((c->rows / kBlk + c->groups) * blocks_of(c->cols) > (1L << 23))
+  // a launch has fewer than 2^32 threads: workgroups of 512 for 128 rows by 128
+  // columns each (16 rows by 128 columns are 256 threads, on a grid of their own)
+  if ((c->rows / kBlk + c->groups) * blocks_of(c->cols) >= (1L << 23))
     return fail(MOE_ERR_UNSUPPORTED, "too many blocks");
   if (a->dy != nullptr) {
     if (c->activation == MOE_ACT_NONE)

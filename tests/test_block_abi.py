@@ -88,6 +88,14 @@ def test_pack_arguments(args, over, status):
     assert pack(args, **over) == status
 
 
+def test_pack_most_blocks():
+    """Both sides of the limit: the larger size is refused before x is looked at."""
+    at = dict(groups=512, cols=1 << 21)  # 2^23 blocks
+    assert pack(dict(x=None), **at) == UNSUPPORTED
+    assert pack(dict(x=None), **dict(at, groups=511)) == INVALID
+    assert b"x is NULL" in moe.lib().moe_last_error()
+
+
 def test_pack_null():
     assert moe.lib().moe_block_pack(None, None, None) == INVALID
 
