@@ -23,6 +23,13 @@
 // in by one fma an element, which needs the accumulators in VGPRs.  To leave
 // room for all this, half of the second operand's fragments are read while the
 // first half is multiplied.
+//
+// 32768 rows of 8 groups 8192 -> 4096 in 861 us, 2.55 PFLOP/s (matrix cores 51 %
+// busy at 2.0 GHz; a library product of one scale reaches 2.75), 512 -> 4096 in
+// 103 us, where a tile's start and its results, 5 us, are the most of it; dw
+// 28672 x 4096 of 8192 rows of 8 groups 1016 us (128 x 128 tiles: 1370).
+// Weights with fp32 scales and with E8M0 ones: 65536 rows of 8 groups 7168 -> 2 x
+// 2048 1768 and 1539 us, of 256 groups 2440 and 2290.
 #include "block.h"
 #include "lds_ring.h"
 
@@ -358,7 +365,9 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
         if constexpr (LIVE > 0) {
           if constexpr (WF32) {
             // Each MFMA is followed by the fmas of the second one before it,
-            // whose sums are there by then; the order is pinned.
+            // whose sums are there by then; the order is pinned (65536 rows of
+            // 256 groups: 2894 us with the fmas after each block of columns,
+            // 2564 so).
             constexpr int LAG = LIVE > 1 ? 2 : 1, ALL = kNB * LIVE;
             f32x4 d[LAG + 1];
             const f32x4 z = {0.f, 0.f, 0.f, 0.f};

@@ -21,6 +21,10 @@
 // rows of the second operand are ordered so that a lane of the result holds NB
 // neighbouring columns: results are stored without a pass through LDS, and the
 // scales of a lane's columns in the weight gradient are one load.
+//
+// Bound by one tile's chain of stages (0.4-0.8 us each) where tiles are few, and
+// by L2 -> LDS bytes: 512 rows of 8 groups 14336 -> 4096 in 107 us (4.4 TB/s of
+// W), 4096 rows of one group 4096 -> 4096 in 76 (the large tiles: 54).
 #include "block.h"
 #include "lds_ring.h"
 
