@@ -86,8 +86,7 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
     constexpr int BAND = 4, CHUNK = 16;
     const int mt = (g.z_dim + kT - 1) / kT;
     const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
-    const long per = static_cast<long>(mt) * nt;
-    const long w = (static_cast<long>(idx / CHUNK) * 8 + xcd) * CHUNK + idx % CHUNK;
+    const uint32_t per = mt * nt, w = (idx / CHUNK * 8 + xcd) * CHUNK + idx % CHUNK;
     if (w >= per * g.groups) return;
     e = static_cast<int>(w / per);
     const int q = static_cast<int>(w - e * per);

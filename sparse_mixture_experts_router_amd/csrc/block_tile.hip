@@ -84,9 +84,9 @@ __global__ __launch_bounds__(256, (Ring<BT, MODE, WIDE>::kDepth == 1 ? 3 : 1)) v
     // XCDs in chunks (see block_mfma.hip).
     const int mt = (g.z_dim + BT - 1) / BT;
     const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
-    const long per = static_cast<long>(mt) * nt;
-    const int chunk = dw_chunk(BT, per * g.groups), rows = chunk >= 128 ? 16 : chunk >= 16 ? 4 : 1;
-    const long w = (static_cast<long>(idx / chunk) * 8 + xcd) * chunk + idx % chunk;
+    const uint32_t per = mt * nt;
+    const int chunk = dw_chunk(BT, static_cast<long>(per) * g.groups), rows = chunk >= 128 ? 16 : chunk >= 16 ? 4 : 1;
+    const uint32_t w = (idx / chunk * 8 + xcd) * chunk + idx % chunk;
     if (w >= per * g.groups) return;
     e = static_cast<int>(w / per);
     const int q = static_cast<int>(w - e * per);
@@ -99,8 +99,7 @@ __global__ __launch_bounds__(256, (Ring<BT, MODE, WIDE>::kDepth == 1 ? 3 : 1)) v
     nst = __builtin_amdgcn_readfirstlane((range.y - range.x + kBlk - 1) / kBlk);
   }
   const int part = blockIdx.y;
-  const int s0 = static_cast<int>(static_cast<long>(nst) * part / g.parts);
-  const int s1 = static_cast<int>(static_cast<long>(nst) * (part + 1) / g.parts);
+  const int s0 = nst * part / g.parts, s1 = nst * (part + 1) / g.parts;  // parts <= 16
 
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);

@@ -174,9 +174,9 @@ __device__ __forceinline__ TileAt find_tile(const TileScan& t, const int32_t* of
 // Work item w (group, row tile, column tile) of the list of all of them: inside
 // a group the tiles go in bands of 8 row tiles, column by column.
 __device__ __forceinline__ void item_at(const TileScan& t, const int32_t* offsets, int groups,
-                                        int rows, int bm, int nt, long w, TileAt& at, int& col) {
+                                        int rows, int bm, int nt, uint32_t w, TileAt& at, int& col) {
   at = find_tile(t, offsets, groups, rows, bm, static_cast<int>(w / nt));
-  const int q = static_cast<int>(w - static_cast<long>(at.before) * nt);
+  const int q = static_cast<int>(w - static_cast<uint32_t>(at.before) * nt);
   const int band = q / (8 * nt), tw = min(8, at.tiles - band * 8), r = q - band * 8 * nt;
   col = r / tw;
   at.m = band * 8 + r % tw;
@@ -188,9 +188,11 @@ __device__ __forceinline__ void item_at(const TileScan& t, const int32_t* offset
 __device__ __forceinline__ bool find_item(const int32_t* offsets, int groups, int rows, int bm,
                                           int nt, TileAt& at, int& col) {
   const TileScan t = scan_tiles(offsets, groups, rows, bm);
-  const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
-  const long items = static_cast<long>(t.total) * nt;
-  const long lo = items * xcd / 8, hi = items * (xcd + 1) / 8;
+  const uint32_t xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
+  // the calls' limits keep 8 items under 2^32 (of offsets that overlap, more
+  // wrap, into the list); divisions in 64 bits cost a small call 0.15 us of 5.3
+  const uint32_t items = static_cast<uint32_t>(t.total) * nt;
+  const uint32_t lo = items * xcd / 8, hi = items * (xcd + 1) / 8;
   if (lo + idx >= hi) return false;
   item_at(t, offsets, groups, rows, bm, nt, lo + idx, at, col);
   return true;
