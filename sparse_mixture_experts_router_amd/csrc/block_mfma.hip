@@ -125,8 +125,8 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
 
   // --------------------------------------------------- this lane's sources
   // Load j of wavefront q stages 8 rows of LDS, 64 q + 8 j ..: lane l the chunk
-  // of row l / 8 that the swizzle puts at its place.  Staged row 16 k + l of a
-  // chunk of 64 columns is column 4 l + k.  The source is off0 + j-th step,
+  // of row l / 8 that the swizzle puts at its place.  Staged row 16 k + l of
+  // 128 columns is column 8 l + k (SwiGLU: of 64, 4 l + k).  The source is off0 + j-th step,
   // clamped to the last row there is: what rows and columns past the end give
   // is not written.
   const int chunk = line_lane_chunk(lane, 0) * 16, l8 = lane >> 3;
@@ -153,13 +153,14 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
       }
       last = valid - 1;
     } else {
-      s8 = 32 * row_bytes;
+      s8 = (GATED ? 32 : 64) * row_bytes;
       s16 = row_bytes;
+      const int spread = 128 * (q >> 1) + 4 * (q & 1) + 8 * l8;
       if constexpr (MODE == kDw) {
         base = reinterpret_cast<const char*>(g.x) +
                (static_cast<size_t>(seg) * g.in_dim + n0) * kBlk;
         step = static_cast<size_t>(g.in_dim) * kBlk;
-        first = 64 * q + 4 * l8;
+        first = spread;
         last = n_dim - 1 - n0;
       } else {
         // SwiGLU: staged rows 0 .. 127 are gate rows, 128 .. 255 the up rows of
@@ -168,7 +169,7 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
         base = reinterpret_cast<const char*>(g.w) +
                (static_cast<size_t>(e) * g.z_dim + n0 + (up ? g.out_dim : 0)) * row_bytes;
         step = kLineBytes;
-        first = 64 * q - (up ? COLS : 0) + 4 * l8;
+        first = GATED ? 64 * q - (up ? COLS : 0) + 4 * l8 : spread;
         last = n_dim - 1 - n0;
       }
     }
@@ -229,7 +230,7 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
     astep = g.z_dim;
     ao[0] = min(q * 64, valid - 64) + 4 * l16;
     bs[0] = g.x_scale + static_cast<size_t>(seg) * g.in_dim + n0;
-    bo = 4 * l16;
+    bo = min(grp * 128 + 8 * l16, n_dim - n0 - 8);
   }
   // As loaded: widened where they are loaded, they would be waited for there.
   struct Raw {
@@ -237,8 +238,6 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
     uint32_t a, b[2];
     float f[2];
   } raw{};
-  const int bc0 = MODE == kDw ? min(grp * 128, n_dim - n0 - 64) : 0;
-  const int bc1 = MODE == kDw ? min(grp * 128 + 64, n_dim - n0 - 64) : 0;
   auto load_scales = [&](int p) {
     const int pc = min(p, nst - 1);
     const uint8_t* const a = as + pc * astep;
@@ -253,8 +252,8 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
     } else {
       raw.a = *reinterpret_cast<const uint32_t*>(a + ao[0]);
       const uint8_t* const b = bs[0] + static_cast<size_t>(pc) * g.in_dim;
-      raw.b[0] = *reinterpret_cast<const uint32_t*>(b + bc0 + bo);
-      raw.b[1] = *reinterpret_cast<const uint32_t*>(b + bc1 + bo);
+      raw.b[0] = *reinterpret_cast<const uint32_t*>(b + bo);
+      raw.b[1] = *reinterpret_cast<const uint32_t*>(b + bo + 4);
     }
     asm volatile("" ::: "memory");
   };
@@ -440,8 +439,8 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
   }
 
   // -------------------------------------------------------------- epilogue
-  // A lane holds 4 neighbouring columns of two chunks of 64 (SwiGLU: gate and
-  // up of one), 16 rows; 16 lanes make a whole line of bf16.
+  // A lane holds 8 neighbouring columns (SwiGLU: 4, gate and up) of 16 rows: 16
+  // lanes make whole lines.
   mfma_drain();
 #pragma unroll
   for (int i = 0; i < kMB; ++i)
@@ -449,37 +448,25 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
     for (int j = 0; j < kNB; ++j) {
       if constexpr (WF32) asm volatile("" : "+v"(acc[i][j]));
     }
-  constexpr int CH = GATED ? 1 : 2;
-  const int c = wcol + 4 * l16;
+  constexpr int NC = GATED ? 4 : 8;  // result columns of a lane
+  const int c = wcol + NC * l16;
   float* const tops = reinterpret_cast<float*>(smem);  // [2][256], SwiGLU packed
   auto tile_row = [&](int i, int r) {
     if (MODE == kDw) return q * 64 + 16 * (lane >> 4) + 4 * r + i;
     return i * 64 + q * 16 + 4 * (lane >> 4) + r;
   };
-  auto values = [&](int i, int r, float (*v)[4]) {
-#pragma unroll
-    for (int h = 0; h < CH; ++h)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float z = acc[i][4 * h + k][r];
-        v[h][k] = GATED ? z * sigmoid_close(z) * acc[i][4 + k][r] : z;
-        if (c + 64 * h >= n_dim) v[h][k] = 0.f;
-      }
-  };
   if constexpr (GATED) {  // once: the passes below read the result
 #pragma unroll
     for (int i = 0; i < kMB; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float v[CH][4];
-        values(i, r, v);
+      for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][k][r] = v[0][k];
-      }
+        for (int k = 0; k < 4; ++k) {
+          const float z = acc[i][k][r];
+          acc[i][k][r] = c < n_dim ? z * sigmoid_close(z) * acc[i][4 + k][r] : 0.f;
+        }
   }
-  auto value = [&](int i, int r, int h, int k) {
-    return GATED ? acc[i][k][r] : (c + 64 * h >= n_dim ? 0.f : acc[i][4 * h + k][r]);
-  };
+  auto value = [&](int i, int r, int k) { return GATED || c < n_dim ? acc[i][k][r] : 0.f; };
   if (MODE == kDw || g.y != nullptr) {
 #pragma unroll
     for (int i = 0; i < kMB; ++i)
@@ -489,18 +476,14 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
         const size_t at = MODE == kDw
             ? (static_cast<size_t>(e) * g.z_dim + m0 + row) * g.in_dim + c
             : static_cast<size_t>(seg + m0 + row) * g.out_dim + c;
+        if (row >= valid || c >= n_dim) continue;
+        typedef __attribute__((ext_vector_type(NC / 2))) uint32_t Words;
+        Words w;
 #pragma unroll
-        for (int h = 0; h < CH; ++h) {
-          if (row >= valid || c + 64 * h >= n_dim) continue;
-          uint32_t w[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            w[k] = static_cast<uint32_t>(f32_to_bf16(value(i, r, h, 2 * k))) |
-                   (static_cast<uint32_t>(f32_to_bf16(value(i, r, h, 2 * k + 1))) << 16);
-          typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
-          __builtin_nontemporal_store(u32x2{w[0], w[1]},
-                                      reinterpret_cast<u32x2*>(static_cast<bf16_t*>(g.y) + at + 64 * h));
-        }
+        for (int k = 0; k < NC / 2; ++k)
+          w[k] = static_cast<uint32_t>(f32_to_bf16(value(i, r, 2 * k))) |
+                 (static_cast<uint32_t>(f32_to_bf16(value(i, r, 2 * k + 1))) << 16);
+        __builtin_nontemporal_store(w, reinterpret_cast<Words*>(static_cast<bf16_t*>(g.y) + at));
       }
   }
   if constexpr (MODE == kFwd) {
@@ -514,9 +497,7 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
       for (int r = 0; r < 4; ++r) {
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int h = 0; h < CH; ++h)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[4 * h + k] = value(i, r, h, k);
+        for (int k = 0; k < NC; ++k) v[k] = value(i, r, k);
         bool bad = false;
         float m = finite_max8(v, bad);
         top[i][r] = max16(m);
@@ -539,17 +520,17 @@ __global__ __launch_bounds__(512, 1) void block_mfma_kernel(BlockArgs g) {
         const float inv = e8m0_inverse(s);
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int h = 0; h < CH; ++h)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x = value(i, r, h, k);
-            v[4 * h + k] = fabsf(x) < INFINITY ? x : __builtin_nanf("");
-          }
+        for (int k = 0; k < NC; ++k) {
+          const float x = value(i, r, k);
+          v[k] = fabsf(x) < INFINITY ? x : __builtin_nanf("");
+        }
         const uint2 q8 = encode8(v, inv);
         if (row >= valid) continue;
         uint8_t* const o = g.y_codes + static_cast<size_t>(seg + m0 + row) * g.out_dim + c;
-        if (c < n_dim) *reinterpret_cast<uint32_t*>(o) = q8.x;
-        if (!GATED && c + 64 < n_dim) *reinterpret_cast<uint32_t*>(o + 64) = q8.y;
+        if (c < n_dim) {
+          if constexpr (GATED) *reinterpret_cast<uint32_t*>(o) = q8.x;
+          else *reinterpret_cast<uint2*>(o) = q8;
+        }
         if (l16 == 0 && (!GATED || grp == 0) && wcol < n_dim)
           g.y_scale[static_cast<size_t>(wcol / kBlk) * g.line + seg + m0 + row] = static_cast<uint8_t>(s);
       }
