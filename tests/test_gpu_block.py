@@ -437,6 +437,36 @@ def test_linear_few_rows_nan_codes_and_repeats():
     torch.cuda.synchronize()
 
 
+def test_linear_few_rows_captured_and_replayed():
+    """A captured call whose shares end inside tiles, and one of split 128 x 128
+    tiles, on one workspace: replayed with other inputs and group sizes between
+    eager calls of the same."""
+    for sizes, K, F in (([9, 5, 0, 2], 4672, 192), ([130, 128, 60], 4160, 4096)):
+        c = Product(sizes, K, F, seed=9)
+        y = torch.zeros((c.rows, F), dtype=torch.bfloat16, device=DEV)
+        yc, ys = u8(c.rows, F), u8(*moe.block_scale_shape(c.rows, F))
+        ws = moe.alloc_block_linear_workspace(c.cfg).fill_(0xFF)
+        call = lambda y=y, yc=yc, ys=ys: moe.moe_block_linear(  # noqa: E731
+            c.cfg, c.x, c.xs, c.offsets, c.w, c.ws, y=y, y_codes=yc, y_scale=ys, workspace=ws)
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        g = torch.Generator(device=DEV)
+        g.manual_seed(1)
+        for k in range(3):
+            c.x.copy_(random_codes(g, c.rows, K))
+            off = c.off.copy()
+            off[1:-1] = np.maximum(off[1:-1] - k, 0)  # every row stays in a group
+            c.offsets.copy_(torch.from_numpy(off))
+            graph.replay()
+            torch.cuda.synchronize()
+            eager = c.run(codes=True)
+            assert torch.equal(y, eager[0]) and torch.equal(yc, eager[1])
+            assert torch.equal(ys[:, :c.rows], eager[2][:, :c.rows])
+
+
 def test_linear_nan_codes_and_repeats():
     c = Product([40, 90], 256, 192, seed=5)
     first = c.run(codes=True)
